@@ -126,8 +126,8 @@ def work(c):
         m, k, n, e = c["rows"], c["k"], c["n"], c["experts"]
         if not c["train"]:
             return dict(bytes=2 * m * k + n * k + 2 * m * n, flops=2 * m * n * k)
-        # x, w and the output's gradient in; y, dx (bf16) and dw (fp32) out
-        return dict(bytes=2 * m * k + 2 * e * k * n + 2 * m * n + 2 * m * n + 2 * m * k + 4 * e * k * n,
+        # x, w and the output's gradient in; y, dx and dw out
+        return dict(bytes=4 * m * k + 4 * e * k * n + 4 * m * n,
                     flops=3 * 2 * m * n * k)
     s = _size(c["dtype"])
     return dict(bytes=2 * s * c["elements"], flops=3 * c["elements"])
@@ -351,7 +351,8 @@ def _linear(s):
     y = torch.cat([_by_runs(xs) @ ws for xs, ws, ds in parts])
     dx = torch.cat([_by_runs(ds) @ ws.t() for xs, ws, ds in parts])
     dw = torch.stack([_by_runs(xs.t()) @ _by_runs(ds.t()).t() for xs, ws, ds in parts])
-    return dict(y=y.to(torch.bfloat16), dx=dx.to(torch.bfloat16), dw=dw if w.dim() == 3 else dw[0])
+    y, dx, dw = (v.to(torch.bfloat16) for v in (y, dx, dw))
+    return dict(y=y, dx=dx, dw=dw if w.dim() == 3 else dw[0])
 
 
 def _served(s):
@@ -417,7 +418,7 @@ def _own(s):
         wt, wd = av.averis_fp8_quant_weight(s["w"])
         return dict(y=av.averis_fp8_gemm(xq, wt, torch.bfloat16, offsets=offs),
                     dx=av.averis_fp8_gemm(dq, wd, torch.bfloat16, offsets=offs),
-                    dw=av.averis_fp8_gemm_wgrad(xt, dt, torch.float32, offsets=offs))
+                    dw=av.averis_fp8_gemm_wgrad(xt, dt, torch.bfloat16, offsets=offs))
     if c["op"] == "fp8":
         xq = av.averis_fp8_quant(s["x"])
         wt = av.FP8(s["codes"], s["scales"], c["n"], c["k"])
