@@ -83,7 +83,9 @@ typedef enum {
   AVERIS_OP_QUANT = 1,        /* rows, cols, nseg (batch for batched quant)   */
   AVERIS_OP_GEMM = 2,         /* rows = M, cols = K, n = N, nseg              */
   AVERIS_OP_WGRAD = 3,        /* rows = m, cols = l (tokens), n               */
-  AVERIS_OP_QUANT_PAIR_MULTI = 4  /* n = number of weights (rows, cols unused) */
+  AVERIS_OP_QUANT_PAIR_MULTI = 4, /* n = number of weights (rows, cols unused) */
+  AVERIS_OP_MOE_SORT = 5,     /* rows = tokens * topk slots, n = experts (cols unused) */
+  AVERIS_OP_GRAD_NORM = 6     /* n = number of tensors (rows, cols unused)    */
 } averis_op_t;
 
 /* An NVFP4-style tensor of rows x cols logical elements, 16-blocks along
@@ -454,6 +456,106 @@ averis_status_t averis_split_quant_noalloc(const void* a, averis_dtype_t dtype, 
                                            averis_round_t rnd, const averis_nvfp4_t* residual,
                                            const averis_nvfp4_t* mean, float* mean_f32,
                                            hipStream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Mixture-of-experts routing and token exchange: from router logits to    */
+/* the rows sorted by expert that every grouped call takes, and back, with */
+/* the gradients.  A slot is one of a token's topk choices: slot t * topk  */
+/* + j; tokens * topk < 2^31.  Matrices are F32 or BF16, any row stride    */
+/* and element alignment; sums are fp32, rounded once on output.           */
+/* ---------------------------------------------------------------------- */
+
+#define AVERIS_MAX_EXPERTS 1024
+#define AVERIS_MAX_TOPK 32
+
+/* expert_ids[t][j], weights[t][j] (tokens x topk): the topk largest of token
+ * t's logits in descending order and their softmax weights.  Ties go to the
+ * lowest expert; a NaN logit counts as the largest (and makes the weights
+ * NaN).  A logit of -inf is masked: never chosen, and a slot for which no
+ * open expert is left gets id -1 and weight 0 (every slot of a token whose
+ * logits are all -inf).  renorm = 1: softmax over the chosen logits; 0: over
+ * all of them.  logits: tokens x experts, row stride ld >= experts;
+ * 1 <= topk <= min(experts, AVERIS_MAX_TOPK). */
+averis_status_t averis_moe_route(const void* logits, averis_dtype_t dtype, int64_t tokens,
+                                 int experts, int64_t ld, int topk, int renorm,
+                                 int32_t* expert_ids, float* weights, hipStream_t stream);
+
+/* dlogits (tokens x experts, the logits' type, row stride ldd >= experts)
+ * from dweights (tokens x topk): the gradient of averis_moe_route's weights
+ * with the choice held fixed.  expert_ids as that call wrote them (for the
+ * same logits, topk and renorm); a slot with id -1 contributes nothing.
+ * dlogits may be logits. */
+averis_status_t averis_moe_route_grad(const void* logits, averis_dtype_t dtype, int64_t tokens,
+                                      int experts, int64_t ld, int topk, int renorm,
+                                      const int32_t* expert_ids, const float* dweights,
+                                      void* dlogits, int64_t ldd, hipStream_t stream);
+
+/* The order of the slots by expert, stable (within an expert by slot):
+ *   seg_offsets[experts + 1]: expert e owns rows seg_offsets[e] ..
+ *                seg_offsets[e + 1] - 1 (the array the grouped calls take);
+ *   pos[slot]:   the slot's row; for a dropped slot (id outside [0, experts))
+ *                ~row, a negative number, its row in the tail
+ *                seg_offsets[experts] .. tokens * topk - 1;
+ *   src[row]:    the row's slot (optional, may be NULL), tail included.
+ * Workspace: AVERIS_OP_MOE_SORT (0 bytes for short inputs). */
+averis_status_t averis_moe_sort(const int32_t* expert_ids, int64_t tokens, int topk, int experts,
+                                int64_t* seg_offsets, int32_t* pos, int32_t* src, void* ws,
+                                size_t ws_bytes, hipStream_t stream);
+
+/* rows[pos[t][j]] = x[t] for every slot; the tail rows are written as zeros.
+ * x: tokens x cols, rows: (tokens * topk) x cols, pos from averis_moe_sort.
+ * Its gradient, dx[t] = sum_j drows[pos[t][j]], is averis_moe_combine with
+ * weights = NULL. */
+averis_status_t averis_moe_dispatch(const void* x, averis_dtype_t dtype, int64_t tokens,
+                                    int64_t cols, int64_t ldx, const int32_t* pos, int topk,
+                                    void* rows, int64_t ldr, hipStream_t stream);
+
+/* y[t] = sum_j weights[t][j] rows[pos[t][j]] over the slots that were not
+ * dropped, in slot order (weights = NULL: all 1); a token without any gets
+ * zeros.  Dropped slots' rows and weights are not read. */
+averis_status_t averis_moe_combine(const void* rows, averis_dtype_t dtype, int64_t tokens,
+                                   int64_t cols, int64_t ldr, const int32_t* pos,
+                                   const float* weights, int topk, void* y, int64_t ldy,
+                                   hipStream_t stream);
+
+/* The gradients of averis_moe_combine: drows[pos[t][j]] = weights[t][j] dy[t]
+ * (tail rows zero) and dweights[t][j] = <dy[t], rows[pos[t][j]]> (0 for a
+ * dropped slot).  drows may be rows. */
+averis_status_t averis_moe_combine_grad(const void* dy, averis_dtype_t dtype, int64_t tokens,
+                                        int64_t cols, int64_t ldy, const void* rows, int64_t ldr,
+                                        const int32_t* pos, const float* weights, int topk,
+                                        void* drows, int64_t lddr, float* dweights,
+                                        hipStream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* The global gradient norm over many tensors, and clipping                */
+/* ---------------------------------------------------------------------- */
+
+/* One gradient: numel elements at grad (device, F32 or BF16, element
+ * aligned), clipped into out (the same type; grad itself for in place, or a
+ * buffer that overlaps no listed gradient). */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  averis_dtype_t dtype;
+} averis_grad_t;
+
+#define AVERIS_MAX_GRADS (1 << 20)
+
+/* norm (device float): sqrt of the sum of squares of every element of the n
+ * tensors (fp64 sums in a fixed order: the same bits on every call; 0 for
+ * none).  grads: host array, read during the call only; out is not used.
+ * Workspace: AVERIS_OP_GRAD_NORM with n. */
+averis_status_t averis_grad_norm(int n, const averis_grad_t* grads, float* norm, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
+
+/* averis_grad_norm, and out = grad * min(1, max_norm / (norm + eps)) for each
+ * tensor, rounded once.  A norm that is not finite is not hidden: an infinite
+ * one scales by 0 (which leaves NaN in place of infinite elements), NaN
+ * scales by NaN.  max_norm, eps >= 0. */
+averis_status_t averis_grad_clip(int n, const averis_grad_t* grads, double max_norm, double eps,
+                                 float* norm, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Utilities                                                               */

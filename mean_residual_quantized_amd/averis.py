@@ -22,8 +22,10 @@ STATUS_NAMES = {0: "OK", 1: "E_NULL", 2: "E_SHAPE", 3: "E_DTYPE", 4: "E_ALIGN",
 F32, BF16 = 0, 1
 RN, SR = 0, 1
 OP_SPLIT_QUANT, OP_QUANT, OP_GEMM, OP_WGRAD, OP_QUANT_PAIR_MULTI = 0, 1, 2, 3, 4
+OP_MOE_SORT, OP_GRAD_NORM = 5, 6
 MAX_WEIGHTS = 16
 MAX_RANK1 = 4
+MAX_EXPERTS, MAX_TOPK, MAX_GRADS = 1024, 32, 1 << 20
 STREAM_ACT, STREAM_MEAN, STREAM_WEIGHT, STREAM_RESIDUAL_T = 0, 1, 2, 3
 
 # every symbol include/averis.h declares
@@ -36,6 +38,8 @@ EXPORTS = [
     "averis_gemm_rank1",
     "averis_split_quant_grouped_rank1", "averis_gemm_grouped_rank1",
     "averis_split_quant_noalloc", "averis_gemm_rank1_stats", "averis_split_quant_from_stats",
+    "averis_moe_route", "averis_moe_route_grad", "averis_moe_sort", "averis_moe_dispatch",
+    "averis_moe_combine", "averis_moe_combine_grad", "averis_grad_norm", "averis_grad_clip",
     "averis_workspace_bytes", "averis_status_str",
     "averis_abi_version", "averis_last_error",
 ]
@@ -56,6 +60,11 @@ class _Weight(ctypes.Structure):
     _fields_ = [("a", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
                 ("lda", ctypes.c_int64), ("seed", ctypes.c_uint64),
                 ("out", ctypes.POINTER(_NVFP4)), ("out_t", ctypes.POINTER(_NVFP4))]
+
+
+class _Grad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -98,6 +107,14 @@ def lib():
             "averis_split_quant_noalloc": [P, I, I64, I64, I64, U64, I, T, T, P, P],
             "averis_gemm_rank1_stats": [T, P, T, P, I64, P, SZ, P],
             "averis_split_quant_from_stats": [P, I64, I64, I64, U64, I, T, T, P, T, P, P, SZ, P],
+            "averis_moe_route": [P, I, I64, I, I64, I, I, P, P, P],
+            "averis_moe_route_grad": [P, I, I64, I, I64, I, I, P, P, P, I64, P],
+            "averis_moe_sort": [P, I64, I, I, P, P, P, P, SZ, P],
+            "averis_moe_dispatch": [P, I, I64, I64, I64, P, I, P, I64, P],
+            "averis_moe_combine": [P, I, I64, I64, I64, P, P, I, P, I64, P],
+            "averis_moe_combine_grad": [P, I, I64, I64, I64, P, I64, P, P, I, P, I64, P, P],
+            "averis_grad_norm": [I, P, P, P, SZ, P],
+            "averis_grad_clip": [I, P, ctypes.c_double, ctypes.c_double, P, P, SZ, P],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -567,3 +584,185 @@ def averis_split_quant_from_stats(c, ws, seed=0, rnd=SR, b=None, rho=None):
         mu.data_ptr(), ctypes.byref(cb) if cb is not None else None,
         rho.data_ptr() if rho is not None else None, ws.data_ptr(), ws.numel(), _stream()))
     return (res, mean, mu) if b is None else (res, mean, mu, rho)
+
+
+# --------------------------------------------------------------------------
+# mixture-of-experts routing and token exchange
+# --------------------------------------------------------------------------
+
+def _like(t, ref, dtype, what, shape=None):
+    """t, checked to be a contiguous tensor of `dtype` (and shape) on ref's device."""
+    if t.dtype != dtype or not t.is_contiguous() or t.device != ref.device:
+        raise ValueError("%s: expected a contiguous %s tensor on %s" % (what, dtype, ref.device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    return t
+
+
+def _matrix(t, ref, what, shape=None):
+    """Row stride of t, checked to be a 2-D tensor of ref's type (and shape) with unit column
+    stride on ref's device."""
+    if t.dim() != 2 or t.dtype != ref.dtype or t.device != ref.device:
+        raise ValueError("%s: expected a 2-D %s tensor on %s" % (what, ref.dtype, ref.device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: expected unit column stride" % what)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def averis_moe_route(logits, topk, renorm=True):
+    """Top-k experts of each token and their softmax weights; returns
+    (expert_ids int32 [tokens, topk], weights float32 [tokens, topk]).  -inf
+    masks an expert; a slot without an open expert has id -1 and weight 0."""
+    ld = _matrix(logits, logits, "logits")
+    tokens, experts = logits.shape
+    ids = torch.empty((tokens, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
+    _check("averis_moe_route", lib().averis_moe_route(
+        logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, topk, int(bool(renorm)),
+        ids.data_ptr(), weights.data_ptr(), _stream()))
+    return ids, weights
+
+
+def averis_moe_route_grad(logits, ids, dweights, renorm=True, out=None):
+    """The logits' gradient (their type) from dweights, for the ids that
+    averis_moe_route returned for the same logits and renorm."""
+    ld = _matrix(logits, logits, "logits")
+    tokens, experts = logits.shape
+    _like(ids, logits, torch.int32, "ids")
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError("ids: expected shape (%d, topk)" % tokens)
+    topk = ids.shape[1]
+    _like(dweights, logits, torch.float32, "dweights", (tokens, topk))
+    out = out if out is not None else torch.empty((tokens, experts), dtype=logits.dtype,
+                                                  device=logits.device)
+    ldd = _matrix(out, logits, "out", (tokens, experts))
+    _check("averis_moe_route_grad", lib().averis_moe_route_grad(
+        logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, topk, int(bool(renorm)),
+        ids.data_ptr(), dweights.data_ptr(), out.data_ptr(), ldd, _stream()))
+    return out
+
+
+def averis_moe_sort(ids, experts, ws=None):
+    """The slots' stable order by expert; returns (offsets int64 [experts + 1],
+    pos int32 [tokens, topk], src int32 [tokens * topk]): offsets as the
+    grouped calls take them, pos[t, j] slot (t, j)'s row (~row if its id is
+    outside [0, experts): a tail row), src[row] the row's slot."""
+    _like(ids, ids, torch.int32, "ids")
+    if ids.dim() != 2:
+        raise ValueError("ids: expected shape (tokens, topk)")
+    tokens, topk = ids.shape
+    dev = ids.device
+    offsets = torch.empty((experts + 1,), dtype=torch.int64, device=dev)
+    pos = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    src = torch.empty((tokens * topk,), dtype=torch.int32, device=dev)
+    need = workspace_bytes(OP_MOE_SORT, tokens * topk, 0, experts)
+    if ws is None and need:
+        ws = _workspace(need, dev)
+    _check("averis_moe_sort", lib().averis_moe_sort(
+        ids.data_ptr(), tokens, topk, experts, offsets.data_ptr(), pos.data_ptr(), src.data_ptr(),
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream()))
+    return offsets, pos, src
+
+
+def _slots(pos, ref):
+    _like(pos, ref, torch.int32, "pos")
+    if pos.dim() != 2:
+        raise ValueError("pos: expected shape (tokens, topk)")
+    return pos.shape
+
+
+def averis_moe_dispatch(x, pos, out=None):
+    """Each token's row copied to its topk rows (tail rows zero); returns
+    rows [tokens * topk, cols].  Its gradient is averis_moe_combine(drows, pos)."""
+    tokens, topk = _slots(pos, x)
+    cols = x.shape[-1]
+    ldx = _matrix(x, x, "x", (tokens, cols))
+    out = out if out is not None else torch.empty((tokens * topk, cols), dtype=x.dtype,
+                                                  device=x.device)
+    ldr = _matrix(out, x, "out", (tokens * topk, cols))
+    _check("averis_moe_dispatch", lib().averis_moe_dispatch(
+        x.data_ptr(), _dtype_code(x), tokens, cols, ldx, pos.data_ptr(), topk, out.data_ptr(), ldr,
+        _stream()))
+    return out
+
+
+def averis_moe_combine(rows, pos, weights=None, out=None):
+    """y[t] = sum_j weights[t, j] rows[pos[t, j]] (weights None: all 1)."""
+    tokens, topk = _slots(pos, rows)
+    cols = rows.shape[-1]
+    ldr = _matrix(rows, rows, "rows", (tokens * topk, cols))
+    if weights is not None:
+        _like(weights, rows, torch.float32, "weights", (tokens, topk))
+    out = out if out is not None else torch.empty((tokens, cols), dtype=rows.dtype,
+                                                  device=rows.device)
+    ldy = _matrix(out, rows, "out", (tokens, cols))
+    _check("averis_moe_combine", lib().averis_moe_combine(
+        rows.data_ptr(), _dtype_code(rows), tokens, cols, ldr, pos.data_ptr(),
+        weights.data_ptr() if weights is not None else None, topk, out.data_ptr(), ldy, _stream()))
+    return out
+
+
+def averis_moe_combine_grad(dy, rows, pos, weights, out=None):
+    """The gradients of averis_moe_combine: returns (drows, dweights)."""
+    tokens, topk = _slots(pos, dy)
+    cols = dy.shape[-1]
+    ldy = _matrix(dy, dy, "dy", (tokens, cols))
+    ldr = _matrix(rows, dy, "rows", (tokens * topk, cols))
+    _like(weights, dy, torch.float32, "weights", (tokens, topk))
+    out = out if out is not None else torch.empty((tokens * topk, cols), dtype=dy.dtype,
+                                                  device=dy.device)
+    lddr = _matrix(out, dy, "out", (tokens * topk, cols))
+    dweights = torch.empty((tokens, topk), dtype=torch.float32, device=dy.device)
+    _check("averis_moe_combine_grad", lib().averis_moe_combine_grad(
+        dy.data_ptr(), _dtype_code(dy), tokens, cols, ldy, rows.data_ptr(), ldr, pos.data_ptr(),
+        weights.data_ptr(), topk, out.data_ptr(), lddr, dweights.data_ptr(), _stream()))
+    return out, dweights
+
+
+# --------------------------------------------------------------------------
+# the global gradient norm, and clipping
+# --------------------------------------------------------------------------
+
+def _grad_list(grads, out):
+    n = len(grads)
+    arr = (_Grad * n)()
+    for i, g in enumerate(grads):
+        o = g if out is None else out[i]
+        if not g.is_contiguous() or not o.is_contiguous():
+            raise ValueError("expected contiguous gradients and outputs")
+        if o is not g and (o.dtype != g.dtype or o.numel() != g.numel() or o.device != g.device):
+            raise ValueError("out[%d]: expected the gradient's type, size and device" % i)
+        if g.device != grads[0].device:
+            raise ValueError("expected gradients on one device")
+        arr[i] = _Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
+    return arr
+
+
+def averis_grad_norm(grads, ws=None):
+    """The 2-norm over every element of the tensors in the list (a float32
+    tensor of no dimensions, on their device)."""
+    arr = _grad_list(grads, None)
+    dev = grads[0].device if len(grads) else "cuda"
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = ws if ws is not None else _workspace(workspace_bytes(OP_GRAD_NORM, 0, 0, len(grads)), dev)
+    _check("averis_grad_norm", lib().averis_grad_norm(
+        len(grads), ctypes.cast(arr, ctypes.c_void_p), norm.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream()))
+    return norm
+
+
+def averis_grad_clip(grads, max_norm, eps=1e-6, out=None, ws=None):
+    """Each gradient times min(1, max_norm / (norm + eps)), in place or into
+    the tensors of the list out; returns the norm as averis_grad_norm does."""
+    if out is not None and len(out) != len(grads):
+        raise ValueError("out: expected %d tensors" % len(grads))
+    arr = _grad_list(grads, out)
+    dev = grads[0].device if len(grads) else "cuda"
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = ws if ws is not None else _workspace(workspace_bytes(OP_GRAD_NORM, 0, 0, len(grads)), dev)
+    _check("averis_grad_clip", lib().averis_grad_clip(
+        len(grads), ctypes.cast(arr, ctypes.c_void_p), max_norm, eps, norm.data_ptr(),
+        ws.data_ptr(), ws.numel(), _stream()))
+    return norm

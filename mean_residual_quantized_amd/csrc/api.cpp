@@ -9,6 +9,7 @@
 #include <cstdio>
 
 #include "../../include/averis.h"
+#include "api_common.hpp"
 #include "launch.hpp"
 #include "segments.hpp"
 
@@ -16,15 +17,9 @@ using namespace averis;
 
 namespace {
 
-constexpr int kMaxSeg = 4096;
 // the split stages the dequantized mean (2 bytes per column) in LDS to form
 // the rank-one row
 constexpr int64_t kRank1MaxK = 32768;
-
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-inline size_t elem_size(averis_dtype_t d) { return d == AVERIS_BF16 ? 2 : 4; }
-inline bool dtype_ok(averis_dtype_t d) { return d == AVERIS_F32 || d == AVERIS_BF16; }
 
 averis_status_t check_tensor(const averis_nvfp4_t* t, int64_t rows, int64_t cols) {
   if (!t || !t->tscale) return AVERIS_E_NULL;
@@ -46,13 +41,6 @@ averis_status_t check_input(const void* a, averis_dtype_t dtype, int64_t rows, i
 }
 
 thread_local char g_last_error[256] = "";
-
-inline averis_status_t hip_status(hipError_t e) {
-  if (e == hipSuccess) return AVERIS_OK;
-  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", hipGetErrorName(e),
-                hipGetErrorString(e));
-  return AVERIS_E_HIP;
-}
 
 // ---------------------------------------------------------------------------
 // The allocation-free split-quant keeps its workspace in this file-scope
@@ -85,6 +73,13 @@ hipError_t scratch_address(void** out) {
 }  // namespace
 
 namespace averis {
+
+averis_status_t hip_status(hipError_t e) {
+  if (e == hipSuccess) return AVERIS_OK;
+  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", hipGetErrorName(e),
+                hipGetErrorString(e));
+  return AVERIS_E_HIP;
+}
 
 size_t split_ws_bytes(int64_t rows, int64_t cols, int nseg) {
   const int ns = nseg > 0 ? nseg : 1;
@@ -134,6 +129,11 @@ extern "C" {
 size_t averis_workspace_bytes(averis_op_t op, int64_t rows, int64_t cols, int64_t n, int64_t nseg) {
   if (op == AVERIS_OP_QUANT_PAIR_MULTI)
     return (n >= 1 && n <= kMaxWeights) ? (size_t)n * kAmaxBlocks * sizeof(float) : 0;
+  if (op == AVERIS_OP_MOE_SORT)
+    return (rows >= 0 && rows <= INT32_MAX && n >= 1 && n <= kMaxExperts)
+               ? moe_sort_ws_bytes(rows, (int)n) : 0;
+  if (op == AVERIS_OP_GRAD_NORM)
+    return (n >= 0 && n <= kMaxGrads) ? grad_norm_ws_bytes((int)n) : 0;
   if (op == AVERIS_OP_WGRAD) {
     // cols = l may be 0 (no tokens)
     if (rows < 0 || cols < 0 || cols % 16 != 0 || n < 0) return 0;
@@ -153,6 +153,8 @@ size_t averis_workspace_bytes(averis_op_t op, int64_t rows, int64_t cols, int64_
       return gemm_ws_bytes(n, cols, (int)nseg);
     case AVERIS_OP_WGRAD:
     case AVERIS_OP_QUANT_PAIR_MULTI:
+    case AVERIS_OP_MOE_SORT:
+    case AVERIS_OP_GRAD_NORM:
       break;
   }
   return 0;

@@ -189,4 +189,45 @@ hipError_t launch_wgrad(const QOperand& xt, const QOperand& dt, const float* mu_
                         const float* mu_d, int64_t m, int64_t n, int64_t l, void* out, bool bf16,
                         int64_t ldo, void* ws, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Mixture-of-experts routing and token exchange (moe.hip)
+// ---------------------------------------------------------------------------
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopk = 32;
+
+hipError_t launch_moe_route(const void* logits, bool bf16, int64_t tokens, int experts, int64_t ld,
+                            int topk, bool renorm, int32_t* ids, float* weights, hipStream_t st);
+hipError_t launch_moe_route_grad(const void* logits, bool bf16, int64_t tokens, int experts,
+                                 int64_t ld, int topk, bool renorm, const int32_t* ids,
+                                 const float* dweights, void* dlogits, int64_t ldd,
+                                 hipStream_t st);
+// counts per expert and chunk of slots (0 when one workgroup sorts them all)
+size_t moe_sort_ws_bytes(int64_t slots, int experts);
+hipError_t launch_moe_sort(const int32_t* ids, int64_t slots, int experts, int64_t* offsets,
+                           int32_t* pos, int32_t* src, void* ws, hipStream_t st);
+hipError_t launch_moe_dispatch(const void* x, bool bf16, int64_t tokens, int64_t cols, int64_t ldx,
+                               const int32_t* pos, int topk, void* rows, int64_t ldr,
+                               hipStream_t st);
+hipError_t launch_moe_combine(const void* rows, bool bf16, int64_t tokens, int64_t cols,
+                              int64_t ldr, const int32_t* pos, const float* weights, int topk,
+                              void* y, int64_t ldy, hipStream_t st);
+hipError_t launch_moe_combine_grad(const void* dy, bool bf16, int64_t tokens, int64_t cols,
+                                   int64_t ldy, const void* rows, int64_t ldr, const int32_t* pos,
+                                   const float* weights, int topk, void* drows, int64_t lddr,
+                                   float* dweights, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Global gradient norm and clipping (clip.hip)
+// ---------------------------------------------------------------------------
+struct GradTensor {
+  const void* g;
+  void* out;
+  int64_t n;
+  bool bf16;
+};
+size_t grad_norm_ws_bytes(int n);
+// norm over the n tensors; scale: also out = g min(1, max_norm / (norm + eps))
+hipError_t launch_grad_clip(int n, const GradTensor* w, bool scale, double max_norm, double eps,
+                            float* norm, void* ws, hipStream_t st);
+
 }  // namespace averis

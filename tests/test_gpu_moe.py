@@ -1,0 +1,272 @@
+"""Routing and token exchange on the GPU against the float64 oracle.
+
+Tolerances.  A softmax weight in fp32: the exponent l - max is rounded once
+(relative 2^-24 of |l - max|, an absolute error of the exponent, so a relative
+error of its exponential), exp and the division add two ulp, and the sum's at
+most 16 + 6 additions 22 x 2^-24: with |l - max| <= 64 under 2^-17 relative.
+Sums of k products in fp32: k + 1 roundings of 2^-24 on the terms' magnitudes.
+bf16 outputs add half an ulp, at most 2^-8 relative."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import moe
+from tests.parity import BF16_REL
+from mean_residual_quantized_amd import averis as av
+
+pytestmark = pytest.mark.gpu
+
+REL_W = 2.0 ** -17
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    av.lib()
+
+
+def half_ulp(ref, dtype):
+    return np.abs(ref) * BF16_REL if dtype == BF16 else np.abs(ref) * 2.0 ** -24
+
+
+def strided(a, pad, lead=0):
+    """a in a buffer whose rows are `pad` elements longer, `lead` elements in."""
+    buf = torch.full((a.shape[0] * (a.shape[1] + pad) + lead,), 7.0, dtype=a.dtype, device="cuda")
+    v = buf[lead:].as_strided(a.shape, (a.shape[1] + pad, 1), lead)
+    v.copy_(a)
+    return v
+
+
+def logits_of(rng, t, e, dtype, masked):
+    l = rng.standard_normal((t, e)).astype(np.float32) * 3.0
+    if masked:
+        l[rng.random((t, e)) < 0.4] = -np.inf
+        l[rng.random(t) < 0.2] = -np.inf
+        if t > 2:
+            l[2, : e - 1] = -np.inf               # a single open expert
+    l[0] = np.round(l[0])                          # ties
+    return torch.from_numpy(l).to(dtype)
+
+
+CASES = [(1, 1, 1), (1, 8, 8), (3, 7, 2), (65, 20, 4), (257, 33, 5), (100, 64, 8), (33, 100, 6),
+         (9, 129, 8), (7, 300, 10), (5, 513, 3), (4, 1024, 32), (2, 40, 32), (31, 64, 1)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("t,e,k", CASES)
+def test_route_and_gradient(t, e, k, masked, dtype):
+    rng = np.random.default_rng([t, e, k, masked])
+    l = logits_of(rng, t, e, dtype, masked)
+    ln = l.double().numpy()
+    lg = strided(l, 3, 1)                          # odd row stride and start
+    for renorm in (True, False):
+        ids, w = av.averis_moe_route(lg, k, renorm=renorm)
+        rid, rw = moe.route(ln, k, renorm)
+        np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+        assert np.all(np.abs(w.cpu().numpy() - rw) <= REL_W * rw + 1e-45)
+        dw = torch.from_numpy(rng.standard_normal((t, k)).astype(np.float32))
+        d = av.averis_moe_route_grad(lg, ids, dw.cuda(), renorm=renorm)
+        ref = moe.route_grad(ln, rid, dw.numpy(), renorm)
+        p = np.stack([moe.softmax(ln[i], [x for x in rid[i] if x >= 0] if renorm else None)
+                      if (rid[i] >= 0).any() else np.zeros(e) for i in range(t)])
+        s = np.zeros((t, e))
+        for i in range(t):
+            for j in range(k):
+                if rid[i, j] >= 0:
+                    s[i, rid[i, j]] = abs(float(dw[i, j]))
+        # w (s - m): the weight's error and those of m and the difference, on |s| + sum w |s|
+        bound = 2.0 ** -15 * p * (s + (p * s).sum(1, keepdims=True)) + half_ulp(ref, dtype) + 1e-38
+        assert d.dtype == dtype
+        assert np.all(np.abs(d.double().cpu().numpy() - ref) <= bound)
+
+
+def test_route_special_values():
+    inf, nan = float("inf"), float("nan")
+    low = torch.finfo(F32).min
+    l = torch.tensor([[0.0, -0.0, -0.0, 0.0],       # equal: by index
+                      [low, -inf, low, -inf],       # the type's lowest value is open
+                      [1.0, nan, 2.0, -inf],
+                      [inf, 1.0, inf, 0.0],
+                      [-nan, 1.0, nan, 0.0]], device="cuda")
+    ids, w = av.averis_moe_route(l, 3)
+    assert ids.tolist() == [[0, 1, 2], [0, 2, -1], [1, 2, 0], [0, 2, 1], [0, 2, 1]]
+    w = w.cpu().numpy()
+    np.testing.assert_allclose(w[0], 1 / 3, rtol=1e-6)
+    np.testing.assert_array_equal(w[1], [0.5, 0.5, 0.0])
+    assert np.isnan(w[2]).all() and np.isnan(w[3]).any() and np.isnan(w[4]).all()
+
+
+def test_route_gradient_against_differences():
+    """d sum(dw w) along a direction, by differences of the GPU's own weights:
+    a step of 2^-6 leaves a truncation error of h^2 |f'''| / 6 < 5e-5 |dw| and
+    rounding of 2^-17 / h < 5e-4 of the weights."""
+    rng = np.random.default_rng(3)
+    l = torch.from_numpy(rng.standard_normal((64, 16)).astype(np.float32)).cuda()
+    l += 4.0 * (torch.arange(16, device="cuda") % 2)     # the choice stays put under the step
+    v = torch.from_numpy(rng.standard_normal((64, 16)).astype(np.float32)).cuda().clamp(-1, 1)
+    dw = torch.from_numpy(rng.standard_normal((64, 8)).astype(np.float32)).cuda()
+    h = 2.0 ** -6
+    for renorm in (True, False):
+        ids, _ = av.averis_moe_route(l, 8, renorm=renorm)
+
+        def f(x):
+            i2, w = av.averis_moe_route(x, 8, renorm=renorm)
+            at = (ids[:, :, None] == i2[:, None, :]).double()
+            assert at.sum() == ids.numel()
+            return (at @ w.double()[:, :, None]).squeeze(2).mul(dw).sum(1)
+        diff = (f(l + h * v) - f(l - h * v)) / (2 * h)
+        d = (av.averis_moe_route_grad(l, ids, dw, renorm=renorm).double() * v).sum(1)
+        assert float((diff - d).abs().max()) < 2e-3 * float(dw.abs().max())
+
+
+SORTS = [(1, 1, 1), (1, 8, 64), (16, 8, 64), (7, 3, 5), (1024, 8, 64), (1025, 8, 64), (2731, 3, 1000),
+         (8192, 1, 1024), (20000, 2, 3), (4096, 8, 128)]
+
+
+@pytest.mark.parametrize("t,k,e", SORTS)
+@pytest.mark.parametrize("kind", ["mixed", "one", "dropped"])
+def test_sort(t, k, e, kind):
+    rng = np.random.default_rng([t, k, e])
+    ids = rng.integers(0, e, (t, k)).astype(np.int32)
+    if kind == "one":
+        ids[:] = e - 1
+    if kind == "dropped":
+        ids[rng.random((t, k)) < 0.5] = -1
+        ids[rng.random((t, k)) < 0.1] = e
+        ids[rng.random((t, k)) < 0.1] = 2 ** 31 - 1
+    off, pos, src = av.averis_moe_sort(torch.from_numpy(ids).cuda(), e)
+    # the definition, by a stable sort of the keys
+    key = np.where((ids.reshape(-1) >= 0) & (ids.reshape(-1) < e), ids.reshape(-1), e)
+    rsrc = np.argsort(key, kind="stable")
+    roff = np.concatenate([[0], np.cumsum(np.bincount(key, minlength=e + 1)[:e])])
+    rpos = np.empty(t * k, np.int64)
+    rpos[rsrc] = np.arange(t * k)
+    rpos = np.where(key < e, rpos, ~rpos).reshape(t, k)
+    np.testing.assert_array_equal(off.cpu().numpy(), roff)
+    np.testing.assert_array_equal(src.cpu().numpy(), rsrc)
+    np.testing.assert_array_equal(pos.cpu().numpy(), rpos)
+    if t * k <= 200:
+        ro, rp, rs = moe.sort(ids, e)
+        np.testing.assert_array_equal(ro, roff)
+        np.testing.assert_array_equal(rp, rpos)
+        np.testing.assert_array_equal(rs, rsrc)
+
+
+def test_sort_of_nothing():
+    off, pos, src = av.averis_moe_sort(torch.empty((0, 4), dtype=torch.int32, device="cuda"), 300)
+    assert off.tolist() == [0] * 301 and pos.shape == (0, 4) and src.numel() == 0
+    ids, w = av.averis_moe_route(torch.empty((0, 8), device="cuda"), 2)
+    assert ids.shape == (0, 2) and w.shape == (0, 2)
+    p = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 8), device="cuda")
+    assert av.averis_moe_dispatch(x, p).shape == (0, 8)
+    assert av.averis_moe_combine(x, p).shape == (0, 8)
+    dr, dw = av.averis_moe_combine_grad(x, x, p, torch.empty((0, 2), device="cuda"))
+    assert dr.shape == (0, 8) and dw.shape == (0, 2)
+
+
+EXCHANGES = [(1, 1, 1, 1), (1, 8, 64, 2048), (5, 2, 3, 7), (33, 3, 4, 515), (16, 9, 32, 1024),
+             (100, 4, 8, 96), (3, 32, 40, 129), (40, 6, 16, 4097)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,k,e,h", EXCHANGES)
+def test_exchange_and_gradients(t, k, e, h, dtype):
+    rng = np.random.default_rng([t, k, e, h])
+    ids = rng.integers(0, e, (t, k)).astype(np.int32)
+    ids[rng.random((t, k)) < 0.2] = -1
+    if t > 4:
+        ids[4] = -1                                # a token without any expert
+    _, pos, _ = av.averis_moe_sort(torch.from_numpy(ids).cuda(), e)
+    pn = pos.cpu().numpy()
+    draw = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dtype)
+    x, rows, dy = draw(t, h), draw(t * k, h), draw(t, h)
+    rows[torch.from_numpy(~pn[pn < 0].astype(np.int64))] = float("nan")   # tail rows are not read
+    w = torch.from_numpy(rng.standard_normal((t, k)).astype(np.float32))
+    w[torch.from_numpy(pn < 0)] = float("nan")                            # nor their weights
+    n64 = lambda a: a.double().numpy()
+    xs, rs, ds = strided(x, 5), strided(rows, 1, 3), strided(dy, 0, 1)
+    got = av.averis_moe_dispatch(xs, pos)
+    np.testing.assert_array_equal(got.double().cpu().numpy(), moe.dispatch(n64(x), pn))
+    for weights in (None, w):
+        y = av.averis_moe_combine(rs, pos, weights.cuda() if weights is not None else None)
+        ref, mag = moe.combine(n64(rows), pn, None if weights is None else n64(weights))
+        assert y.dtype == dtype
+        assert np.all(np.abs(y.double().cpu().numpy() - ref)
+                      <= (k + 1) * 2.0 ** -24 * mag + half_ulp(ref, dtype))
+    dr, dw = av.averis_moe_combine_grad(ds, rs, pos, w.cuda())
+    rdr, rdw, mag = moe.combine_grad(n64(dy), n64(rows), pn, n64(w))
+    assert np.all(np.abs(dr.double().cpu().numpy() - rdr)
+                  <= 1.01 * half_ulp(rdr, dtype) + 2.0 ** -24 * np.abs(rdr))
+    assert np.all(np.abs(dw.cpu().numpy() - rdw) <= (h / 64 + 16) * 2.0 ** -24 * mag)
+    # in place: the rows' gradient over the rows
+    dr2, dw2 = av.averis_moe_combine_grad(ds, rs, pos, w.cuda(), out=rs)
+    assert torch.equal(dr2, dr) and torch.equal(dw2, dw) and dr2.data_ptr() == rs.data_ptr()
+
+
+def test_outputs_stay_inside_their_rows():
+    """Strided outputs: nothing outside the columns is touched."""
+    t, k, h = 9, 3, 45
+    ids = torch.randint(0, 4, (t, k), dtype=torch.int32, device="cuda")
+    _, pos, _ = av.averis_moe_sort(ids, 4)
+    for dtype in (BF16, F32):
+        buf = torch.full((t * k, h + 6), 5.0, dtype=dtype, device="cuda")
+        av.averis_moe_dispatch(torch.randn(t, h, device="cuda").to(dtype), pos, out=buf[:, 3:3 + h])
+        assert (buf[:, :3] == 5).all() and (buf[:, 3 + h:] == 5).all()
+        buf2 = torch.full((t, h + 6), 5.0, dtype=dtype, device="cuda")
+        av.averis_moe_combine(buf[:, 3:3 + h], pos, out=buf2[:, 3:3 + h])
+        assert (buf2[:, :3] == 5).all() and (buf2[:, 3 + h:] == 5).all()
+
+
+def test_other_stream_and_graph_replay():
+    """The calls run on the current stream, and a captured step replays to the
+    eager results with other work in between."""
+    t, k, e, h = 3000, 4, 32, 256
+    l = torch.randn(t, e, device="cuda").to(BF16)
+    x = torch.randn(t, h, device="cuda").to(BF16)
+    dy = torch.randn(t, h, device="cuda").to(BF16)
+
+    def step():
+        ids, w = av.averis_moe_route(l, k)
+        off, pos, src = av.averis_moe_sort(ids, e)
+        rows = av.averis_moe_dispatch(x, pos)
+        y = av.averis_moe_combine(rows, pos, w)
+        dr, dw = av.averis_moe_combine_grad(dy, rows, pos, w)
+        return [ids, w, off, pos, src, rows, y, dr, dw, av.averis_moe_combine(dr, pos),
+                av.averis_moe_route_grad(l, ids, dw)]
+    ref = [v.clone() for v in step()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = step()
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for _ in range(3):
+        for v in out:
+            v.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+        step()
+
+
+def test_rows_past_2_31_bytes():
+    """Row addresses past 32 bits: 70000 rows of 32768 bytes."""
+    t, k, h = 70000, 1, 16384
+    ids = torch.zeros((t, k), dtype=torch.int32, device="cuda")
+    ids[::2] = 1
+    _, pos, _ = av.averis_moe_sort(ids, 2)
+    x = torch.randn(t, 64, device="cuda").to(BF16).repeat(1, h // 64)
+    rows = av.averis_moe_dispatch(x, pos)
+    p = pos[:, 0].long()
+    assert torch.equal(rows[p[-5:]], x[-5:]) and torch.equal(rows[p[:5]], x[:5])
+    y = av.averis_moe_combine(rows, pos)
+    assert torch.equal(y, x)
