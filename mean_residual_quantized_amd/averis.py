@@ -22,7 +22,7 @@ STATUS_NAMES = {0: "OK", 1: "E_NULL", 2: "E_SHAPE", 3: "E_DTYPE", 4: "E_ALIGN",
 F32, BF16 = 0, 1
 RN, SR = 0, 1
 OP_SPLIT_QUANT, OP_QUANT, OP_GEMM, OP_WGRAD, OP_QUANT_PAIR_MULTI = 0, 1, 2, 3, 4
-OP_MOE_SORT, OP_GRAD_NORM = 5, 6
+OP_MOE_SORT, OP_GRAD_NORM, OP_FP8_GEMM, OP_FP8_WGRAD = 5, 6, 7, 8
 MAX_WEIGHTS = 16
 MAX_RANK1 = 4
 MAX_EXPERTS, MAX_TOPK, MAX_GRADS = 1024, 32, 1 << 20
@@ -40,6 +40,8 @@ EXPORTS = [
     "averis_split_quant_noalloc", "averis_gemm_rank1_stats", "averis_split_quant_from_stats",
     "averis_moe_route", "averis_moe_route_grad", "averis_moe_sort", "averis_moe_dispatch",
     "averis_moe_combine", "averis_moe_combine_grad", "averis_grad_norm", "averis_grad_clip",
+    "averis_fp8_seg_cols", "averis_fp8_quant", "averis_fp8_quant_weight", "averis_fp8_gemm",
+    "averis_fp8_gemm_wgrad",
     "averis_workspace_bytes", "averis_status_str",
     "averis_abi_version", "averis_last_error",
 ]
@@ -62,6 +64,11 @@ class _Weight(ctypes.Structure):
                 ("out", ctypes.POINTER(_NVFP4)), ("out_t", ctypes.POINTER(_NVFP4))]
 
 
+class _FP8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
 class _Grad(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype", ctypes.c_int)]
@@ -80,7 +87,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I64, U64, I, U32, SZ = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_int,
                                    ctypes.c_uint32, ctypes.c_size_t)
-        T = ctypes.POINTER(_NVFP4)
+        T, F8 = ctypes.POINTER(_NVFP4), ctypes.POINTER(_FP8)
         sig = {
             "averis_split_quant": [P, I, I64, I64, I64, U64, I, T, T, P, P, SZ, P],
             "averis_split_quant_grouped": [P, I, I64, I64, I64, P, I, U64, I, T, T, P, P, SZ, P],
@@ -113,6 +120,10 @@ def lib():
             "averis_moe_dispatch": [P, I, I64, I64, I64, P, I, P, I64, P],
             "averis_moe_combine": [P, I, I64, I64, I64, P, P, I, P, I64, P],
             "averis_moe_combine_grad": [P, I, I64, I64, I64, P, I64, P, P, I, P, I64, P, P],
+            "averis_fp8_quant": [P, I, I64, I64, I64, P, I, F8, F8, P],
+            "averis_fp8_quant_weight": [P, I, I, I64, I64, I64, I64, F8, F8, P],
+            "averis_fp8_gemm": [F8, F8, P, I, P, I, I64, P, SZ, P],
+            "averis_fp8_gemm_wgrad": [F8, F8, I64, P, I, P, I, I64, P, SZ, P],
             "averis_grad_norm": [I, P, P, P, SZ, P],
             "averis_grad_clip": [I, P, ctypes.c_double, ctypes.c_double, P, P, SZ, P],
         }
@@ -122,6 +133,8 @@ def lib():
             f.restype = ctypes.c_int
         L.averis_workspace_bytes.argtypes = [I, I64, I64, I64, I64]
         L.averis_workspace_bytes.restype = SZ
+        L.averis_fp8_seg_cols.argtypes = [I64, I64]
+        L.averis_fp8_seg_cols.restype = I64
         L.averis_status_str.argtypes = [I]
         L.averis_status_str.restype = ctypes.c_char_p
         L.averis_abi_version.argtypes = []
@@ -606,6 +619,8 @@ def _matrix(t, ref, what, shape=None):
         raise ValueError("%s: expected a 2-D %s tensor on %s" % (what, ref.dtype, ref.device))
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.numel() == 0:
+        return max(t.shape[1], 1)
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("%s: expected unit column stride" % what)
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
@@ -719,6 +734,132 @@ def averis_moe_combine_grad(dy, rows, pos, weights, out=None):
         dy.data_ptr(), _dtype_code(dy), tokens, cols, ldy, rows.data_ptr(), ldr, pos.data_ptr(),
         weights.data_ptr(), topk, out.data_ptr(), lddr, dweights.data_ptr(), _stream()))
     return out, dweights
+
+
+# --------------------------------------------------------------------------
+# linears in block-scaled fp8
+# --------------------------------------------------------------------------
+
+@dataclass
+class FP8:
+    """Device fp8 tensor with one power-of-two scale for 128 elements along the
+    columns: codes u8[rows, cols rounded up to 128] (E4M3, zero past cols),
+    scales u8[rows, ceil(cols / 128) rounded up to 4] (E8M0)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    cols: int
+
+    @staticmethod
+    def pitches(cols):
+        blocks = (cols + 127) // 128
+        return 128 * blocks, (blocks + 3) // 4 * 4
+
+    @staticmethod
+    def empty(rows, cols, device="cuda"):
+        p, s = FP8.pitches(cols)
+        return FP8(torch.empty((rows, p), dtype=torch.uint8, device=device),
+                   torch.empty((rows, s), dtype=torch.uint8, device=device), rows, cols)
+
+    def c(self):
+        p, s = FP8.pitches(self.cols)
+        if (tuple(self.codes.shape) != (self.rows, p) or tuple(self.scales.shape) != (self.rows, s)
+                or self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8
+                or not self.codes.is_contiguous() or not self.scales.is_contiguous()):
+            raise ValueError("expected contiguous uint8 codes %s and scales %s"
+                             % ((self.rows, p), (self.rows, s)))
+        return _FP8(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+
+
+def _segments(offsets, ref):
+    """(address or None, number of segments) of the offsets of a grouped call."""
+    if offsets is None:
+        return None, 1
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets: expected nseg + 1 values")
+    _like(offsets, ref, torch.int64, "offsets")
+    return offsets.data_ptr(), offsets.numel() - 1
+
+
+def averis_fp8_quant(a, transposed=False, offsets=None, plain=True):
+    """a quantized along its columns, and (transposed=True) its transpose along
+    a's rows too; returns q, or (q, qt) with q None unless plain.  offsets:
+    the rows' segments (each starts a run of its own in qt)."""
+    lda = _matrix(a, a, "a")
+    rows, cols = a.shape
+    offs, nseg = _segments(offsets, a)
+    q = FP8.empty(rows, cols, a.device) if plain else None
+    qt = None
+    if transposed:
+        tc = rows if offsets is None else int(lib().averis_fp8_seg_cols(rows, nseg))
+        qt = FP8.empty(cols, tc, a.device)
+    _check("averis_fp8_quant", lib().averis_fp8_quant(
+        a.data_ptr(), _dtype_code(a), rows, cols, lda, offs, nseg,
+        ctypes.byref(q.c()) if q is not None else None,
+        ctypes.byref(qt.c()) if qt is not None else None, _stream()))
+    return (q, qt) if transposed else q
+
+
+def averis_fp8_quant_weight(w):
+    """Both copies of a weight from one quantization in 128 x 128 tiles:
+    returns (wt, wd) as averis_quant_pair does, wt = Q(w)^T (the forward
+    operand) and wd = Q(w) (the dgrad operand).  w: 2-D, or 3-D (a stack)."""
+    a = w if w.dim() == 3 else w.unsqueeze(0)
+    batch, rows, cols = a.shape
+    if a.stride(2) != 1:
+        raise ValueError("expected unit innermost stride")
+    wd = FP8.empty(batch * rows, cols, w.device)
+    wt = FP8.empty(batch * cols, rows, w.device)
+    _check("averis_fp8_quant_weight", lib().averis_fp8_quant_weight(
+        a.data_ptr(), _dtype_code(a), batch, rows, cols, a.stride(1), a.stride(0),
+        ctypes.byref(wd.c()), ctypes.byref(wt.c()), _stream()))
+    return wt, wd
+
+
+def _fp8_product(ws, op, dims, dev):
+    """The workspace of a product: the caller's, a new one, or none."""
+    if ws is None:
+        need = workspace_bytes(op, *dims)
+        ws = _workspace(need, dev) if need else None
+    return (ws.data_ptr(), ws.numel()) if ws is not None else (None, 0)
+
+
+def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=None):
+    """c = deq(a) deq(b)^T; with offsets the rows of segment s times the s-th
+    of the matrices stacked in b."""
+    dev = a.codes.device
+    offs, nseg = _segments(offsets, a.codes)
+    m, k, n = a.rows, a.cols, b.rows // nseg
+    c = _out(m, n, out_dtype, dev, out)
+    ldc = _matrix(c, c, "out", (m, n))
+    wp, wn = _fp8_product(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
+    _check("averis_fp8_gemm", lib().averis_fp8_gemm(
+        ctypes.byref(a.c()), ctypes.byref(b.c()), offs, nseg, c.data_ptr(), _dtype_code(c), ldc,
+        wp, wn, _stream()))
+    return c
+
+
+def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=None, out=None,
+                          ws=None):
+    """dw = deq(xt) deq(dt)^T over the tokens (m x n), from averis_fp8_quant's
+    transposed copies; with the offsets of the quantization and its number of
+    rows (by default the largest that the copies can hold) one matrix a
+    segment (nseg x m x n)."""
+    dev = xt.codes.device
+    offs, nseg = _segments(offsets, xt.codes)
+    m, n = xt.rows, dt.rows
+    if rows is None:
+        # seg_cols(rows) = (ceil(rows / 128) + nseg) * 128 for more than one segment
+        rows = xt.cols - (128 * nseg if offsets is not None and nseg > 1 else 0)
+    shape = (m, n) if offsets is None else (nseg, m, n)
+    c = out if out is not None else torch.empty(shape, dtype=out_dtype, device=dev)
+    if tuple(c.shape) != shape or not c.is_contiguous():
+        raise ValueError("out: expected a contiguous tensor of shape %s" % (shape,))
+    wp, wn = _fp8_product(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
+    _check("averis_fp8_gemm_wgrad", lib().averis_fp8_gemm_wgrad(
+        ctypes.byref(xt.c()), ctypes.byref(dt.c()), rows, offs, nseg, c.data_ptr(),
+        _dtype_code(c), n, wp, wn, _stream()))
+    return c
 
 
 # --------------------------------------------------------------------------

@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libaveris.so")
 BUILD = os.path.join(ROOT, "_build")
 
-SOURCES = ["api.cpp", "api_moe.cpp", "quant.hip", "gemm.hip", "gemm_ws.hip", "gemm_win.hip",
-           "moe.hip", "clip.hip"]
+SOURCES = ["api.cpp", "api_moe.cpp", "api_fp8.cpp", "quant.hip", "gemm.hip", "gemm_ws.hip",
+           "gemm_win.hip", "moe.hip", "clip.hip", "fp8_quant.hip", "gemm_fp8.hip"]
 
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",

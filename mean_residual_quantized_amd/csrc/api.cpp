@@ -132,6 +132,15 @@ size_t averis_workspace_bytes(averis_op_t op, int64_t rows, int64_t cols, int64_
   if (op == AVERIS_OP_MOE_SORT)
     return (rows >= 0 && rows <= INT32_MAX && n >= 1 && n <= kMaxExperts)
                ? moe_sort_ws_bytes(rows, (int)n) : 0;
+  if (op == AVERIS_OP_FP8_GEMM || op == AVERIS_OP_FP8_WGRAD) {
+    const bool wgrad = op == AVERIS_OP_FP8_WGRAD;
+    if (rows < 0 || n < 0 || nseg < 0 || nseg > kMaxSeg || cols < (wgrad ? 0 : 1)) return 0;
+    const int64_t k = wgrad && nseg > 0 ? averis_fp8_seg_cols(cols, nseg) : cols;
+    return k < 0 ? 0
+                 : fp8_gemm_ws_bytes(rows, n, (k + 127) / 128,
+                                     nseg == 0 ? kF8All : wgrad ? kF8BlockSegs : kF8RowSegs,
+                                     nseg > 0 ? (int)nseg : 1);
+  }
   if (op == AVERIS_OP_GRAD_NORM)
     return (n >= 0 && n <= kMaxGrads) ? grad_norm_ws_bytes((int)n) : 0;
   if (op == AVERIS_OP_WGRAD) {
@@ -155,6 +164,8 @@ size_t averis_workspace_bytes(averis_op_t op, int64_t rows, int64_t cols, int64_
     case AVERIS_OP_QUANT_PAIR_MULTI:
     case AVERIS_OP_MOE_SORT:
     case AVERIS_OP_GRAD_NORM:
+    case AVERIS_OP_FP8_GEMM:
+    case AVERIS_OP_FP8_WGRAD:
       break;
   }
   return 0;

@@ -1,0 +1,329 @@
+// Quantization to block-scaled fp8 (fp8_common.hpp) for gfx950.
+//
+//   k_fp8_rows   runs of 128 along the columns: one read of the input, no LDS
+//   k_fp8_tile   128 x 128 tiles through LDS: the transposed copy (runs along
+//                the rows), with or without the plain copy, from one read; or
+//                both copies of a weight with one scale for the whole tile
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp8_common.hpp"
+#include "launch.hpp"
+#include "segments.hpp"
+
+namespace averis {
+namespace {
+
+// eight consecutive elements of a row, as loaded
+template <typename T>
+struct Eight;
+template <>
+struct Eight<uint16_t> {
+  u32x4_t w;
+  __device__ __forceinline__ void zero() { w = u32x4_t{0u, 0u, 0u, 0u}; }
+  // elements c .. c + 7 of a row of cols elements, 0 past its end
+  __device__ __forceinline__ void load(const uint16_t* row, int64_t c, int64_t cols) {
+    if (c + 8 <= cols) {
+      w = *reinterpret_cast<const f8_piece_t*>(row + c);
+      return;
+    }
+    zero();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) w[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
+  }
+  // bits of the largest magnitude, as fp32
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t k = 0x7FFF7FFFu;
+    const uint32_t m = pk_max_u16(pk_max_u16(w[0] & k, w[1] & k), pk_max_u16(w[2] & k, w[3] & k));
+    const uint32_t lo = m << 16, hi = m & 0xFFFF0000u;
+    return lo > hi ? lo : hi;
+  }
+  __device__ __forceinline__ u32x2_t codes(uint32_t byte) const {
+    return u32x2_t{f8_codes4_bf16(w[0], w[1], byte), f8_codes4_bf16(w[2], w[3], byte)};
+  }
+};
+template <>
+struct Eight<float> {
+  u32x4_t w[2];
+  __device__ __forceinline__ void zero() { w[0] = w[1] = u32x4_t{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const float* row, int64_t c, int64_t cols) {
+    if (c + 8 <= cols) {
+      w[0] = *reinterpret_cast<const f8_piece_t*>(row + c);
+      w[1] = *reinterpret_cast<const f8_piece_t*>(row + c + 4);
+      return;
+    }
+    zero();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) w[i / 4][i % 4] = __float_as_uint(row[c + i]);
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t a = w[i / 4][i % 4] & 0x7FFFFFFFu;
+      m = a > m ? a : m;
+    }
+    return m;
+  }
+  __device__ __forceinline__ u32x2_t codes(uint32_t byte) const {
+    auto f = [&](int i) { return __uint_as_float(w[i / 4][i % 4]); };
+    return u32x2_t{f8_codes4(f(0), f(1), f(2), f(3), byte), f8_codes4(f(4), f(5), f(6), f(7), byte)};
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ u32x2_t eight_codes(const Eight<T>& v, uint32_t amax, uint32_t& byte) {
+  byte = f8_scale_byte(amax);
+  if (__builtin_expect(f8_not_finite(amax), 0)) {
+    byte = kF8One;
+    return u32x2_t{kF8NanCodes, kF8NanCodes};
+  }
+  return v.codes(byte);
+}
+
+// A wavefront takes 512 columns (four blocks, sixteen lanes each, eight
+// elements a lane) of kRowsPerWave rows: all rows' loads in flight, then per
+// row the blocks' maxima by four DPP steps, the codes (8 bytes a lane, 512
+// contiguous bytes a row) and the four scale bytes as one word.
+constexpr int kRowsPerWave = 4;
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_fp8_rows(const T* __restrict__ a, int64_t rows,
+                                                  int64_t cols, int64_t lda, int groups,
+                                                  uint8_t* __restrict__ codes, int64_t pitch,
+                                                  uint8_t* __restrict__ scales, int64_t spitch) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t task = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6));
+  const int g = (int)(task % (uint32_t)groups);
+  const int64_t r0 = (int64_t)(task / (uint32_t)groups) * kRowsPerWave;
+  if (r0 >= rows) return;
+  const int64_t c = 512 * (int64_t)g + 8 * lane;
+  Eight<T> v[kRowsPerWave];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWave; ++i) {
+    v[i].zero();
+    if (r0 + i < rows) v[i].load(a + (r0 + i) * lda, c, cols);
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWave; ++i) {
+    uint32_t byte;
+    const u32x2_t q = eight_codes(v[i], row16_max(v[i].amax()), byte);
+    const uint32_t word = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
+                          __builtin_amdgcn_readlane(byte, 32) << 16 |
+                          __builtin_amdgcn_readlane(byte, 48) << 24;
+    if (r0 + i >= rows) break;
+    if (c < pitch) *reinterpret_cast<u32x2_t*>(codes + (r0 + i) * pitch + c) = q;
+    if (lane == 0) *reinterpret_cast<uint32_t*>(scales + (r0 + i) * spitch + 4 * g) = word;
+  }
+}
+
+// One 128 x 128 tile per workgroup.  Thread (r = t / 16, i = t % 16) holds
+// eight columns of rows r, r + 16, ..; a row's run is sixteen lanes, so the
+// plain copy comes from the registers.  The values go to LDS as loaded; for
+// the transposed copy a thread takes a column's (bf16: a column pair's) run of
+// rows from there, and the codes go back through LDS so that eight lanes store
+// a 128-byte row of the transposed copy.
+//
+// TILE: one scale for the tile (both copies then hold the same codes).
+template <typename T>
+constexpr size_t fp8_tile_lds() {
+  return (size_t)128 * 128 * sizeof(T) + 128 * 128 + 4 * 128 * 4;
+}
+
+template <typename T, bool TILE>
+__global__ __launch_bounds__(256) void k_fp8_tile(const T* __restrict__ a, int64_t rows,
+                                                  int64_t cols, int64_t lda, int64_t bstride,
+                                                  const int64_t* offs, int nseg, Fp8Out out,
+                                                  Fp8Out out_t) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
+  T* raw = reinterpret_cast<T*>(sm);                           // [128][128]
+  unsigned char* ct = sm + 128 * 128 * sizeof(T);              // [128 columns][128 rows] codes
+  uint32_t* red = reinterpret_cast<uint32_t*>(ct + 128 * 128);   // maxima of the four wavefronts
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const int64_t c0 = (int64_t)blockIdx.y * 128;
+  // a chunk of 128 rows, of one segment where there are several
+  const SegRange sr = locate_chunk(offs, nseg, rows, 128, blockIdx.x);
+  if (sr.seg < 0) return;
+  const int64_t r0 = sr.r0;
+  const int nr = (int)(sr.r1 - sr.r0);
+  const int64_t b = blockIdx.z;
+  a += b * bstride;
+  const int i = t & 15, r = t >> 4;
+  Eight<T> v[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    v[p].zero();
+    if (r + 16 * p < nr) v[p].load(a + (r0 + r + 16 * p) * lda, c0 + 8 * i, cols);
+  }
+  uint32_t tile_max = 0;
+  if constexpr (TILE) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const uint32_t m = v[p].amax();
+      tile_max = m > tile_max ? m : tile_max;
+    }
+    tile_max = row16_max(tile_max);
+    if (i == 0) red[r] = tile_max;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 16; ++q) tile_max = red[q] > tile_max ? red[q] : tile_max;
+  }
+  if (out.codes) {
+    const int64_t row0 = b * rows + r0 + r;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t byte;
+      const uint32_t m = TILE ? tile_max : row16_max(v[p].amax());
+      const u32x2_t q = eight_codes(v[p], m, byte);
+      if (r + 16 * p < nr) {
+        *reinterpret_cast<u32x2_t*>(out.codes + (row0 + 16 * p) * out.pitch + c0 + 8 * i) = q;
+        if (i == 0) out.scales[(row0 + 16 * p) * out.spitch + blockIdx.y] = (uint8_t)byte;
+      }
+    }
+  }
+  if (!out_t.codes) return;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    T* dst = raw + (r + 16 * p) * 128 + 8 * i;
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<u32x4_t*>(dst) = v[p].w;
+    } else {
+      *reinterpret_cast<u32x4_t*>(dst) = v[p].w[0];
+      *reinterpret_cast<u32x4_t*>(dst + 4) = v[p].w[1];
+    }
+  }
+  __syncthreads();
+  const int64_t orow = b * cols + c0;   // row of the transposed copy
+  auto scale_out = [&](int col, uint32_t byte) {
+    if (c0 + col < cols) out_t.scales[(orow + col) * out_t.spitch + blockIdx.x] = (uint8_t)byte;
+  };
+  // piece q (16 rows) of a column's codes is kept at q ^ (column / 2 mod 8):
+  // neighbouring lanes' writes go to different banks
+  auto put = [&](int col, int q, u32x4_t x) {
+    *reinterpret_cast<u32x4_t*>(ct + col * 128 + 16 * (q ^ ((col >> 1) & 7))) = x;
+  };
+  if constexpr (sizeof(T) == 2) {
+    // columns 2 lane, 2 lane + 1, rows 32 w .. 32 w + 31
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(raw) + 32 * w * 64 + lane;
+    uint32_t x[32];
+#pragma unroll
+    for (int q = 0; q < 32; ++q) x[q] = src[q * 64];
+    uint32_t m0 = tile_max, m1 = tile_max;
+    if constexpr (!TILE) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) m = pk_max_u16(m, x[q] & 0x7FFF7FFFu);
+      red[w * 64 + lane] = m;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) m = pk_max_u16(m, red[q * 64 + lane]);
+      m0 = m << 16;
+      m1 = m & 0xFFFF0000u;
+    }
+    const uint32_t b0 = f8_not_finite(m0) ? kF8One : f8_scale_byte(m0);
+    const uint32_t b1 = f8_not_finite(m1) ? kF8One : f8_scale_byte(m1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4_t y0, y1;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t* z = x + 16 * h + 4 * q;
+        // the low and the high halves of neighbouring rows
+        y0[q] = f8_codes4_bf16(__builtin_amdgcn_perm(z[1], z[0], 0x05040100u),
+                               __builtin_amdgcn_perm(z[3], z[2], 0x05040100u), b0);
+        y1[q] = f8_codes4_bf16(__builtin_amdgcn_perm(z[1], z[0], 0x07060302u),
+                               __builtin_amdgcn_perm(z[3], z[2], 0x07060302u), b1);
+        if (f8_not_finite(m0)) y0[q] = kF8NanCodes;
+        if (f8_not_finite(m1)) y1[q] = kF8NanCodes;
+      }
+      put(2 * lane, 2 * w + h, y0);
+      put(2 * lane + 1, 2 * w + h, y1);
+    }
+    if (w == 0) {
+      scale_out(2 * lane, b0);
+      scale_out(2 * lane + 1, b1);
+    }
+  } else {
+    // column t mod 128, rows 64 (t / 128) .. + 63
+    const int col = t & 127, half = t >> 7;
+    const float* src = reinterpret_cast<const float*>(raw) + 64 * half * 128 + col;
+    uint32_t m = tile_max;
+    if constexpr (!TILE) {
+      for (int q = 0; q < 64; ++q) {
+        const uint32_t z = __float_as_uint(src[q * 128]) & 0x7FFFFFFFu;
+        m = z > m ? z : m;
+      }
+      red[half * 128 + col] = m;
+      __syncthreads();
+      const uint32_t o = red[(half ^ 1) * 128 + col];
+      m = o > m ? o : m;
+    }
+    const uint32_t byte = f8_not_finite(m) ? kF8One : f8_scale_byte(m);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      u32x4_t y;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* z = src + (16 * h + 4 * q) * 128;
+        y[q] = f8_not_finite(m) ? kF8NanCodes : f8_codes4(z[0], z[128], z[256], z[384], byte);
+      }
+      put(col, 4 * half + h, y);
+    }
+    if (half == 0) scale_out(col, byte);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int col = (t >> 3) + 32 * p, q = t & 7;
+    if (c0 + col < cols)
+      *reinterpret_cast<u32x4_t*>(out_t.codes + (orow + col) * out_t.pitch + (int64_t)blockIdx.x * 128 +
+                                  16 * q) =
+          *reinterpret_cast<const u32x4_t*>(ct + col * 128 + 16 * (q ^ ((col >> 1) & 7)));
+  }
+}
+
+template <typename T, bool TILE>
+hipError_t tile_t(const void* a, int batch, int64_t rows, int64_t cols, int64_t lda,
+                  int64_t bstride, const int64_t* offs, int nseg, const Fp8Out& out,
+                  const Fp8Out& out_t, hipStream_t st) {
+  constexpr size_t lds = fp8_tile_lds<T>();
+  const hipError_t e = lds_attr_once<&k_fp8_tile<T, TILE>>((int)lds);
+  if (e != hipSuccess) return e;
+  const dim3 g((unsigned)chunk_upper_bound(rows, offs ? nseg : 1, 128),
+               (unsigned)((cols + 127) / 128), (unsigned)batch);
+  k_fp8_tile<T, TILE><<<g, 256, lds, st>>>(static_cast<const T*>(a), rows, cols, lda, bstride,
+                                           offs, nseg, out, out_t);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_rows(const void* a, bool bf16, int64_t rows, int64_t cols, int64_t lda,
+                           const Fp8Out& out, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  const int groups = (int)((cols + 511) / 512);
+  const int64_t tasks = (rows + kRowsPerWave - 1) / kRowsPerWave * groups;
+  const dim3 g((unsigned)((tasks + 3) / 4));
+  if (bf16)
+    k_fp8_rows<uint16_t><<<g, 256, 0, st>>>(static_cast<const uint16_t*>(a), rows, cols, lda,
+                                            groups, out.codes, out.pitch, out.scales, out.spitch);
+  else
+    k_fp8_rows<float><<<g, 256, 0, st>>>(static_cast<const float*>(a), rows, cols, lda, groups,
+                                         out.codes, out.pitch, out.scales, out.spitch);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_tile(const void* a, bool bf16, bool tile, int batch, int64_t rows,
+                           int64_t cols, int64_t lda, int64_t bstride, const int64_t* offs,
+                           int nseg, const Fp8Out& out, const Fp8Out& out_t, hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  if (bf16)
+    return tile ? tile_t<uint16_t, true>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st)
+                : tile_t<uint16_t, false>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st);
+  return tile ? tile_t<float, true>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st)
+              : tile_t<float, false>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st);
+}
+
+}  // namespace averis

@@ -230,4 +230,48 @@ size_t grad_norm_ws_bytes(int n);
 hipError_t launch_grad_clip(int n, const GradTensor* w, bool scale, double max_norm, double eps,
                             float* norm, void* ws, hipStream_t st);
 
+// ---------------------------------------------------------------------------
+// Block-scaled fp8 (fp8_quant.hip, gemm_fp8.hip)
+// ---------------------------------------------------------------------------
+struct Fp8Out {
+  uint8_t* codes;   // rows of `pitch` bytes
+  uint8_t* scales;  // rows of `spitch` bytes
+  int64_t pitch, spitch;
+};
+struct Fp8Operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t pitch, spitch;
+};
+inline int64_t fp8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
+inline int64_t fp8_spitch(int64_t cols) { return ((cols + 127) / 128 + 3) / 4 * 4; }
+
+// scales for runs of 128 along the columns
+hipError_t launch_fp8_rows(const void* a, bool bf16, int64_t rows, int64_t cols, int64_t lda,
+                           const Fp8Out& out, hipStream_t st);
+// out (may be empty) and out_t of `batch` matrices by 128 x 128 tiles; tile:
+// one scale a tile, else one a run of each copy; offs: the rows' segments
+// (out_t then holds each segment's rows from a multiple of 128 on)
+hipError_t launch_fp8_tile(const void* a, bool bf16, bool tile, int batch, int64_t rows,
+                           int64_t cols, int64_t lda, int64_t bstride, const int64_t* offs,
+                           int nseg, const Fp8Out& out, const Fp8Out& out_t, hipStream_t st);
+
+// What a product contracts: all of k_blocks blocks of 128 (kAll), rows of a
+// and c by segment with a stack of b (kRowSegs), or a range of blocks for each
+// segment, c a stack (kBlockSegs; rows: the rows the segments divide).
+enum Fp8Mode { kF8All, kF8RowSegs, kF8BlockSegs };
+struct Fp8Gemm {
+  Fp8Operand a, b;
+  int64_t m, n, k_blocks;
+  Fp8Mode mode;
+  const int64_t* offs;
+  int nseg;
+  int64_t rows;
+  void* c;
+  bool c_bf16;
+  int64_t ldc;
+};
+size_t fp8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg);
+hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st);
+
 }  // namespace averis
