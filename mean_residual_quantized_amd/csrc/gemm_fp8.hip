@@ -28,13 +28,13 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kF8Threads = 256;   // four wavefronts, 2 x 2 over the tile
 constexpr int kF8BM = 256;        // rows of a tile
+constexpr int kF8Cus = 256;       // CUs of the card: one workgroup each
 
-// two slots of a stage's codes (128 bytes a row) and two of scale words (four
-// stages, 4 bytes a row); the epilogue stages the bf16 tile over them
-constexpr size_t f8_ring_bytes(int fn) { return (size_t)(kF8BM + 64 * fn) * (2 * 128 + 2 * 4); }
-constexpr size_t f8_epi_row(int fn) { return (size_t)2 * 64 * fn + 16; }
+// two slots of a stage's codes (128 bytes a row), two of scale words (four
+// stages, 4 bytes a row), and 4 KB a wavefront for its output
+constexpr int kF8Stage = 4096;
 constexpr size_t f8_lds_bytes(int fn) {
-  return f8_ring_bytes(fn) > kF8BM * f8_epi_row(fn) ? f8_ring_bytes(fn) : kF8BM * f8_epi_row(fn);
+  return (size_t)(kF8BM + 64 * fn) * (2 * 128 + 2 * 4) + 4 * kF8Stage;
 }
 
 template <int V>
@@ -46,8 +46,103 @@ __device__ __forceinline__ i32x8_t frag(u32x4_t a, u32x4_t b) {
   return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
+// f(F8Step<0>), .., f(F8Step<N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each_step(F f) {
+  if constexpr (I < N) {
+    f(F8Step<I>{});
+    each_step<N, I + 1>(f);
+  }
+}
+
+// s_waitcnt vmcnt(N) (vmcnt in bits 3:0 and 15:14; the others not waited for)
+template <int N>
+__device__ __forceinline__ void f8_wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// Chunks of the segments, 64 segments at a time, one a lane: the segment of a
+// chunk (of `ch` rows) or a segment's chunks come from a ballot, with no LDS
+// and no barrier.  Up to 64 segments are read once for a whole kernel.
+struct SegTable {
+  const int64_t* offs;
+  int nseg, ch;
+  int64_t rows;
+  int base;       // first segment of the loaded 64
+  int r0, r1;     // this lane's segment's rows
+  int c0, c1;     // its chunks
+
+  __device__ __forceinline__ void load(int b, int before) {
+    const int lane = threadIdx.x & 63;
+    base = b;
+    int64_t a = 0, e = 0;
+    if (b + lane < nseg) seg_bounds(offs, b + lane, rows, a, e);
+    r0 = (int)a;
+    r1 = (int)e;
+    const int n = (r1 - r0 + ch - 1) / ch;
+    int incl = n;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int t = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += t;
+    }
+    c1 = before + incl;
+    c0 = c1 - n;
+  }
+  __device__ __forceinline__ void init(const int64_t* o, int ns, int64_t r, int c) {
+    offs = o;
+    nseg = ns;
+    rows = r;
+    ch = c;
+    load(0, 0);
+  }
+  // the next 64 segments (false past the last)
+  __device__ __forceinline__ bool advance() {
+    if (base + 64 >= nseg) return false;
+    load(base + 64, __builtin_amdgcn_readlane(c1, 63));
+    return true;
+  }
+  // rows [a, b) of chunk c and its segment; false past the last chunk
+  __device__ __forceinline__ bool chunk(int c, int& seg, int& a, int& b) {
+    if (c < (int)__builtin_amdgcn_readfirstlane(c0)) load(0, 0);
+    do {
+      const uint64_t hit = __ballot(c >= c0 && c < c1);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        seg = base + l;
+        a = (int)__builtin_amdgcn_readlane(r0, l) + (c - (int)__builtin_amdgcn_readlane(c0, l)) * ch;
+        b = __builtin_amdgcn_readlane(r1, l);
+        b = a + ch < b ? a + ch : b;
+        return true;
+      }
+    } while (advance());
+    return false;
+  }
+  // chunks of all segments
+  __device__ __forceinline__ int count() {
+    while (advance()) {}
+    const int n = __builtin_amdgcn_readlane(c1, 63);
+    if (base != 0) load(0, 0);
+    return n;
+  }
+  // chunks [a, b) of a segment
+  __device__ __forceinline__ void segment(int s, int& a, int& b) {
+    if (s < base) load(0, 0);
+    while (s >= base + 64 && advance()) {}
+    a = __builtin_amdgcn_readlane(c0, (s - base) & 63);
+    b = __builtin_amdgcn_readlane(c1, (s - base) & 63);
+  }
+};
+
+// One output tile: rows m0 .. m0 + rows - 1, columns n0 .. n0 + cols - 1 and
+// the blocks kb0 .. kb0 + nk - 1 it contracts (all uniform).
+struct F8Tile {
+  int m0, n0, seg;   // seg: matrix of a stacked b, or plane of c
+  int rows, cols, kb0, nk;
+};
+
 // ---------------------------------------------------------------------------
-// The tiled kernel: 256 x 64 FN outputs a workgroup, one workgroup a CU, each
+// The tiled kernel: 256 x 64 FN outputs a tile, one workgroup a CU, each
 // wavefront 128 x 32 FN of them (4 x FN accumulators of 32 x 32).
 //
 // A stage is one block of 128 k: two k-steps of 64.  Its codes come straight
@@ -56,243 +151,420 @@ __device__ __forceinline__ i32x8_t frag(u32x4_t a, u32x4_t b) {
 // twice).  Two slots: stage s computes k-step 0 from registers while it reads
 // k-step 1's fragments; then (its slot read out, stage s + 1 landed) one
 // barrier; then k-step 1 while stage s + 2 is loaded into the slot and stage s
-// + 1's first fragments are read.
+// + 1's first fragments are read.  Per MFMA one LDS read and one load, by
+// sched_group_barrier.  Scale bytes come four stages at a time, one aligned
+// word a row, the same way.
 //
-// Scale bytes come four stages at a time, one aligned word a row, the same
-// way.
+// A workgroup takes several tiles.  The barrier inside a tile's last stage
+// frees both slots, so the next tile's first two stages are on their way
+// before this tile's output is; the output goes through 4 KB of LDS of the
+// wavefront's own (no barrier) to whole 128-byte lines, and its stores drain
+// under the next tile's products (the waits of the first stage count them).
 // ---------------------------------------------------------------------------
-template <int FN, bool OUT_BF16>
-__global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Operand B, int64_t m,
-                                                           int64_t n, int k_blocks, int mode,
-                                                           const int64_t* offs, int nseg,
-                                                           int64_t seg_rows, void* c, int64_t ldc,
+template <int FN, bool OUT_BF16, int MODE>
+__global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Operand B, int m, int n,
+                                                           int k_blocks, const int64_t* offs,
+                                                           int nseg, int64_t seg_rows, int splits,
+                                                           int tx, int ty, void* c, int64_t ldc,
                                                            int64_t c_split) {
   constexpr int BM = kF8BM, BN = 64 * FN, ROWS = BM + BN;
   constexpr int SLOT = ROWS * 128, SSLOT = ROWS * 4;
   constexpr int CPW = ROWS / 8 / 4;    // code loads a wavefront issues for a stage
   constexpr int SPW = (ROWS / 64 + 3) / 4;   // scale loads for four stages, at most
   constexpr int NF = 4 + FN;
+  constexpr int ES = OUT_BF16 ? 2 : 4;
+  constexpr int GROUP = 128 / ES;      // columns of an output pass: 128 bytes
+  constexpr int PASSES = (32 * FN + GROUP - 1) / GROUP;   // of a 32-row fragment
+  // store instructions of a whole tile
+  constexpr int STORES = 4 * (32 * FN * ES * 32 / 1024);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_f8[];
   unsigned char* ring = smem_f8;
   unsigned char* sring = smem_f8 + 2 * SLOT;
 
-  int64_t tile_x, tile_y;
-  xcd_tile(tile_x, tile_y);
-  int64_t m0 = tile_y * BM, m_end = m;
-  int kb0 = 0, kb1 = k_blocks;
-  int64_t boff = 0;
-  if (mode == kF8RowSegs) {
-    const SegRange sr = locate_chunk(offs, nseg, m, BM, tile_y);
-    if (sr.seg < 0) return;
-    m0 = sr.r0;
-    m_end = sr.r1;
-    boff = (int64_t)sr.seg * n;
-  } else if (mode == kF8BlockSegs) {
-    const SegRange sr = describe_segment(offs, nseg, seg_rows, 128, blockIdx.z);
-    kb0 = (int)sr.c0;
-    kb1 = (int)sr.c1;
-  } else if (gridDim.z > 1) {   // a split's share of the blocks
-    kb0 = (int)((int64_t)k_blocks * blockIdx.z / gridDim.z);
-    kb1 = (int)((int64_t)k_blocks * (blockIdx.z + 1) / gridDim.z);
-  }
-  c = static_cast<char*>(c) + (int64_t)blockIdx.z * c_split * (OUT_BF16 ? 2 : 4);
-  const int64_t n0 = tile_x * BN;
-  const int nk = kb1 - kb0;
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const int rows_here = (int)(m_end - m0 < BM ? m_end - m0 : BM);
-  const int cols_here = (int)(n - n0 < BN ? n - n0 : BN);
+  unsigned char* stg = smem_f8 + 2 * SLOT + 2 * SSLOT + wave * kF8Stage;
 
-  f32x16_t acc[4][FN];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  SegTable segs;
+  if constexpr (MODE == kF8RowSegs) segs.init(offs, nseg, m, BM);
+  if constexpr (MODE == kF8BlockSegs) segs.init(offs, nseg, seg_rows, 128);
 
-  if (nk > 0) {
-    const uint8_t* a_c = A.codes + m0 * A.pitch + (int64_t)kb0 * 128;
-    const uint8_t* b_c = B.codes + (boff + n0) * B.pitch + (int64_t)kb0 * 128;
+  // Tiles are numbered plane by plane (split or segment), within a plane by
+  // groups of four tile rows, column by column.  Workgroup w runs on die w
+  // mod 8; with a workgroup a CU each die takes an eighth of the numbers, its
+  // workgroups side by side, so the tiles a die runs together share operand
+  // rows in its L2.  With a workgroup a tile (segments of very different
+  // lengths are better left to the dispatcher) that is done plane by plane.
+  if constexpr (MODE == kF8RowSegs) ty = segs.count();   // the grid is for as many as there may be
+  const int txy = tx * ty, total = txy * (MODE == kF8BlockSegs ? nseg : splits);
+  const int w = blockIdx.x, grid = gridDim.x;
+  int id, id_end, id_step;
+  if (MODE != kF8BlockSegs && grid == kF8Cus) {
+    const int x = w % kXcds, per = kF8Cus / kXcds;
+    id = total / kXcds * x + total % kXcds * x / kXcds + w / kXcds;
+    id_end = total / kXcds * (x + 1) + total % kXcds * (x + 1) / kXcds;
+    id_step = per;
+  } else {
+    if (w >= total) return;
+    const int z = w / txy, r = w - z * txy, even = txy - txy % kXcds;
+    id = z * txy + (r < even ? (r % kXcds) * (even / kXcds) + r / kXcds : r);
+    id_end = id + 1;
+    id_step = 1;
+  }
+
+  // the next tile with rows, from number id on; false: none
+  auto next_tile = [&](F8Tile& tl) __attribute__((always_inline)) -> bool {
+    for (; id < id_end; id += id_step) {
+      const int z = id / txy, r = id - z * txy;
+      const int g = r / (4 * tx), rr = r - g * 4 * tx;
+      const int gm = ty - 4 * g < 4 ? ty - 4 * g : 4;
+      const int x = rr / gm, y = 4 * g + (rr - x * gm);
+      tl.n0 = x * BN;
+      tl.cols = n - tl.n0 < BN ? n - tl.n0 : BN;
+      tl.m0 = y * BM;
+      int m_end = m;
+      tl.seg = z;
+      tl.kb0 = 0;
+      tl.nk = k_blocks;
+      if constexpr (MODE == kF8RowSegs) {
+        if (!segs.chunk(y, tl.seg, tl.m0, m_end)) continue;
+      } else if constexpr (MODE == kF8BlockSegs) {
+        int kb1;
+        segs.segment(z, tl.kb0, kb1);
+        tl.nk = kb1 - tl.kb0;
+      } else {
+        // (k_blocks < 2^23, splits <= 16)
+        tl.kb0 = k_blocks * z / splits;
+        tl.nk = k_blocks * (z + 1) / splits - tl.kb0;
+      }
+      tl.rows = m_end - tl.m0 < BM ? m_end - tl.m0 : BM;
+      // the quotients come from vector registers: back to scalar ones, which
+      // every base address below then stays in
+      tl.m0 = __builtin_amdgcn_readfirstlane(tl.m0);
+      tl.n0 = __builtin_amdgcn_readfirstlane(tl.n0);
+      tl.seg = __builtin_amdgcn_readfirstlane(tl.seg);
+      tl.rows = __builtin_amdgcn_readfirstlane(tl.rows);
+      tl.cols = __builtin_amdgcn_readfirstlane(tl.cols);
+      tl.kb0 = __builtin_amdgcn_readfirstlane(tl.kb0);
+      tl.nk = __builtin_amdgcn_readfirstlane(tl.nk);
+      id += id_step;
+      return true;
+    }
+    return false;
+  };
+
+  // what the loads of a tile go by
+  const uint8_t *a_c, *b_c, *a_s, *b_s;
+  uint32_t cofs[CPW], sofs[SPW];
+  int ph, g_last;
+  auto set_tile = [&](const F8Tile& tl) __attribute__((always_inline)) {
+    const int64_t brow = (MODE == kF8RowSegs ? (int64_t)tl.seg * n : 0) + tl.n0;
+    a_c = A.codes + tl.m0 * A.pitch + (int64_t)tl.kb0 * 128;
+    b_c = B.codes + brow * B.pitch + (int64_t)tl.kb0 * 128;
     // word g of a row: its stages 4 g .. 4 g + 3 counted from kb0 rounded down
-    const int ph = kb0 & 3;
-    const uint8_t* a_s = A.scales + m0 * A.spitch + (kb0 - ph);
-    const uint8_t* b_s = B.scales + (boff + n0) * B.spitch + (kb0 - ph);
-    const int g_last = (ph + nk - 1) >> 2;
-
+    ph = tl.kb0 & 3;
+    a_s = A.scales + tl.m0 * A.spitch + (tl.kb0 - ph);
+    b_s = B.scales + brow * B.spitch + (tl.kb0 - ph);
+    g_last = (ph + tl.nk - 1) >> 2;
     // code load j: rows 8 j .. 8 j + 7 of the tile's A rows, then B rows; rows
     // past the edge repeat the last one (their products are never stored)
-    const int lr = lane >> 3;
-    const uint32_t piece_off = 16u * (uint32_t)((lane & 7) ^ lr);
-    uint32_t cofs[CPW], sofs[SPW];
+    const uint32_t ap = (uint32_t)A.pitch, bp = (uint32_t)B.pitch;
+    const uint32_t row = 8 * wave + (lane >> 3), piece = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+    const uint32_t a_last = (uint32_t)(tl.rows - 1) * ap, b_last = (uint32_t)(tl.cols - 1) * bp;
 #pragma unroll
     for (int q = 0; q < CPW; ++q) {
-      const int j = wave + 4 * q;
-      const bool isa = 8 * j < BM;
-      const int r = (isa ? 8 * j : 8 * j - BM) + lr;
-      const int lim = isa ? rows_here : cols_here;
-      cofs[q] = (uint32_t)((r < lim ? r : lim - 1) * (isa ? A.pitch : B.pitch)) + piece_off;
+      const bool isa = q < BM / 32;   // exactly when 8 j < BM
+      const uint32_t o = isa ? row * ap + q * 32 * ap : row * bp + (q - BM / 32) * 32 * bp;
+      const uint32_t last = isa ? a_last : b_last;
+      cofs[q] = (o < last ? o : last) + piece;
     }
 #pragma unroll
     for (int q = 0; q < SPW; ++q) {
-      const int i = wave + 4 * q;
-      const bool isa = 64 * i < BM;
-      const int r = (isa ? 64 * i : 64 * i - BM) + lane;
-      const int lim = isa ? rows_here : cols_here;
-      sofs[q] = (uint32_t)((r < lim ? r : lim - 1) * (isa ? A.spitch : B.spitch));
+      const bool isa = q < BM / 256;   // exactly when 64 i < BM
+      const int r = 64 * (wave + 4 * (isa ? q : q - BM / 256)) + lane;
+      const int lim = isa ? tl.rows : tl.cols;
+      sofs[q] = (uint32_t)(r < lim ? r : lim - 1) * (uint32_t)(isa ? A.spitch : B.spitch);
     }
-    auto load_codes = [&](int s, int slot) __attribute__((always_inline)) {
+  };
+  // where stage s's codes start, in scalar registers (a load then takes base and
+  // offset as they are, with no address arithmetic a lane)
+  auto scalar_base = [&](const uint8_t* p) __attribute__((always_inline)) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return reinterpret_cast<const uint8_t*>(((uint64_t)hi << 32) | lo);
+  };
+  auto stage_base = [&](const uint8_t* p, int s) __attribute__((always_inline)) {
+    return scalar_base(p + 128 * (int64_t)s);
+  };
+  // the wavefront's code load q of the stage that starts at ab, bb
+  auto load_code = [&](const uint8_t* ab, const uint8_t* bb, int slot, int q) __attribute__((always_inline)) {
+    __builtin_amdgcn_global_load_lds((const void*)((q < BM / 32 ? ab : bb) + cofs[q]),
+                                     (lds_void*)(ring + slot * SLOT + (wave + 4 * q) * 1024), 16, 0, 0);
+  };
+  auto load_codes = [&](int s, int slot) __attribute__((always_inline)) {
+    const uint8_t *ab = stage_base(a_c, s), *bb = stage_base(b_c, s);
 #pragma unroll
-      for (int q = 0; q < CPW; ++q) {
-        const int j = wave + 4 * q;
-        // 8 j < BM exactly when q < BM / 32
-        const uint8_t* base = (q < BM / 32 ? a_c : b_c) + 128 * (int64_t)s;
-        __builtin_amdgcn_global_load_lds((const void*)(base + cofs[q]),
-                                         (lds_void*)(ring + slot * SLOT + j * 1024), 16, 0, 0);
+    for (int q = 0; q < CPW; ++q) load_code(ab, bb, slot, q);
+  };
+  auto load_scales = [&](int g) __attribute__((always_inline)) {
+    const int gl = g < g_last ? g : g_last;
+#pragma unroll
+    for (int q = 0; q < SPW; ++q) {
+      if (ROWS / 64 % 4 == 0 || wave + 4 * q < ROWS / 64) {
+        const uint8_t* base = scalar_base((q < BM / 256 ? a_s : b_s) + 4 * (int64_t)gl);
+        __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
+                                         (lds_void*)(sring + (g & 1) * SSLOT + (wave + 4 * q) * 256), 4, 0, 0);
       }
-    };
-    auto load_scales = [&](int g) __attribute__((always_inline)) {
-      const int gl = g < g_last ? g : g_last;
-#pragma unroll
-      for (int q = 0; q < SPW; ++q) {
-        const int i = wave + 4 * q;
-        if (ROWS / 64 % 4 == 0 || i < ROWS / 64) {
-          // 64 i < BM exactly when q < BM / 256
-          const uint8_t* base = (q < BM / 256 ? a_s : b_s) + 4 * (int64_t)gl;
-          __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
-                                           (lds_void*)(sring + (g & 1) * SSLOT + i * 256), 4, 0, 0);
-        }
-      }
-    };
-    const int lrow = lane & 31, lh = lane >> 5;
-    auto row_of = [&](int f) { return f < 4 ? wm * 128 + 32 * f : BM + wn * 32 * FN + 32 * (f - 4); };
-    i32x8_t fr[2][NF];
-    // fragments of k-step js (lane half h: pieces 4 js + 2 h and the next)
-    auto read_step = [&](int slot, auto jc) __attribute__((always_inline)) {
-      constexpr int js = decltype(jc)::value;
-      const unsigned char* sl = ring + slot * SLOT + lrow * 128;
-      const int p0 = 16 * ((4 * js + 2 * lh) ^ (lane & 7)), p1 = 16 * ((4 * js + 2 * lh + 1) ^ (lane & 7));
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(sl + row_of(f) * 128 + p0);
-        const u32x4_t y = *reinterpret_cast<const u32x4_t*>(sl + row_of(f) * 128 + p1);
-        fr[js][f] = frag(x, y);
-      }
-    };
-    uint32_t words[NF];
-    auto read_words = [&](int g) __attribute__((always_inline)) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-        words[f] = *reinterpret_cast<const uint32_t*>(sring + (g & 1) * SSLOT + (row_of(f) + lrow) * 4);
-    };
-    int sc[NF];
-    // B's fragment first: a lane then holds four consecutive columns of a row
-    auto mfmas = [&](auto jc) __attribute__((always_inline)) {
-      constexpr int js = decltype(jc)::value;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fr[js][4 + j], fr[js][i], acc[i][j], 0, 0, 0, sc[4 + j], 0, sc[i]);
-    };
-    auto barrier = []() __attribute__((always_inline)) {
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-    };
-    constexpr F8Step<0> step0{};
-    constexpr F8Step<1> step1{};
+    }
+  };
 
+  f32x16_t acc[4][FN];
+  const int lrow = lane & 31, lh = lane >> 5;
+  auto row_of = [&](int f) { return f < 4 ? wm * 128 + 32 * f : BM + wn * 32 * FN + 32 * (f - 4); };
+  i32x8_t fr[2][NF];
+  // half x of fragment f of k-step js (lane half h: piece 4 js + 2 h + x)
+  auto read_half = [&](int slot, int js, int f, int x) __attribute__((always_inline)) {
+    const int piece = 16 * ((4 * js + 2 * lh + x) ^ (lane & 7));
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(ring + slot * SLOT + (row_of(f) + lrow) * 128 + piece);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) fr[js][f][4 * x + e] = (int)v[e];
+  };
+  auto read_step = [&](int slot, int js) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      read_half(slot, js, f, 0);
+      read_half(slot, js, f, 1);
+    }
+  };
+  uint32_t words[NF];
+  auto read_words = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+      words[f] = *reinterpret_cast<const uint32_t*>(sring + (g & 1) * SSLOT + (row_of(f) + lrow) * 4);
+  };
+  int sc[NF];
+  // A k-step's products one by one, each with its share of what runs beside
+  // them: the reads of the other k-step's fragments from slot rslot (READ), and
+  // stage ls's loads into slot lslot (LOAD).  Loads keep the path from the
+  // cache to LDS busy for 16 cycles each, 64 of them a stage: issued in a row
+  // they would hold up the products behind them.  B's fragment goes first: a
+  // lane then holds four consecutive columns of a row.
+  auto k_step = [&](auto jc, auto readc, int rslot, auto loadc, int ls, int lslot) __attribute__((always_inline)) {
+    constexpr int js = decltype(jc)::value, N = 4 * FN;
+    const uint8_t *ab = nullptr, *bb = nullptr;
+    if constexpr (decltype(loadc)::value != 0) {
+      ab = stage_base(a_c, ls);
+      bb = stage_base(b_c, ls);
+    }
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      const int i = x / FN, j = x % FN;
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          fr[js][4 + j], fr[js][i], acc[i][j], 0, 0, 0, sc[4 + j], 0, sc[i]);
+      if constexpr (decltype(loadc)::value != 0) {
+#pragma unroll
+        for (int q = x * CPW / N; q < (x + 1) * CPW / N; ++q) load_code(ab, bb, lslot, q);
+      }
+      if constexpr (decltype(readc)::value != 0) {
+#pragma unroll
+        for (int r = x * 2 * NF / N; r < (x + 1) * 2 * NF / N; ++r) read_half(rslot, js ^ 1, r / 2, r % 2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // a barrier without a fence (which would wait for every load in flight)
+  auto barrier = []() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  constexpr F8Step<0> step0{};
+  constexpr F8Step<1> step1{};
+  // a whole tile's stores were issued after the loads of stages 0 and 1
+  bool behind = false;
+  // the loads landed: stage 0's (later: those of stage 1 and the stores behind
+  // it, if any) or every one
+  auto wait_loads = [&](auto firstc) __attribute__((always_inline)) {
+    constexpr int LATER = decltype(firstc)::value != 0 ? CPW : 0;
+    if (OUT_BF16 && behind) f8_wait_vm<(OUT_BF16 ? STORES + LATER : 0)>();
+    else f8_wait_vm<LATER>();
+  };
+  // stage s in slot s & 1; on entry its first fragments and scale words are
+  // in registers.  NEXT: there is a stage s + 1; LOAD: a stage s + 2.
+  auto stage = [&](int s, auto nextc, auto loadc) __attribute__((always_inline)) {
+    constexpr bool NEXT = decltype(nextc)::value != 0;
+    const int slot = s & 1, q = s + ph;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) sc[f] = (int)(words[f] >> (8 * (q & 3)));
+    __builtin_amdgcn_sched_barrier(0);
+    k_step(step0, step1, slot, step0, 0, 0);
+    // this slot read out and stage s + 1 landed, for every wavefront
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    wait_loads(step0);
+    behind = false;
+    barrier();
+    if constexpr (NEXT) {
+      if ((q & 3) == 0) load_scales((q >> 2) + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (NEXT) read_words((q + 1) >> 2);
+    k_step(step1, nextc, slot ^ 1, loadc, s + 2, slot);
+  };
+  auto first_loads = [&](const F8Tile& tl) __attribute__((always_inline)) {
     load_scales(0);
     load_scales(1);
     load_codes(0, 0);
-    load_codes(nk > 1 ? 1 : 0, 1);
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): nothing else is counted
-    barrier();
-    read_words(0);
-    read_step(0, step0);
-    for (int s = 0; s < nk; ++s) {
-      const int slot = s & 1, q = s + ph;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) sc[f] = (int)(words[f] >> (8 * (q & 3)));
-      read_step(slot, step1);
-      mfmas(step0);
-      // this slot read out and stage s + 1 landed, for every wavefront
-      __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
-      barrier();
-      if (s + 2 < nk) load_codes(s + 2, slot);
-      if (s > 0 && (q & 3) == 0) load_scales((q >> 2) + 1);
-      if (s + 1 < nk) {
-        read_step(slot ^ 1, step0);
-        if (((q + 1) & 3) == 0) read_words((q + 1) >> 2);
-      }
-      mfmas(step1);
-    }
-    mfma_drain();
-    __builtin_amdgcn_s_waitcnt(0x0F70);
-  }
+    load_codes(tl.nk > 1 ? 1 : 0, 1);
+  };
 
-  // ------------------------------------------------------------------ epilogue
-  const int srow = wm * 128 + (lane & 31);
-  const int scol = wn * 32 * FN + (lane >> 5) * 4;
-  if constexpr (OUT_BF16) {
-    __syncthreads();   // every wavefront done with the ring
-    constexpr int kStLd = (int)f8_epi_row(FN);
-    unsigned char* stg = smem_f8;
+  F8Tile cur;
+  if (!next_tile(cur)) return;
+  if (cur.nk > 0) {
+    set_tile(cur);
+    first_loads(cur);
+  }
+  while (true) {
+    const int nk = cur.nk;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const u32x2_t pk = {bf16x2_rne(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                              bf16x2_rne(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
-          *reinterpret_cast<u32x2_t*>(stg + (srow + 32 * i) * kStLd + 2 * (scol + j * 32 + 8 * q)) = pk;
-        }
-    __syncthreads();
-    constexpr int CPR = 2 * BN / 16;   // 16-byte pieces of a tile row
-    uint16_t* cb = static_cast<uint16_t*>(c) + m0 * ldc + n0;
-    const bool st_vec = (ldc % 8 == 0) && ((reinterpret_cast<uintptr_t>(c) & 15) == 0);
-#pragma unroll 4
-    for (int it = 0; it < BM * CPR / kF8Threads; ++it) {
-      const int cidx = t + kF8Threads * it;
-      const int r = cidx / CPR, cc = cidx - r * CPR;
-      if (r >= rows_here) continue;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(stg + r * kStLd + cc * 16);
-      uint16_t* dst = cb + (int64_t)r * ldc + cc * 8;
-      if (st_vec && cc * 8 + 8 <= cols_here) {
-        store_stream(v, reinterpret_cast<u32x4_t*>(dst));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (cc * 8 + e < cols_here) dst[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-      }
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+    if (nk > 0) {
+      wait_loads(step1);
+      barrier();
+      read_words(0);
+      read_step(0, 0);
+      int s = 0;
+      for (; s + 2 < nk; ++s) stage(s, step1, step1);
+      if (s + 1 < nk) stage(s++, step1, step0);
+      stage(s, step0, step0);
+      mfma_drain();
     }
-  } else {
-    const bool vec = rows_here == BM && cols_here == BN && (ldc % 4 == 0) &&
-                     ((reinterpret_cast<uintptr_t>(c) & 15) == 0);
+    F8Tile nxt;
+    const bool more = next_tile(nxt);
+    __builtin_amdgcn_sched_barrier(0);
+    if (more && nxt.nk > 0) {
+      set_tile(nxt);
+      first_loads(nxt);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---------------------------------------------------------------- output
+    // In passes of 32 rows x 128 bytes.  A lane holds four consecutive columns
+    // of a row, lane + 32 the next four; for bf16 the halves swap so that each
+    // has eight (16 bytes).  To LDS (row r's 16-byte piece p at p ^ (r mod 8):
+    // no bank twice), back eight lanes to a row, and out.  A pass's values are
+    // formed while the one before comes back from LDS.  The LDS writes are
+    // asm: the compiler would wait for every load to LDS in flight before a
+    // write of its own.  A wavefront's LDS accesses are in order.
+    char* cb = static_cast<char*>(c) +
+               ((MODE == kF8RowSegs ? 0 : cur.seg * c_split) + cur.m0 * ldc + cur.n0) * ES;
+    const bool whole = (ldc * ES) % 16 == 0 && (c_split * ES) % 16 == 0 && ldc <= (1 << 24) &&
+                       (reinterpret_cast<uintptr_t>(c) & 15) == 0 && cur.rows == BM &&
+                       cur.cols == BN;
+    // the lane's places are formed anew for each tile: kept over the products
+    // they would not fit the registers
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const uint32_t wr = (uint32_t)(uintptr_t)(lds_void*)stg + (ln & 31) * 128 +
+                        16 * ((ln & 7) ^ (ln >> 5));   // piece h; piece p + h at ^ 16 p
+    const unsigned char* src = stg + (ln >> 3) * 128 + 16 * ((ln & 7) ^ (ln >> 3));
+    const uint32_t off = (uint32_t)(ln >> 3) * (uint32_t)(ldc * ES) + 16 * (ln & 7);
+    constexpr int FPP = GROUP / 32;   // fragments of a pass
+    static_assert(FN % FPP == 0, "whole passes");
+    u32x4_t out[4];   // a bf16 pass's values: pieces of two fragments
+    auto form = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
+      if constexpr (OUT_BF16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = srow + 32 * i;
+        for (int u = 0; u < 4; ++u) {
+          // fragment u / 2, column groups 8 q and 8 q + 8, q = 2 (u mod 2)
+          const f32x16_t& y = acc[i][p * FPP + u / 2];
+          const int q = 8 * (u & 1);
+          const auto a = __builtin_amdgcn_permlane32_swap(bf16x2_rne(y[q], y[q + 1]),
+                                                          bf16x2_rne(y[q + 4], y[q + 5]), false, false);
+          const auto b = __builtin_amdgcn_permlane32_swap(bf16x2_rne(y[q + 2], y[q + 3]),
+                                                          bf16x2_rne(y[q + 6], y[q + 7]), false, false);
+          out[u] = u32x4_t{a[0], b[0], a[1], b[1]};
+        }
+      }
+    };
+    // pieces 2 u + h; fp32 straight from the accumulation registers
+    auto to_lds = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t at = wr ^ (32 * u);
+        if constexpr (OUT_BF16) {
+          const u32x4_t v = out[u];
+          asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
+        } else {
+          const f32x16_t& y = acc[i][p];
+          const f32x4_t v = {y[4 * u], y[4 * u + 1], y[4 * u + 2], y[4 * u + 3]};
+          asm volatile("ds_write_b128 %0, %1" ::"v"(at), "a"(v) : "memory");
+        }
+      }
+    };
+    char* base = cb + ((int64_t)(wm * 128) * ldc + wn * 32 * FN) * ES;   // of the wavefront
+    const int64_t step8 = 8 * ldc * ES;
+    if (whole) {
+      form(F8Step<0>{});
+      each_step<4 * PASSES>([&](auto pc) __attribute__((always_inline)) {
+        constexpr int P = decltype(pc)::value;
+        to_lds(pc);
+        u32x4_t v[4];   // row 8 it + lane / 8, piece lane mod 8
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int cl = scol + j * 32 + 8 * q;
-          float* dst = static_cast<float*>(c) + (m0 + r) * ldc + n0 + cl;
-          const f32x4_t y = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                             acc[i][j][4 * q + 3]};
-          if (vec) {
-            store_out(y, reinterpret_cast<f32x4_t*>(dst));
-          } else if (r < rows_here) {
+        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const u32x4_t*>(src + it * 1024);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (P + 1 < 4 * PASSES) form(F8Step<P + 1>{});
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (cl + e < cols_here) dst[e] = y[e];
+        for (int it = 0; it < 4; ++it) {
+          u32x4_t* dst = reinterpret_cast<u32x4_t*>(base + P % PASSES * 128 + off);
+          if constexpr (OUT_BF16) store_stream(v[it], dst);
+          else store_out(v[it], dst);
+          if (it + 1 < 4 || P % PASSES + 1 == PASSES) base += step8;
+          else base -= 3 * step8;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    } else {
+      // rows and columns past the edge left out, any alignment
+      each_step<4 * PASSES>([&](auto pc) __attribute__((always_inline)) {
+        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
+        form(pc);
+        to_lds(pc);
+        const int left = cur.cols - wn * 32 * FN - p * GROUP - (ln & 7) * (16 / ES);
+        int r = wm * 128 + 32 * i + (ln >> 3);
+        char* dst = base + (32 * i + (ln >> 3)) * ldc * ES + p * 128 + 16 * (ln & 7);
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it, r += 8, dst += step8) {
+          const unsigned char* from = src + it * 1024;
+          if (r < cur.rows && left > 0) {
+            if (left >= 16 / ES) {
+              *reinterpret_cast<f8_piece_t*>(dst) = *reinterpret_cast<const u32x4_t*>(from);
+            } else {
+#pragma unroll 1
+              for (int x = 0; x < left; ++x) {
+                if constexpr (OUT_BF16)
+                  reinterpret_cast<uint16_t*>(dst)[x] = reinterpret_cast<const uint16_t*>(from)[x];
+                else
+                  reinterpret_cast<uint32_t*>(dst)[x] = reinterpret_cast<const uint32_t*>(from)[x];
+              }
+            }
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
+      });
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if (!more) break;
+    behind = whole;
+    cur = nxt;
   }
 }
 
@@ -440,20 +712,42 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg)
   return p;
 }
 
-template <int FN, bool OB>
+template <int FN, bool OB, int MODE>
 hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
                      hipStream_t st) {
   constexpr size_t lds = f8_lds_bytes(FN);
-  static_assert(lds + 64 <= 160 * 1024, "fits one CU's LDS");
-  const hipError_t e = lds_attr_once<&k_gemm_f8<FN, OB>>((int)lds);
+  static_assert(lds <= 160 * 1024, "fits one CU's LDS");
+  const hipError_t e = lds_attr_once<&k_gemm_f8<FN, OB, MODE>>((int)lds);
   if (e != hipSuccess) return e;
-  const int64_t tm = g.mode == kF8RowSegs ? chunk_upper_bound(g.m, g.nseg, kF8BM)
-                                          : (g.m + kF8BM - 1) / kF8BM;
-  const dim3 grid((unsigned)((g.n + 64 * FN - 1) / (64 * FN)), (unsigned)tm,
-                  (unsigned)(g.mode == kF8BlockSegs ? g.nseg : splits));
-  k_gemm_f8<FN, OB><<<grid, kF8Threads, lds, st>>>(g.a, g.b, g.m, g.n, (int)g.k_blocks, g.mode,
-                                                   g.offs, g.nseg, g.rows, c, ldc, c_split);
+  const int64_t ty = MODE == kF8RowSegs ? chunk_upper_bound(g.m, g.nseg, kF8BM)
+                                        : (g.m + kF8BM - 1) / kF8BM;
+  const int64_t tx = (g.n + 64 * FN - 1) / (64 * FN);
+  const int64_t tiles = tx * ty * (MODE == kF8BlockSegs ? g.nseg : splits);
+  if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
+  const int64_t grid = MODE == kF8BlockSegs || tiles < kF8Cus ? tiles : kF8Cus;
+  k_gemm_f8<FN, OB, MODE><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(
+      g.a, g.b, (int)g.m, (int)g.n, (int)g.k_blocks, g.offs, g.nseg, g.rows, splits, (int)tx,
+      (int)ty, c, ldc, c_split);
   return hipGetLastError();
+}
+
+template <int FN, bool OB>
+hipError_t gemm_f8_mode(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
+                        hipStream_t st) {
+  switch (g.mode) {
+    case kF8RowSegs: return gemm_f8_t<FN, OB, kF8RowSegs>(g, splits, c, ldc, c_split, st);
+    case kF8BlockSegs: return gemm_f8_t<FN, OB, kF8BlockSegs>(g, splits, c, ldc, c_split, st);
+    default: return gemm_f8_t<FN, OB, kF8All>(g, splits, c, ldc, c_split, st);
+  }
+}
+
+hipError_t gemm_f8(const Fp8Gemm& g, int fn, bool bf16, int splits, void* c, int64_t ldc,
+                   int64_t c_split, hipStream_t st) {
+  if (bf16)
+    return fn == 4 ? gemm_f8_mode<4, true>(g, splits, c, ldc, c_split, st)
+                   : gemm_f8_mode<2, true>(g, splits, c, ldc, c_split, st);
+  return fn == 4 ? gemm_f8_mode<4, false>(g, splits, c, ldc, c_split, st)
+                 : gemm_f8_mode<2, false>(g, splits, c, ldc, c_split, st);
 }
 
 template <int MF>
@@ -483,8 +777,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
   if (p.skinny == 2) return skinny_t<2>(g, st);
   if (p.skinny == 4) return skinny_t<4>(g, st);
   if (p.splits > 1) {
-    hipError_t e = p.fn == 4 ? gemm_f8_t<4, false>(g, p.splits, ws, g.n, g.m * g.n, st)
-                             : gemm_f8_t<2, false>(g, p.splits, ws, g.n, g.m * g.n, st);
+    const hipError_t e = gemm_f8(g, p.fn, false, p.splits, ws, g.n, g.m * g.n, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((g.m * g.n + 1023) / 1024));
     if (g.c_bf16)
@@ -493,12 +786,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
       k_f8_reduce<false><<<grid, 256, 0, st>>>(static_cast<const float*>(ws), p.splits, g.m, g.n, g.c, g.ldc);
     return hipGetLastError();
   }
-  const int64_t cs = g.mode == kF8BlockSegs ? g.m * g.ldc : 0;
-  if (g.c_bf16)
-    return p.fn == 4 ? gemm_f8_t<4, true>(g, 1, g.c, g.ldc, cs, st)
-                     : gemm_f8_t<2, true>(g, 1, g.c, g.ldc, cs, st);
-  return p.fn == 4 ? gemm_f8_t<4, false>(g, 1, g.c, g.ldc, cs, st)
-                   : gemm_f8_t<2, false>(g, 1, g.c, g.ldc, cs, st);
+  return gemm_f8(g, p.fn, g.c_bf16, 1, g.c, g.ldc, g.mode == kF8BlockSegs ? g.m * g.ldc : 0, st);
 }
 
 }  // namespace averis
