@@ -55,6 +55,14 @@ __device__ __forceinline__ void each_step(F f) {
   }
 }
 
+// items [p N / P, (p + 1) N / P) go with step p of P: the step of item k
+template <int N, int P>
+constexpr int step_of(int k) {
+  int p = 0;
+  while ((p + 1) * N / P <= k) ++p;
+  return p;
+}
+
 // s_waitcnt vmcnt(N) (vmcnt in bits 3:0 and 15:14; the others not waited for)
 template <int N>
 __device__ __forceinline__ void f8_wait_vm() {
@@ -175,8 +183,6 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   constexpr int ES = OUT_BF16 ? 2 : 4;
   constexpr int GROUP = 128 / ES;      // columns of an output pass: 128 bytes
   constexpr int PASSES = (32 * FN + GROUP - 1) / GROUP;   // of a 32-row fragment
-  // store instructions of a whole tile
-  constexpr int STORES = 4 * (32 * FN * ES * 32 / 1024);
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_f8[];
   unsigned char* ring = smem_f8;
   unsigned char* sring = smem_f8 + 2 * SLOT;
@@ -303,21 +309,33 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     __builtin_amdgcn_global_load_lds((const void*)((q < BM / 32 ? ab : bb) + cofs[q]),
                                      (lds_void*)(ring + slot * SLOT + (wave + 4 * q) * 1024), 16, 0, 0);
   };
-  auto load_codes = [&](int s, int slot) __attribute__((always_inline)) {
-    const uint8_t *ab = stage_base(a_c, s), *bb = stage_base(b_c, s);
-#pragma unroll
-    for (int q = 0; q < CPW; ++q) load_code(ab, bb, slot, q);
+  // the wavefront's scale load q of word g
+  auto load_scale = [&](int g, int q) __attribute__((always_inline)) {
+    const int gl = g < g_last ? g : g_last;
+    if (ROWS / 64 % 4 == 0 || wave + 4 * q < ROWS / 64) {
+      const uint8_t* base = scalar_base((q < BM / 256 ? a_s : b_s) + 4 * (int64_t)gl);
+      __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
+                                       (lds_void*)(sring + (g & 1) * SSLOT + (wave + 4 * q) * 256), 4, 0, 0);
+    }
   };
   auto load_scales = [&](int g) __attribute__((always_inline)) {
-    const int gl = g < g_last ? g : g_last;
 #pragma unroll
-    for (int q = 0; q < SPW; ++q) {
-      if (ROWS / 64 % 4 == 0 || wave + 4 * q < ROWS / 64) {
-        const uint8_t* base = scalar_base((q < BM / 256 ? a_s : b_s) + 4 * (int64_t)gl);
-        __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
-                                         (lds_void*)(sring + (g & 1) * SSLOT + (wave + 4 * q) * 256), 4, 0, 0);
-      }
+    for (int q = 0; q < SPW; ++q) load_scale(g, q);
+  };
+  // the first loads of a tile of nk stages, one by one: two words of scales,
+  // stage 0, stage 1
+  constexpr int FIRST0 = 2 * SPW + CPW, FIRST = FIRST0 + CPW;
+  auto first_load = [&](int k, int nk) __attribute__((always_inline)) {
+    if (k < 2 * SPW) {
+      load_scale(k / SPW, k % SPW);
+    } else {
+      const int s = k < FIRST0 ? 0 : 1, q = k - (s ? FIRST0 : 2 * SPW), st = s < nk ? s : 0;
+      load_code(stage_base(a_c, st), stage_base(b_c, st), s, q);
     }
+  };
+  auto first_loads = [&](int nk) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < FIRST; ++k) first_load(k, nk);
   };
 
   f32x16_t acc[4][FN];
@@ -382,14 +400,16 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   };
   constexpr F8Step<0> step0{};
   constexpr F8Step<1> step1{};
-  // a whole tile's stores were issued after the loads of stages 0 and 1
-  bool behind = false;
-  // the loads landed: stage 0's (later: those of stage 1 and the stores behind
-  // it, if any) or every one
+  // The loads of stage 0 (later: of stage 1) landed.  A whole tile's output
+  // passes each issue a share of them and then four stores: behind them are
+  // the stores of the pass that issued the last one and all that followed.
+  constexpr int OUT_PASSES = 4 * PASSES;
+  constexpr int AFTER0 = CPW + 4 * (OUT_PASSES - step_of<FIRST, OUT_PASSES>(FIRST0 - 1));
+  static_assert(step_of<FIRST, OUT_PASSES>(FIRST - 1) == OUT_PASSES - 1, "stage 1's last load is the last pass's");
+  bool behind = false;   // the first loads went out with a whole tile's output
   auto wait_loads = [&](auto firstc) __attribute__((always_inline)) {
-    constexpr int LATER = decltype(firstc)::value != 0 ? CPW : 0;
-    if (OUT_BF16 && behind) f8_wait_vm<(OUT_BF16 ? STORES + LATER : 0)>();
-    else f8_wait_vm<LATER>();
+    if (behind) f8_wait_vm<(decltype(firstc)::value != 0 ? AFTER0 : 4)>();
+    else f8_wait_vm<0>();
   };
   // stage s in slot s & 1; on entry its first fragments and scale words are
   // in registers.  NEXT: there is a stage s + 1; LOAD: a stage s + 2.
@@ -412,27 +432,23 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     if constexpr (NEXT) read_words((q + 1) >> 2);
     k_step(step1, nextc, slot ^ 1, loadc, s + 2, slot);
   };
-  auto first_loads = [&](const F8Tile& tl) __attribute__((always_inline)) {
-    load_scales(0);
-    load_scales(1);
-    load_codes(0, 0);
-    load_codes(tl.nk > 1 ? 1 : 0, 1);
+  auto zero = [&](int i, int j) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
   };
 
   F8Tile cur;
   if (!next_tile(cur)) return;
   if (cur.nk > 0) {
     set_tile(cur);
-    first_loads(cur);
+    first_loads(cur.nk);
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) zero(i, j);
   while (true) {
     const int nk = cur.nk;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     if (nk > 0) {
       wait_loads(step1);
       barrier();
@@ -445,12 +461,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
       mfma_drain();
     }
     F8Tile nxt;
-    const bool more = next_tile(nxt);
+    const bool more = next_tile(nxt), loads = more && nxt.nk > 0;
     __builtin_amdgcn_sched_barrier(0);
-    if (more && nxt.nk > 0) {
-      set_tile(nxt);
-      first_loads(nxt);
-    }
+    if (loads) set_tile(nxt);
     __builtin_amdgcn_sched_barrier(0);
 
     // ---------------------------------------------------------------- output
@@ -511,16 +524,27 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     };
     char* base = cb + ((int64_t)(wm * 128) * ldc + wn * 32 * FN) * ES;   // of the wavefront
     const int64_t step8 = 8 * ldc * ES;
+    auto clear = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
+#pragma unroll
+      for (int f = 0; f < FPP; ++f) zero(i, p * FPP + f);
+    };
     if (whole) {
       form(F8Step<0>{});
-      each_step<4 * PASSES>([&](auto pc) __attribute__((always_inline)) {
+      each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
         constexpr int P = decltype(pc)::value;
         to_lds(pc);
+        clear(pc);
         u32x4_t v[4];   // row 8 it + lane / 8, piece lane mod 8
 #pragma unroll
         for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const u32x4_t*>(src + it * 1024);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (P + 1 < 4 * PASSES) form(F8Step<P + 1>{});
+        if constexpr (P + 1 < OUT_PASSES) form(F8Step<P + 1>{});
+        if (loads) {
+#pragma unroll
+          for (int k = P * FIRST / OUT_PASSES; k < (P + 1) * FIRST / OUT_PASSES; ++k)
+            first_load(k, nxt.nk);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
@@ -534,10 +558,12 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
       });
     } else {
       // rows and columns past the edge left out, any alignment
-      each_step<4 * PASSES>([&](auto pc) __attribute__((always_inline)) {
+      if (loads) first_loads(nxt.nk);
+      each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
         constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
         form(pc);
         to_lds(pc);
+        clear(pc);
         const int left = cur.cols - wn * 32 * FN - p * GROUP - (ln & 7) * (16 / ES);
         int r = wm * 128 + 32 * i + (ln >> 3);
         char* dst = base + (32 * i + (ln >> 3)) * ldc * ES + p * 128 + 16 * (ln & 7);
