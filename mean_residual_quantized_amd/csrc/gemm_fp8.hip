@@ -27,14 +27,14 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kF8Threads = 256;   // four wavefronts, 2 x 2 over the tile
-constexpr int kF8BM = 256;        // rows of a tile
 constexpr int kF8Cus = 256;       // CUs of the card: one workgroup each
 
 // two slots of a stage's codes (128 bytes a row), two of scale words (four
-// stages, 4 bytes a row), and 4 KB a wavefront for its output
+// stages, 4 bytes a row), and 4 KB a wavefront for its output (in the small
+// tile, which is its workgroup's only one, over the slots)
 constexpr int kF8Stage = 4096;
-constexpr size_t f8_lds_bytes(int fn) {
-  return (size_t)(kF8BM + 64 * fn) * (2 * 128 + 2 * 4) + 4 * kF8Stage;
+constexpr size_t f8_lds_bytes(int f) {
+  return (size_t)(2 * 64 * f) * (2 * 128 + 2 * 4) + (f == 4 ? 4 * kF8Stage : 0);
 }
 
 template <int V>
@@ -150,8 +150,9 @@ struct F8Tile {
 };
 
 // ---------------------------------------------------------------------------
-// The tiled kernel: 256 x 64 FN outputs a tile, one workgroup a CU, each
-// wavefront 128 x 32 FN of them (4 x FN accumulators of 32 x 32).
+// The tiled kernel: 64 F x 64 F outputs a tile, each of four wavefronts 32 F x
+// 32 F of them (F x F accumulators of 32 x 32): F = 4, one workgroup a CU, or 2
+// (128 x 128), two.
 //
 // A stage is one block of 128 k: two k-steps of 64.  Its codes come straight
 // from memory to LDS (16 bytes a lane, eight lanes to a row, the row's pieces
@@ -169,20 +170,19 @@ struct F8Tile {
 // wavefront's own (no barrier) to whole 128-byte lines, and its stores drain
 // under the next tile's products (the waits of the first stage count them).
 // ---------------------------------------------------------------------------
-template <int FN, bool OUT_BF16, int MODE>
-__global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Operand B, int m, int n,
-                                                           int k_blocks, const int64_t* offs,
-                                                           int nseg, int64_t seg_rows, int splits,
-                                                           int tx, int ty, void* c, int64_t ldc,
-                                                           int64_t c_split) {
-  constexpr int BM = kF8BM, BN = 64 * FN, ROWS = BM + BN;
+template <int F, bool OUT_BF16, int MODE>
+__global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
+    Fp8Operand A, Fp8Operand B, int m, int n, int k_blocks, const int64_t* offs, int nseg,
+    int64_t seg_rows, int splits, int tx, int ty, void* c, int64_t ldc, int64_t c_split) {
+  constexpr bool MANY = F == 4 && MODE != kF8BlockSegs;   // several tiles a workgroup
+  constexpr int BM = 64 * F, BN = 64 * F, ROWS = BM + BN;
   constexpr int SLOT = ROWS * 128, SSLOT = ROWS * 4;
   constexpr int CPW = ROWS / 8 / 4;    // code loads a wavefront issues for a stage
   constexpr int SPW = (ROWS / 64 + 3) / 4;   // scale loads for four stages, at most
-  constexpr int NF = 4 + FN;
+  constexpr int NF = 2 * F;
   constexpr int ES = OUT_BF16 ? 2 : 4;
   constexpr int GROUP = 128 / ES;      // columns of an output pass: 128 bytes
-  constexpr int PASSES = (32 * FN + GROUP - 1) / GROUP;   // of a 32-row fragment
+  constexpr int PASSES = (32 * F + GROUP - 1) / GROUP;   // of a 32-row fragment
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_f8[];
   unsigned char* ring = smem_f8;
   unsigned char* sring = smem_f8 + 2 * SLOT;
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  unsigned char* stg = smem_f8 + 2 * SLOT + 2 * SSLOT + wave * kF8Stage;
+  unsigned char* stg = smem_f8 + (F == 4 ? 2 * SLOT + 2 * SSLOT : 0) + wave * kF8Stage;
 
   SegTable segs;
   if constexpr (MODE == kF8RowSegs) segs.init(offs, nseg, m, BM);
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   const int txy = tx * ty, total = txy * (MODE == kF8BlockSegs ? nseg : splits);
   const int w = blockIdx.x, grid = gridDim.x;
   int id, id_end, id_step;
-  if (MODE != kF8BlockSegs && grid == kF8Cus) {
+  if (MANY && grid == kF8Cus) {
     const int x = w % kXcds, per = kF8Cus / kXcds;
     id = total / kXcds * x + total % kXcds * x / kXcds + w / kXcds;
     id_end = total / kXcds * (x + 1) + total % kXcds * (x + 1) / kXcds;
@@ -287,8 +287,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     }
 #pragma unroll
     for (int q = 0; q < SPW; ++q) {
-      const bool isa = q < BM / 256;   // exactly when 64 i < BM
-      const int r = 64 * (wave + 4 * (isa ? q : q - BM / 256)) + lane;
+      const int i = wave + 4 * q;
+      const bool isa = 64 * i < BM;
+      const int r = (isa ? 64 * i : 64 * i - BM) + lane;
       const int lim = isa ? tl.rows : tl.cols;
       sofs[q] = (uint32_t)(r < lim ? r : lim - 1) * (uint32_t)(isa ? A.spitch : B.spitch);
     }
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   auto load_scale = [&](int g, int q) __attribute__((always_inline)) {
     const int gl = g < g_last ? g : g_last;
     if (ROWS / 64 % 4 == 0 || wave + 4 * q < ROWS / 64) {
-      const uint8_t* base = scalar_base((q < BM / 256 ? a_s : b_s) + 4 * (int64_t)gl);
+      const uint8_t* base = scalar_base((64 * (wave + 4 * q) < BM ? a_s : b_s) + 4 * (int64_t)gl);
       __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
                                        (lds_void*)(sring + (g & 1) * SSLOT + (wave + 4 * q) * 256), 4, 0, 0);
     }
@@ -338,9 +339,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     for (int k = 0; k < FIRST; ++k) first_load(k, nk);
   };
 
-  f32x16_t acc[4][FN];
+  f32x16_t acc[F][F];
   const int lrow = lane & 31, lh = lane >> 5;
-  auto row_of = [&](int f) { return f < 4 ? wm * 128 + 32 * f : BM + wn * 32 * FN + 32 * (f - 4); };
+  auto row_of = [&](int f) { return f < F ? wm * 32 * F + 32 * f : BM + wn * 32 * F + 32 * (f - F); };
   i32x8_t fr[2][NF];
   // half x of fragment f of k-step js (lane half h: piece 4 js + 2 h + x)
   auto read_half = [&](int slot, int js, int f, int x) __attribute__((always_inline)) {
@@ -370,7 +371,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   // they would hold up the products behind them.  B's fragment goes first: a
   // lane then holds four consecutive columns of a row.
   auto k_step = [&](auto jc, auto readc, int rslot, auto loadc, int ls, int lslot) __attribute__((always_inline)) {
-    constexpr int js = decltype(jc)::value, N = 4 * FN;
+    constexpr int js = decltype(jc)::value, N = F * F;
     const uint8_t *ab = nullptr, *bb = nullptr;
     if constexpr (decltype(loadc)::value != 0) {
       ab = stage_base(a_c, ls);
@@ -378,9 +379,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     }
 #pragma unroll
     for (int x = 0; x < N; ++x) {
-      const int i = x / FN, j = x % FN;
+      const int i = x / F, j = x % F;
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          fr[js][4 + j], fr[js][i], acc[i][j], 0, 0, 0, sc[4 + j], 0, sc[i]);
+          fr[js][F + j], fr[js][i], acc[i][j], 0, 0, 0, sc[F + j], 0, sc[i]);
       if constexpr (decltype(loadc)::value != 0) {
 #pragma unroll
         for (int q = x * CPW / N; q < (x + 1) * CPW / N; ++q) load_code(ab, bb, lslot, q);
@@ -403,7 +404,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
   // The loads of stage 0 (later: of stage 1) landed.  A whole tile's output
   // passes each issue a share of them and then four stores: behind them are
   // the stores of the pass that issued the last one and all that followed.
-  constexpr int OUT_PASSES = 4 * PASSES;
+  constexpr int OUT_PASSES = F * PASSES;
   constexpr int AFTER0 = CPW + 4 * (OUT_PASSES - step_of<FIRST, OUT_PASSES>(FIRST0 - 1));
   static_assert(step_of<FIRST, OUT_PASSES>(FIRST - 1) == OUT_PASSES - 1, "stage 1's last load is the last pass's");
   bool behind = false;   // the first loads went out with a whole tile's output
@@ -444,9 +445,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     first_loads(cur.nk);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) zero(i, j);
+    for (int j = 0; j < F; ++j) zero(i, j);
   while (true) {
     const int nk = cur.nk;
     if (nk > 0) {
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
       mfma_drain();
     }
     F8Tile nxt;
-    const bool more = next_tile(nxt), loads = more && nxt.nk > 0;
+    const bool more = MANY && next_tile(nxt), loads = more && nxt.nk > 0;
     __builtin_amdgcn_sched_barrier(0);
     if (loads) set_tile(nxt);
     __builtin_amdgcn_sched_barrier(0);
@@ -488,7 +489,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
     const unsigned char* src = stg + (ln >> 3) * 128 + 16 * ((ln & 7) ^ (ln >> 3));
     const uint32_t off = (uint32_t)(ln >> 3) * (uint32_t)(ldc * ES) + 16 * (ln & 7);
     constexpr int FPP = GROUP / 32;   // fragments of a pass
-    static_assert(FN % FPP == 0, "whole passes");
+    static_assert(F % FPP == 0, "whole passes");
     u32x4_t out[4];   // a bf16 pass's values: pieces of two fragments
     auto form = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
@@ -522,7 +523,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
         }
       }
     };
-    char* base = cb + ((int64_t)(wm * 128) * ldc + wn * 32 * FN) * ES;   // of the wavefront
+    char* base = cb + ((int64_t)(wm * 32 * F) * ldc + wn * 32 * F) * ES;   // of the wavefront
     const int64_t step8 = 8 * ldc * ES;
     auto clear = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
@@ -564,8 +565,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
         form(pc);
         to_lds(pc);
         clear(pc);
-        const int left = cur.cols - wn * 32 * FN - p * GROUP - (ln & 7) * (16 / ES);
-        int r = wm * 128 + 32 * i + (ln >> 3);
+        const int left = cur.cols - wn * 32 * F - p * GROUP - (ln & 7) * (16 / ES);
+        int r = wm * 32 * F + 32 * i + (ln >> 3);
         char* dst = base + (32 * i + (ln >> 3)) * ldc * ES + p * 128 + 16 * (ln & 7);
 #pragma unroll 1
         for (int it = 0; it < 4; ++it, r += 8, dst += step8) {
@@ -597,31 +598,25 @@ __global__ __launch_bounds__(kF8Threads, 1) void k_gemm_f8(Fp8Operand A, Fp8Oper
 // ---------------------------------------------------------------------------
 // Few rows: 16 columns (rows of b) and 16 MF rows of a to a workgroup of eight
 // wavefronts that divide the blocks among them; a wavefront's operands come
-// straight to registers (a block of a row: 32 bytes a lane), and the partial
-// sums meet in LDS.
+// straight to registers (a block of a row: 32 bytes a lane), several blocks'
+// loads in flight, and the partial sums meet in LDS.
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyWaves = 8;
 
 template <int MF, bool OUT_BF16>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_f8_skinny(
-    Fp8Operand A, Fp8Operand B, int64_t m, int64_t n, int k_blocks, const int64_t* offs, int nseg,
-    void* c, int64_t ldc) {
+__global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_f8_skinny(Fp8Operand A, Fp8Operand B,
+                                                                      int64_t m, int64_t n,
+                                                                      int k_blocks, void* c,
+                                                                      int64_t ldc) {
   __shared__ float part[kSkinnyWaves][16][16 * MF + 4];   // [..][column][row]
-  int64_t m0 = (int64_t)blockIdx.y * 16 * MF, m_end = m, boff = 0;
-  if (offs) {
-    const SegRange sr = locate_chunk(offs, nseg, m, 16 * MF, blockIdx.y);
-    if (sr.seg < 0) return;
-    m0 = sr.r0;
-    m_end = sr.r1;
-    boff = (int64_t)sr.seg * n;
-  }
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t m0 = (int64_t)blockIdx.y * 16 * MF, n0 = (int64_t)blockIdx.x * 16;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int rows_here = (int)(m_end - m0 < 16 * MF ? m_end - m0 : 16 * MF);
+  const int rows_here = (int)(m - m0 < 16 * MF ? m - m0 : 16 * MF);
   const int cols_here = (int)(n - n0 < 16 ? n - n0 : 16);
   // rows past the edge repeat the last one (their products are never stored)
-  const int64_t br = boff + n0 + (r < cols_here ? r : cols_here - 1);
+  const int64_t br = n0 + (r < cols_here ? r : cols_here - 1);
   const uint8_t* bc = B.codes + br * B.pitch + 32 * g;
   const uint8_t* bs = B.scales + br * B.spitch;
   const uint8_t *ac[MF], *as[MF];
@@ -634,20 +629,36 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_f8_skinny(
   f32x4_t acc[MF];
 #pragma unroll
   for (int i = 0; i < MF; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int kb0 = k_blocks * w / kSkinnyWaves, kb1 = k_blocks * (w + 1) / kSkinnyWaves;
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int64_t k = (int64_t)kb * 128;
-    const i32x8_t bf = frag(*reinterpret_cast<const u32x4_t*>(bc + k),
-                            *reinterpret_cast<const u32x4_t*>(bc + k + 16));
-    const int sb = bs[kb];
+  // U blocks: every load, then the products
+  auto blocks = [&](int kb, auto uc) __attribute__((always_inline)) {
+    constexpr int U = decltype(uc)::value;
+    i32x8_t bf[U], af[U][MF];
+    int sb[U], sa[U][MF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const i32x8_t af = frag(*reinterpret_cast<const u32x4_t*>(ac[i] + k),
-                              *reinterpret_cast<const u32x4_t*>(ac[i] + k + 16));
-      acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf, af, acc[i], 0, 0, 0, sb, 0,
-                                                                (int)as[i][kb]);
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = (int64_t)(kb + u) * 128;
+      bf[u] = frag(*reinterpret_cast<const u32x4_t*>(bc + k),
+                   *reinterpret_cast<const u32x4_t*>(bc + k + 16));
+      sb[u] = bs[kb + u];
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        af[u][i] = frag(*reinterpret_cast<const u32x4_t*>(ac[i] + k),
+                        *reinterpret_cast<const u32x4_t*>(ac[i] + k + 16));
+        sa[u][i] = as[i][kb + u];
+      }
     }
-  }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[u], af[u][i], acc[i], 0, 0, 0,
+                                                                  sb[u], 0, sa[u][i]);
+  };
+  int kb = (int)((int64_t)k_blocks * w / kSkinnyWaves);
+  const int kb1 = (int)((int64_t)k_blocks * (w + 1) / kSkinnyWaves);
+  for (; kb + 4 <= kb1; kb += 4) blocks(kb, F8Step<4>{});
+  for (; kb + 2 <= kb1; kb += 2) blocks(kb, F8Step<2>{});
+  if (kb < kb1) blocks(kb, F8Step<1>{});
 #pragma unroll
   for (int i = 0; i < MF; ++i)
 #pragma unroll
@@ -710,82 +721,109 @@ __global__ __launch_bounds__(256) void k_f8_reduce(const float* __restrict__ par
 // What runs a product
 // ---------------------------------------------------------------------------
 struct Fp8Plan {
-  int skinny;   // 16-row fragments of the few-rows kernel, 0: the tiled one
-  int fn;       // tile width / 64
-  int splits;   // of the blocks
+  int skinny;   // 16-row fragments of the few-rows kernel, 0: a tiled one
+  int f;        // tile side / 64
+  int splits;   // of the blocks, into fp32 partials
 };
 
+// The choice minimises an estimate in microseconds, fitted to this card: the
+// 256 x 256 tile (a workgroup a CU) takes 1.46 a stage and 9.3 a round of 256
+// tiles, the 128 x 128 tile (two a CU) 1.05 and 2.5 a round of 512, or 0.62 a
+// stage alone on its CU; a split output costs another launch and 8 bytes a
+// value and split at 9.5 TB/s; the few-rows kernel reads both operands once a
+// workgroup at 6.5 TB/s.  Measured either side (us, large / small tile):
+// 8192^3 414 / 558, 16384 x 1024 x 3072 48.5 / 58.2, 2048 x 1024 x 2048 24.0 /
+// 12.4; 64 segments of 512 rows, 768 x 2048: 71.5 / 73.9, of 64 rows: 33.4 /
+// 23.5; weight gradient over 16384 tokens, 1024 x 3072: 140 in one split, 66
+// in five; 16 rows x 1024 x 2048: 9.9 small tile, 4.4 few-rows kernel.
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg) {
-  Fp8Plan p{0, 4, 1};
-  if (mode != kF8BlockSegs) {
-    const int64_t avg = mode == kF8RowSegs ? (m + nseg - 1) / nseg : m;
-    if (avg <= 64) {
-      p.skinny = avg <= 16 ? 1 : avg <= 32 ? 2 : 4;
-      return p;
+  Fp8Plan best{0, 4, 1};
+  double best_us = 1e300;
+  auto offer = [&](const Fp8Plan& p, double us) {
+    if (us < best_us) {
+      best_us = us;
+      best = p;
+    }
+  };
+  const double dm = (double)m, dn = (double)n;
+  for (int f = 4; f >= 2; f -= 2) {
+    const int side = 64 * f, slots = f == 4 ? kF8Cus : 2 * kF8Cus;
+    const double tx = (double)((n + side - 1) / side);
+    double tiles = tx * (double)((m + side - 1) / side), stages = (double)k_blocks;
+    // segments end in part of a tile (a block): half of one on average
+    if (mode == kF8RowSegs) tiles = tx * (dm / side + 0.5 * (double)(nseg < m ? nseg : m));
+    if (mode == kF8BlockSegs) {
+      tiles *= nseg;
+      stages = stages / nseg;
+    }
+    for (int splits = 1; splits <= 16; ++splits) {
+      if (splits > 1 && (mode != kF8All || k_blocks < 2 * splits)) break;
+      const double t = tiles * splits;
+      const double stage = f == 4 ? 1.46 : t <= kF8Cus ? 0.62 : 1.05;
+      const double tile = f == 4 ? 9.3 : t <= kF8Cus ? 1.5 : 2.5;
+      const double rounds = t <= slots ? 1.0 : mode == kF8All ? (double)(int64_t)((t + slots - 1) / slots) : t / slots;
+      offer(Fp8Plan{0, f, splits}, 3.0 + rounds * ((double)((int64_t)(stages + splits - 1) / splits) * stage + tile) +
+                                       (splits > 1 ? 5.0 + splits * dm * dn * 8.0 / 9.5e6 : 0.0));
     }
   }
-  const int64_t tm = mode == kF8RowSegs ? chunk_upper_bound(m, nseg, kF8BM) : (m + kF8BM - 1) / kF8BM;
-  auto tiles = [&](int fn) {
-    return tm * ((n + 64 * fn - 1) / (64 * fn)) * (mode == kF8BlockSegs ? nseg : 1);
-  };
-  // the wider tile unless the narrower one needs less time in rounds of 256
-  const int64_t c4 = (tiles(4) + 255) / 256 * 4, c2 = (tiles(2) + 255) / 256 * 2;
-  if (c2 < c4) p.fn = 2;
   if (mode == kF8All) {
-    const int64_t tl = tiles(p.fn);
-    while (p.splits < 16 && tl * p.splits * 2 <= 256 && k_blocks / (p.splits * 2) >= 4) p.splits *= 2;
+    for (int mf = 1; mf <= 4; mf *= 2) {
+      const double wgs = (double)((n + 15) / 16) * (double)((m + 16 * mf - 1) / (16 * mf));
+      if (wgs > 65536.0) continue;
+      offer(Fp8Plan{mf, 0, 1}, 3.0 + wgs * (double)k_blocks * 128.0 * (16.0 + 16.0 * mf) / 6.5e6 + 0.5 * mf);
+    }
   }
-  return p;
+  return best;
 }
 
-template <int FN, bool OB, int MODE>
+template <int F, bool OB, int MODE>
 hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
                      hipStream_t st) {
-  constexpr size_t lds = f8_lds_bytes(FN);
-  static_assert(lds <= 160 * 1024, "fits one CU's LDS");
-  const hipError_t e = lds_attr_once<&k_gemm_f8<FN, OB, MODE>>((int)lds);
+  constexpr size_t lds = f8_lds_bytes(F);
+  static_assert(lds <= 160 * 1024 / (F == 4 ? 1 : 2), "fits one CU's LDS");
+  const hipError_t e = lds_attr_once<&k_gemm_f8<F, OB, MODE>>((int)lds);
   if (e != hipSuccess) return e;
-  const int64_t ty = MODE == kF8RowSegs ? chunk_upper_bound(g.m, g.nseg, kF8BM)
-                                        : (g.m + kF8BM - 1) / kF8BM;
-  const int64_t tx = (g.n + 64 * FN - 1) / (64 * FN);
+  const int64_t ty = MODE == kF8RowSegs ? chunk_upper_bound(g.m, g.nseg, 64 * F)
+                                        : (g.m + 64 * F - 1) / (64 * F);
+  const int64_t tx = (g.n + 64 * F - 1) / (64 * F);
   const int64_t tiles = tx * ty * (MODE == kF8BlockSegs ? g.nseg : splits);
   if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-  const int64_t grid = MODE == kF8BlockSegs || tiles < kF8Cus ? tiles : kF8Cus;
-  k_gemm_f8<FN, OB, MODE><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(
+  const bool many = F == 4 && MODE != kF8BlockSegs;
+  const int64_t grid = many && tiles > kF8Cus ? kF8Cus : tiles;
+  k_gemm_f8<F, OB, MODE><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(
       g.a, g.b, (int)g.m, (int)g.n, (int)g.k_blocks, g.offs, g.nseg, g.rows, splits, (int)tx,
       (int)ty, c, ldc, c_split);
   return hipGetLastError();
 }
 
-template <int FN, bool OB>
+template <int F, bool OB>
 hipError_t gemm_f8_mode(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
                         hipStream_t st) {
   switch (g.mode) {
-    case kF8RowSegs: return gemm_f8_t<FN, OB, kF8RowSegs>(g, splits, c, ldc, c_split, st);
-    case kF8BlockSegs: return gemm_f8_t<FN, OB, kF8BlockSegs>(g, splits, c, ldc, c_split, st);
-    default: return gemm_f8_t<FN, OB, kF8All>(g, splits, c, ldc, c_split, st);
+    case kF8RowSegs: return gemm_f8_t<F, OB, kF8RowSegs>(g, splits, c, ldc, c_split, st);
+    case kF8BlockSegs: return gemm_f8_t<F, OB, kF8BlockSegs>(g, splits, c, ldc, c_split, st);
+    default: return gemm_f8_t<F, OB, kF8All>(g, splits, c, ldc, c_split, st);
   }
 }
 
-hipError_t gemm_f8(const Fp8Gemm& g, int fn, bool bf16, int splits, void* c, int64_t ldc,
+hipError_t gemm_f8(const Fp8Gemm& g, const Fp8Plan& p, bool bf16, void* c, int64_t ldc,
                    int64_t c_split, hipStream_t st) {
-  if (bf16)
-    return fn == 4 ? gemm_f8_mode<4, true>(g, splits, c, ldc, c_split, st)
-                   : gemm_f8_mode<2, true>(g, splits, c, ldc, c_split, st);
-  return fn == 4 ? gemm_f8_mode<4, false>(g, splits, c, ldc, c_split, st)
-                 : gemm_f8_mode<2, false>(g, splits, c, ldc, c_split, st);
+  if (p.f == 2)
+    return bf16 ? gemm_f8_mode<2, true>(g, p.splits, c, ldc, c_split, st)
+                : gemm_f8_mode<2, false>(g, p.splits, c, ldc, c_split, st);
+  return bf16 ? gemm_f8_mode<4, true>(g, p.splits, c, ldc, c_split, st)
+              : gemm_f8_mode<4, false>(g, p.splits, c, ldc, c_split, st);
 }
 
 template <int MF>
 hipError_t skinny_t(const Fp8Gemm& g, hipStream_t st) {
-  const dim3 grid((unsigned)((g.n + 15) / 16),
-                  (unsigned)chunk_upper_bound(g.m, g.offs ? g.nseg : 1, 16 * MF));
+  const dim3 grid((unsigned)((g.n + 15) / 16), (unsigned)((g.m + 16 * MF - 1) / (16 * MF)));
   if (g.c_bf16)
-    k_gemm_f8_skinny<MF, true><<<grid, 64 * kSkinnyWaves, 0, st>>>(
-        g.a, g.b, g.m, g.n, (int)g.k_blocks, g.offs, g.nseg, g.c, g.ldc);
+    k_gemm_f8_skinny<MF, true><<<grid, 64 * kSkinnyWaves, 0, st>>>(g.a, g.b, g.m, g.n,
+                                                                   (int)g.k_blocks, g.c, g.ldc);
   else
-    k_gemm_f8_skinny<MF, false><<<grid, 64 * kSkinnyWaves, 0, st>>>(
-        g.a, g.b, g.m, g.n, (int)g.k_blocks, g.offs, g.nseg, g.c, g.ldc);
+    k_gemm_f8_skinny<MF, false><<<grid, 64 * kSkinnyWaves, 0, st>>>(g.a, g.b, g.m, g.n,
+                                                                    (int)g.k_blocks, g.c, g.ldc);
   return hipGetLastError();
 }
 
@@ -803,7 +841,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
   if (p.skinny == 2) return skinny_t<2>(g, st);
   if (p.skinny == 4) return skinny_t<4>(g, st);
   if (p.splits > 1) {
-    const hipError_t e = gemm_f8(g, p.fn, false, p.splits, ws, g.n, g.m * g.n, st);
+    const hipError_t e = gemm_f8(g, p, false, ws, g.n, g.m * g.n, st);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)((g.m * g.n + 1023) / 1024));
     if (g.c_bf16)
@@ -812,7 +850,7 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
       k_f8_reduce<false><<<grid, 256, 0, st>>>(static_cast<const float*>(ws), p.splits, g.m, g.n, g.c, g.ldc);
     return hipGetLastError();
   }
-  return gemm_f8(g, p.fn, g.c_bf16, 1, g.c, g.ldc, g.mode == kF8BlockSegs ? g.m * g.ldc : 0, st);
+  return gemm_f8(g, p, g.c_bf16, g.c, g.ldc, g.mode == kF8BlockSegs ? g.m * g.ldc : 0, st);
 }
 
 }  // namespace averis

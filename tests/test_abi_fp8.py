@@ -88,9 +88,9 @@ def test_gemm_rejections(L):
     assert g(dt=3) == 3
     assert g(ldc=95) == 2
     assert g(ws=P + 16) == 4
-    big = dict(a=f8(300, 1 << 14), b=f8(96, 1 << 14))
-    need = av.workspace_bytes(av.OP_FP8_GEMM, 300, 1 << 14, 96)
-    assert need >= 2 * 300 * 96 * 4                        # the contraction is split
+    big = dict(a=f8(1024, 1 << 14), b=f8(1024, 1 << 14), ldc=1024)
+    need = av.workspace_bytes(av.OP_FP8_GEMM, 1024, 1 << 14, 1024)
+    assert need >= 2 * 1024 * 1024 * 4                     # the contraction is split
     assert g(ws=None, **big) == 5
     assert g(wsb=need - 1, **big) == 5
 
@@ -110,8 +110,8 @@ def test_wgrad_rejections(L):
     assert g(dt=8) == 3
     assert g(ld=95) == 2
     assert g(ws=P + 8) == 4
-    need = av.workspace_bytes(av.OP_FP8_WGRAD, 200, 1 << 14, 96)
-    big = dict(x=f8(200, 1 << 14), d=f8(96, 1 << 14), rows=1 << 14)
+    need = av.workspace_bytes(av.OP_FP8_WGRAD, 1024, 1 << 14, 1024)
+    big = dict(x=f8(1024, 1 << 14), d=f8(1024, 1 << 14), rows=1 << 14, ld=1024)
     assert need > 0 and g(wsb=need - 1, **big) == 5
 
 
