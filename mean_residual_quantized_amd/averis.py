@@ -195,7 +195,18 @@ def _dtype_code(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle: torch.cuda.current_stream() builds an object around it
+    # (2.9 us against 0.2 us, as much as a launch)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _stream_on(t):
+    """The current stream, for a call on tensors that are where t is: t must be
+    on the current GPU."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("expected tensors on the current GPU, got %s" % t.device)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _workspace(nbytes, device):
@@ -607,23 +618,26 @@ def _like(t, ref, dtype, what, shape=None):
     """t, checked to be a contiguous tensor of `dtype` (and shape) on ref's device."""
     if t.dtype != dtype or not t.is_contiguous() or t.device != ref.device:
         raise ValueError("%s: expected a contiguous %s tensor on %s" % (what, dtype, ref.device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, shape, tuple(t.shape)))
     return t
 
 
 def _matrix(t, ref, what, shape=None):
     """Row stride of t, checked to be a 2-D tensor of ref's type (and shape) with unit column
     stride on ref's device."""
-    if t.dim() != 2 or t.dtype != ref.dtype or t.device != ref.device:
+    sh = t.shape
+    if len(sh) != 2 or (t is not ref and (t.dtype != ref.dtype or t.device != ref.device)):
         raise ValueError("%s: expected a 2-D %s tensor on %s" % (what, ref.dtype, ref.device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
-    if t.numel() == 0:
-        return max(t.shape[1], 1)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if shape is not None and sh != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, shape, tuple(sh)))
+    rows, cols = sh
+    if rows == 0 or cols == 0:
+        return max(cols, 1)
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError("%s: expected unit column stride" % what)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return ld if rows > 1 else max(ld, cols)
 
 
 def averis_moe_route(logits, topk, renorm=True):
@@ -636,7 +650,7 @@ def averis_moe_route(logits, topk, renorm=True):
     weights = torch.empty((tokens, topk), dtype=torch.float32, device=logits.device)
     _check("averis_moe_route", lib().averis_moe_route(
         logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, topk, int(bool(renorm)),
-        ids.data_ptr(), weights.data_ptr(), _stream()))
+        ids.data_ptr(), weights.data_ptr(), _stream_on(logits)))
     return ids, weights
 
 
@@ -655,7 +669,7 @@ def averis_moe_route_grad(logits, ids, dweights, renorm=True, out=None):
     ldd = _matrix(out, logits, "out", (tokens, experts))
     _check("averis_moe_route_grad", lib().averis_moe_route_grad(
         logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, topk, int(bool(renorm)),
-        ids.data_ptr(), dweights.data_ptr(), out.data_ptr(), ldd, _stream()))
+        ids.data_ptr(), dweights.data_ptr(), out.data_ptr(), ldd, _stream_on(logits)))
     return out
 
 
@@ -677,7 +691,8 @@ def averis_moe_sort(ids, experts, ws=None):
         ws = _workspace(need, dev)
     _check("averis_moe_sort", lib().averis_moe_sort(
         ids.data_ptr(), tokens, topk, experts, offsets.data_ptr(), pos.data_ptr(), src.data_ptr(),
-        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0, _stream()))
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _stream_on(ids)))
     return offsets, pos, src
 
 
@@ -699,7 +714,7 @@ def averis_moe_dispatch(x, pos, out=None):
     ldr = _matrix(out, x, "out", (tokens * topk, cols))
     _check("averis_moe_dispatch", lib().averis_moe_dispatch(
         x.data_ptr(), _dtype_code(x), tokens, cols, ldx, pos.data_ptr(), topk, out.data_ptr(), ldr,
-        _stream()))
+        _stream_on(x)))
     return out
 
 
@@ -715,7 +730,8 @@ def averis_moe_combine(rows, pos, weights=None, out=None):
     ldy = _matrix(out, rows, "out", (tokens, cols))
     _check("averis_moe_combine", lib().averis_moe_combine(
         rows.data_ptr(), _dtype_code(rows), tokens, cols, ldr, pos.data_ptr(),
-        weights.data_ptr() if weights is not None else None, topk, out.data_ptr(), ldy, _stream()))
+        weights.data_ptr() if weights is not None else None, topk, out.data_ptr(), ldy,
+        _stream_on(rows)))
     return out
 
 
@@ -732,7 +748,7 @@ def averis_moe_combine_grad(dy, rows, pos, weights, out=None):
     dweights = torch.empty((tokens, topk), dtype=torch.float32, device=dy.device)
     _check("averis_moe_combine_grad", lib().averis_moe_combine_grad(
         dy.data_ptr(), _dtype_code(dy), tokens, cols, ldy, rows.data_ptr(), ldr, pos.data_ptr(),
-        weights.data_ptr(), topk, out.data_ptr(), lddr, dweights.data_ptr(), _stream()))
+        weights.data_ptr(), topk, out.data_ptr(), lddr, dweights.data_ptr(), _stream_on(dy)))
     return out, dweights
 
 
@@ -740,15 +756,24 @@ def averis_moe_combine_grad(dy, rows, pos, weights, out=None):
 # linears in block-scaled fp8
 # --------------------------------------------------------------------------
 
-@dataclass
 class FP8:
     """Device fp8 tensor with one power-of-two scale for 128 elements along the
     columns: codes u8[rows, cols rounded up to 128] (E4M3, zero past cols),
     scales u8[rows, ceil(cols / 128) rounded up to 4] (E8M0)."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    rows: int
-    cols: int
+    __slots__ = ("codes", "scales", "rows", "cols", "c")
+
+    def __init__(self, codes, scales, rows, cols):
+        pitch, spitch = FP8.pitches(cols)
+        if codes.shape != (rows, pitch) or scales.shape != (rows, spitch):
+            raise ValueError("expected codes %s and scales %s" % ((rows, pitch), (rows, spitch)))
+        if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8
+                or not codes.is_contiguous() or not scales.is_contiguous()):
+            raise ValueError("expected contiguous uint8 codes and scales")
+        self._set(codes, scales, rows, cols)
+
+    def _set(self, codes, scales, rows, cols):
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.c = _FP8(codes.data_ptr(), scales.data_ptr(), rows, cols)   # the C descriptor
 
     @staticmethod
     def pitches(cols):
@@ -758,17 +783,10 @@ class FP8:
     @staticmethod
     def empty(rows, cols, device="cuda"):
         p, s = FP8.pitches(cols)
-        return FP8(torch.empty((rows, p), dtype=torch.uint8, device=device),
-                   torch.empty((rows, s), dtype=torch.uint8, device=device), rows, cols)
-
-    def c(self):
-        p, s = FP8.pitches(self.cols)
-        if (tuple(self.codes.shape) != (self.rows, p) or tuple(self.scales.shape) != (self.rows, s)
-                or self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8
-                or not self.codes.is_contiguous() or not self.scales.is_contiguous()):
-            raise ValueError("expected contiguous uint8 codes %s and scales %s"
-                             % ((self.rows, p), (self.rows, s)))
-        return _FP8(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+        q = FP8.__new__(FP8)
+        q._set(torch.empty((rows, p), dtype=torch.uint8, device=device),
+               torch.empty((rows, s), dtype=torch.uint8, device=device), rows, cols)
+        return q
 
 
 def _segments(offsets, ref):
@@ -795,8 +813,7 @@ def averis_fp8_quant(a, transposed=False, offsets=None, plain=True):
         qt = FP8.empty(cols, tc, a.device)
     _check("averis_fp8_quant", lib().averis_fp8_quant(
         a.data_ptr(), _dtype_code(a), rows, cols, lda, offs, nseg,
-        ctypes.byref(q.c()) if q is not None else None,
-        ctypes.byref(qt.c()) if qt is not None else None, _stream()))
+        q.c if q is not None else None, qt.c if qt is not None else None, _stream_on(a)))
     return (q, qt) if transposed else q
 
 
@@ -812,8 +829,15 @@ def averis_fp8_quant_weight(w):
     wt = FP8.empty(batch * cols, rows, w.device)
     _check("averis_fp8_quant_weight", lib().averis_fp8_quant_weight(
         a.data_ptr(), _dtype_code(a), batch, rows, cols, a.stride(1), a.stride(0),
-        ctypes.byref(wd.c()), ctypes.byref(wt.c()), _stream()))
+        wd.c, wt.c, _stream_on(w)))
     return wt, wd
+
+
+def _one_device(a, b):
+    dev = a.codes.device
+    if b.codes.device != dev:
+        raise ValueError("expected operands on one device")
+    return dev
 
 
 def _fp8_product(ws, op, dims, dev):
@@ -827,15 +851,16 @@ def _fp8_product(ws, op, dims, dev):
 def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=None):
     """c = deq(a) deq(b)^T; with offsets the rows of segment s times the s-th
     of the matrices stacked in b."""
-    dev = a.codes.device
+    dev = _one_device(a, b)
     offs, nseg = _segments(offsets, a.codes)
     m, k, n = a.rows, a.cols, b.rows // nseg
     c = _out(m, n, out_dtype, dev, out)
-    ldc = _matrix(c, c, "out", (m, n))
+    ldc = n if out is None else _matrix(c, c, "out", (m, n))
+    if c.device != dev:
+        raise ValueError("out: expected a tensor on %s" % dev)
     wp, wn = _fp8_product(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm", lib().averis_fp8_gemm(
-        ctypes.byref(a.c()), ctypes.byref(b.c()), offs, nseg, c.data_ptr(), _dtype_code(c), ldc,
-        wp, wn, _stream()))
+        a.c, b.c, offs, nseg, c.data_ptr(), _dtype_code(c), ldc, wp, wn, _stream_on(c)))
     return c
 
 
@@ -845,7 +870,7 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
     transposed copies; with the offsets of the quantization and its number of
     rows (by default the largest that the copies can hold) one matrix a
     segment (nseg x m x n)."""
-    dev = xt.codes.device
+    dev = _one_device(xt, dt)
     offs, nseg = _segments(offsets, xt.codes)
     m, n = xt.rows, dt.rows
     if rows is None:
@@ -853,12 +878,11 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
         rows = xt.cols - (128 * nseg if offsets is not None and nseg > 1 else 0)
     shape = (m, n) if offsets is None else (nseg, m, n)
     c = out if out is not None else torch.empty(shape, dtype=out_dtype, device=dev)
-    if tuple(c.shape) != shape or not c.is_contiguous():
-        raise ValueError("out: expected a contiguous tensor of shape %s" % (shape,))
+    if out is not None and (c.shape != shape or not c.is_contiguous() or c.device != dev):
+        raise ValueError("out: expected a contiguous tensor of shape %s on %s" % (shape, dev))
     wp, wn = _fp8_product(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm_wgrad", lib().averis_fp8_gemm_wgrad(
-        ctypes.byref(xt.c()), ctypes.byref(dt.c()), rows, offs, nseg, c.data_ptr(),
-        _dtype_code(c), n, wp, wn, _stream()))
+        xt.c, dt.c, rows, offs, nseg, c.data_ptr(), _dtype_code(c), n, wp, wn, _stream_on(c)))
     return c
 
 
@@ -867,30 +891,36 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
 # --------------------------------------------------------------------------
 
 def _grad_list(grads, out):
-    n = len(grads)
-    arr = (_Grad * n)()
+    """The C descriptors (averis_grad_t, four 8-byte words each) of the list."""
+    dev = grads[0].device if len(grads) else None
+    words = []
     for i, g in enumerate(grads):
-        o = g if out is None else out[i]
-        if not g.is_contiguous() or not o.is_contiguous():
-            raise ValueError("expected contiguous gradients and outputs")
-        if o is not g and (o.dtype != g.dtype or o.numel() != g.numel() or o.device != g.device):
-            raise ValueError("out[%d]: expected the gradient's type, size and device" % i)
-        if g.device != grads[0].device:
-            raise ValueError("expected gradients on one device")
-        arr[i] = _Grad(g.data_ptr(), o.data_ptr(), g.numel(), _dtype_code(g))
-    return arr
+        n, o = g.numel(), g
+        if out is not None:
+            o = out[i]
+            if o.dtype != g.dtype or o.numel() != n or o.device != dev or not o.is_contiguous():
+                raise ValueError("out[%d]: expected a contiguous tensor of the gradient's type, "
+                                 "size and device" % i)
+        if g.device != dev or not g.is_contiguous():
+            raise ValueError("expected contiguous gradients on one device")
+        words += (g.data_ptr(), o.data_ptr(), n, _dtype_code(g))
+    return (ctypes.c_uint64 * len(words))(*words)
+
+
+def _grad_call(grads, out, ws):
+    arr = _grad_list(grads, out)
+    dev = grads[0].device if len(grads) else "cuda"
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws = ws if ws is not None else _workspace(workspace_bytes(OP_GRAD_NORM, 0, 0, len(grads)), dev)
+    return arr, norm, ws
 
 
 def averis_grad_norm(grads, ws=None):
     """The 2-norm over every element of the tensors in the list (a float32
     tensor of no dimensions, on their device)."""
-    arr = _grad_list(grads, None)
-    dev = grads[0].device if len(grads) else "cuda"
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else _workspace(workspace_bytes(OP_GRAD_NORM, 0, 0, len(grads)), dev)
+    arr, norm, ws = _grad_call(grads, None, ws)
     _check("averis_grad_norm", lib().averis_grad_norm(
-        len(grads), ctypes.cast(arr, ctypes.c_void_p), norm.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream()))
+        len(grads), arr, norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(norm)))
     return norm
 
 
@@ -899,11 +929,8 @@ def averis_grad_clip(grads, max_norm, eps=1e-6, out=None, ws=None):
     the tensors of the list out; returns the norm as averis_grad_norm does."""
     if out is not None and len(out) != len(grads):
         raise ValueError("out: expected %d tensors" % len(grads))
-    arr = _grad_list(grads, out)
-    dev = grads[0].device if len(grads) else "cuda"
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else _workspace(workspace_bytes(OP_GRAD_NORM, 0, 0, len(grads)), dev)
+    arr, norm, ws = _grad_call(grads, out, ws)
     _check("averis_grad_clip", lib().averis_grad_clip(
-        len(grads), ctypes.cast(arr, ctypes.c_void_p), max_norm, eps, norm.data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream()))
+        len(grads), arr, max_norm, eps, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream_on(norm)))
     return norm

@@ -120,10 +120,14 @@ def test_binding_checks_tensors():
     q = av.FP8.empty(4, 200, "cpu")
     assert q.codes.shape == (4, 256) and q.scales.shape == (4, 4)
     with pytest.raises(ValueError):
-        av.FP8(q.codes[:, :200], q.scales, 4, 200).c()
+        av.FP8(q.codes[:, :200], q.scales, 4, 200)
     with pytest.raises(ValueError):
-        av.FP8(q.codes, q.scales[:2], 4, 200).c()
+        av.FP8(q.codes, q.scales[:2], 4, 200)
     with pytest.raises(ValueError):
+        av.FP8(q.codes.int(), q.scales, 4, 200)
+    with pytest.raises(ValueError, match="current GPU"):
+        av.averis_fp8_quant(a)                             # host memory
+    with pytest.raises(ValueError, match="column stride"):
         av.averis_fp8_quant(a.t())
     with pytest.raises(ValueError):
         av.averis_fp8_quant(a, transposed=True, offsets=torch.zeros(3, dtype=torch.int32))

@@ -170,6 +170,13 @@ def test_binding_checks_tensors():
         av.averis_moe_combine_grad(torch.zeros(4, 16).bfloat16(), rows, pos, w)
     with pytest.raises(TypeError):
         av.averis_moe_route(l.double(), 2)
+    for call in (lambda: av.averis_moe_route(l, 2), lambda: av.averis_moe_route_grad(l, ids, w),
+                 lambda: av.averis_moe_sort(ids, 8), lambda: av.averis_moe_dispatch(rows[:4], pos),
+                 lambda: av.averis_moe_combine(rows, pos),
+                 lambda: av.averis_moe_combine_grad(rows[:4], rows, pos, w),
+                 lambda: av.averis_grad_clip([l], 1.0), lambda: av.averis_grad_norm([l])):
+        with pytest.raises(ValueError, match="current GPU"):   # host memory
+            call()
     with pytest.raises(ValueError):
         av.averis_grad_clip([l, l.t()], 1.0)
     with pytest.raises(ValueError):
