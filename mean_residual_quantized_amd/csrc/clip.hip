@@ -5,13 +5,19 @@
 //
 // Both passes walk the same 32 KiB chunks of the listed tensors.  A launch
 // takes a table of up to kClipTensors tensors by value (nothing is copied to
-// the device first); a workgroup finds its chunk's tensor by a binary search
-// of the chunks' prefix counts.  The first pass leaves one fp64 partial per
-// workgroup; every workgroup of the second sums all the partials itself, in
-// the same fixed order, so there is no launch between the two, no atomic, and
-// the same bits on every call.  Squares and sums are fp64: exact squares, and
-// no overflow for any finite gradient.
+// the device first); a workgroup finds its next chunk's tensor from its last
+// one's.  The first pass leaves one fp64 partial per workgroup; every workgroup
+// of the second sums all the partials itself, in the same fixed order, so there
+// is no launch between the two, no atomic, and the same bits on every call.
+// Squares and sums are fp64: exact squares, and no overflow for any finite
+// gradient.
+//
+// Both are bound by memory: the first reads every gradient, with the next
+// chunk's loads in flight while a chunk is squared; the second reads and writes
+// them, last chunk first, so that what the first pass read last is taken from
+// the last-level cache.
 #include <hip/hip_runtime.h>
+#include <alloca.h>
 #include <stdint.h>
 
 #include "device_common.hpp"
@@ -25,7 +31,7 @@ constexpr int kClipTensors = 128;          // tensors of one launch
 constexpr int64_t kClipBytes = 32768;      // bytes of a chunk
 constexpr int kClipThreads = 256;
 constexpr int kClipPieces = (int)(kClipBytes / 16 / kClipThreads);   // 16-byte pieces a thread takes
-constexpr int kClipBlocks = 1024;          // workgroups (and partials) of one launch, at most
+constexpr int kClipBlocks = 2048;          // workgroups (and partials) of one launch, at most
 
 struct ClipTable {
   const void* g[kClipTensors];
@@ -40,15 +46,60 @@ static_assert(sizeof(ClipTable) + 64 <= 4096, "passed by value");
 // 16 bytes at element alignment
 typedef u32x4_t piece_t __attribute__((aligned(2)));
 
-// tensor of chunk c
-__device__ __forceinline__ int tensor_of(const ClipTable& t, uint32_t c) {
-  int lo = 0, hi = t.count - 1;
+// tensor of chunk c, `from` the tensor of some chunk before it (after it, with
+// DOWN)
+template <bool DOWN>
+__device__ __forceinline__ int tensor_of(const ClipTable& t, uint32_t c, int from) {
+  // mostly the same tensor or a neighbour; else by bisection
+  if (DOWN ? t.first[from] <= c : c < t.first[from + 1]) return from;
+  int lo = DOWN ? 0 : from + 1, hi = DOWN ? from - 1 : t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (t.first[mid] <= c) lo = mid;
     else hi = mid - 1;
   }
   return lo;
+}
+
+// a chunk: its bytes
+struct Chunk {
+  const char* g;
+  char* out;
+  int bytes;
+  bool bf16;
+};
+__device__ __forceinline__ Chunk chunk_of(const ClipTable& t, uint32_t c, int i) {
+  Chunk k;
+  k.bf16 = t.bf16[i] != 0;
+  const int64_t at = (int64_t)(c - t.first[i]) * kClipBytes;
+  const int64_t left = t.n[i] * (k.bf16 ? 2 : 4) - at;
+  k.g = static_cast<const char*>(t.g[i]) + at;
+  k.out = static_cast<char*>(t.out[i]) + at;
+  k.bytes = (int)(left < kClipBytes ? left : kClipBytes);
+  return k;
+}
+// the thread's 16-byte pieces of a chunk, 0 past its end
+__device__ __forceinline__ void load_chunk(const Chunk& k, u32x4_t* v) {
+  if (k.bytes == kClipBytes) {
+    const char* g = k.g + threadIdx.x * 16;
+#pragma unroll
+    for (int i = 0; i < kClipPieces; ++i)
+      v[i] = *reinterpret_cast<const piece_t*>(g + i * (kClipThreads * 16));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kClipPieces; ++i) {
+    const int at = (i * kClipThreads + (int)threadIdx.x) * 16;
+    v[i] = u32x4_t{0u, 0u, 0u, 0u};
+    if (at + 16 <= k.bytes) {
+      v[i] = *reinterpret_cast<const piece_t*>(k.g + at);
+    } else if (at < k.bytes) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + 2 * j < k.bytes)
+          v[i][j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(k.g + at + 2 * j) << (16 * (j & 1));
+    }
+  }
 }
 
 __device__ __forceinline__ void add_square(double& s, float v) {
@@ -67,62 +118,57 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* g, int64_t n, double s) {
-  constexpr int P = 16 / (int)sizeof(T);
-  u32x4_t v[kClipPieces];
-#pragma unroll
-  for (int i = 0; i < kClipPieces; ++i) {
-    const int64_t e = ((int64_t)i * kClipThreads + threadIdx.x) * P;
-    v[i] = u32x4_t{0u, 0u, 0u, 0u};
-    if (e + P <= n) {
-      v[i] = *reinterpret_cast<const piece_t*>(g + e);
-    } else if (e < n) {
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        if (e + j < n) {
-          if constexpr (sizeof(T) == 2) v[i][j / 2] |= (uint32_t)g[e + j] << (16 * (j & 1));
-          else v[i][j] = __float_as_uint(g[e + j]);
-        }
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kClipPieces; ++i) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (sizeof(T) == 2) {
-        add_square(s, bf16_lo(v[i][j]));
-        add_square(s, bf16_hi(v[i][j]));
-      } else {
-        add_square(s, __uint_as_float(v[i][j]));
-      }
-    }
-  }
-  return s;
-}
-
 __global__ __launch_bounds__(kClipThreads) void k_square_sums(ClipTable t, double* __restrict__ part) {
   __shared__ double sh[4];
-  double s = 0.0;
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const int64_t per = kClipBytes >> (t.bf16[i] ? 1 : 2);
-    const int64_t e0 = (int64_t)(c - t.first[i]) * per;
-    const int64_t n = t.n[i] - e0 < per ? t.n[i] - e0 : per;
-    if (t.bf16[i])
-      s = chunk_squares(static_cast<const uint16_t*>(t.g[i]) + e0, n, s);
-    else
-      s = chunk_squares(static_cast<const float*>(t.g[i]) + e0, n, s);
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  uint32_t c = blockIdx.x;   // the grid has no more workgroups than chunks
+  int i = tensor_of<false>(t, c, 0);
+  Chunk k = chunk_of(t, c, i);
+  u32x4_t v[kClipPieces];
+  load_chunk(k, v);
+  while (true) {
+    const bool bf16 = k.bf16;
+    c += gridDim.x;
+    const bool more = c < t.first[t.count];
+    u32x4_t w[kClipPieces];
+    if (more) {
+      i = tensor_of<false>(t, c, i);
+      k = chunk_of(t, c, i);
+      load_chunk(k, w);
+    }
+    if (bf16) {
+#pragma unroll
+      for (int p = 0; p < kClipPieces; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          add_square(s[j], bf16_lo(v[p][j]));
+          add_square(s[j], bf16_hi(v[p][j]));
+        }
+    } else {
+#pragma unroll
+      for (int p = 0; p < kClipPieces; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) add_square(s[j], __uint_as_float(v[p][j]));
+    }
+    if (!more) break;
+#pragma unroll
+    for (int p = 0; p < kClipPieces; ++p) v[p] = w[p];
   }
-  s = block_sum(s, sh);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  const double r = block_sum((s[0] + s[1]) + (s[2] + s[3]), sh);
+  if (threadIdx.x == 0) part[blockIdx.x] = r;
 }
 
 __device__ __forceinline__ double norm_of(const double* part, int parts, double* sh) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kClipThreads) s += part[i];
-  return sqrt(block_sum(s, sh));
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  int i = threadIdx.x;
+  for (; i + 3 * kClipThreads < parts; i += 4 * kClipThreads) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s[u] += part[i + u * kClipThreads];
+  }
+#pragma unroll
+  for (int u = 0; u < 3; ++u)
+    if (i + u * kClipThreads < parts) s[u] += part[i + u * kClipThreads];
+  return sqrt(block_sum((s[0] + s[1]) + (s[2] + s[3]), sh));
 }
 
 __global__ __launch_bounds__(kClipThreads) void k_norm(const double* __restrict__ part, int parts,
@@ -132,51 +178,57 @@ __global__ __launch_bounds__(kClipThreads) void k_norm(const double* __restrict_
   if (threadIdx.x == 0) *norm = (float)r;
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* g, T* out, int64_t n, float coef) {
-  constexpr int P = 16 / (int)sizeof(T);
+__device__ __forceinline__ u32x4_t scaled(u32x4_t v, bool bf16, float coef) {
 #pragma unroll
-  for (int i = 0; i < kClipPieces; ++i) {
-    const int64_t e = ((int64_t)i * kClipThreads + threadIdx.x) * P;
-    if (e + P <= n) {
-      u32x4_t v = *reinterpret_cast<const piece_t*>(g + e);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (sizeof(T) == 2)
-          v[j] = bf16x2_rne(bf16_lo(v[j]) * coef, bf16_hi(v[j]) * coef);
-        else
-          v[j] = __float_as_uint(__uint_as_float(v[j]) * coef);
-      }
-      *reinterpret_cast<piece_t*>(out + e) = v;
-    } else {
-      for (int j = 0; j < P && e + j < n; ++j) {
-        if constexpr (sizeof(T) == 2)
-          out[e + j] = (uint16_t)bf16x2_rne(bf16_lo(g[e + j]) * coef, 0.0f);
-        else
-          out[e + j] = g[e + j] * coef;
-      }
-    }
-  }
+  for (int j = 0; j < 4; ++j)
+    v[j] = bf16 ? bf16x2_rne(bf16_lo(v[j]) * coef, bf16_hi(v[j]) * coef)
+                : __float_as_uint(__uint_as_float(v[j]) * coef);
+  return v;
 }
 
 __global__ __launch_bounds__(kClipThreads) void k_clip(ClipTable t, const double* __restrict__ part,
                                                        int parts, double max_norm, double eps,
                                                        float* __restrict__ norm) {
   __shared__ double sh[4];
+  // the first chunk is on its way while the partials are summed
+  int64_t c = (int64_t)t.first[t.count] - 1 - blockIdx.x;
+  int i = tensor_of<true>(t, (uint32_t)c, t.count - 1);
+  Chunk k = chunk_of(t, (uint32_t)c, i);
+  u32x4_t v[kClipPieces];
+  load_chunk(k, v);
   const double r = norm_of(part, parts, sh);
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
   const double c64 = max_norm / (r + eps);
   const float coef = c64 > 1.0 ? 1.0f : (float)c64;   // NaN stays NaN
-  for (uint32_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    if (coef == 1.0f && t.g[i] == t.out[i]) continue;   // in place and unchanged
-    const int64_t per = kClipBytes >> (t.bf16[i] ? 1 : 2);
-    const int64_t e0 = (int64_t)(c - t.first[i]) * per;
-    const int64_t n = t.n[i] - e0 < per ? t.n[i] - e0 : per;
-    if (t.bf16[i])
-      chunk_scale(static_cast<const uint16_t*>(t.g[i]) + e0, static_cast<uint16_t*>(t.out[i]) + e0, n, coef);
-    else
-      chunk_scale(static_cast<const float*>(t.g[i]) + e0, static_cast<float*>(t.out[i]) + e0, n, coef);
+  while (true) {
+    if (coef != 1.0f || k.g != k.out) {   // else in place and unchanged
+#pragma unroll
+      for (int p = 0; p < kClipPieces; ++p) v[p] = scaled(v[p], k.bf16, coef);
+      if (k.bytes == kClipBytes) {
+        char* o = k.out + threadIdx.x * 16;
+#pragma unroll
+        for (int p = 0; p < kClipPieces; ++p)
+          *reinterpret_cast<piece_t*>(o + p * (kClipThreads * 16)) = v[p];
+      } else {
+#pragma unroll
+        for (int p = 0; p < kClipPieces; ++p) {
+          const int at = (p * kClipThreads + (int)threadIdx.x) * 16;
+          if (at + 16 <= k.bytes) {
+            *reinterpret_cast<piece_t*>(k.out + at) = v[p];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (at + 2 * j < k.bytes)
+                *reinterpret_cast<uint16_t*>(k.out + at + 2 * j) = (uint16_t)(v[p][j / 2] >> (16 * (j & 1)));
+          }
+        }
+      }
+    }
+    c -= gridDim.x;
+    if (c < 0) break;
+    i = tensor_of<true>(t, (uint32_t)c, i);
+    k = chunk_of(t, (uint32_t)c, i);
+    if (coef != 1.0f || k.g != k.out) load_chunk(k, v);
   }
 }
 
@@ -215,11 +267,14 @@ size_t grad_norm_ws_bytes(int n) {
 hipError_t launch_grad_clip(int n, const GradTensor* w, bool scale, double max_norm, double eps,
                             float* norm, void* ws, hipStream_t st) {
   double* part = static_cast<double*>(ws);
-  int parts = 0;
+  int parts = 0, launches = 0;
+  int* begin = static_cast<int*>(alloca(((size_t)n / kClipTensors + 1) * sizeof(int)));
   ClipTable t;
   for (int i = 0; i < n;) {
+    const int from = i;
     i = fill_table(w, n, i, t);
     if (t.count == 0) break;
+    begin[launches++] = from;
     const unsigned g = clip_grid(t);
     k_square_sums<<<g, kClipThreads, 0, st>>>(t, part + parts);
     parts += (int)g;
@@ -228,9 +283,9 @@ hipError_t launch_grad_clip(int n, const GradTensor* w, bool scale, double max_n
     k_norm<<<1, kClipThreads, 0, st>>>(part, parts, norm);
     return hipGetLastError();
   }
-  for (int i = 0; i < n;) {
-    i = fill_table(w, n, i, t);
-    if (t.count == 0) break;
+  // the last launch's tensors first: what was read last
+  for (int l = launches - 1; l >= 0; --l) {
+    fill_table(w, n, begin[l], t);
     k_clip<<<clip_grid(t), kClipThreads, 0, st>>>(t, part, parts, max_norm, eps, norm);
     norm = nullptr;   // written once
   }
