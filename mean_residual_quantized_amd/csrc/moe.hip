@@ -133,48 +133,76 @@ __device__ __forceinline__ float group_fmax(float v) {
 }
 
 // ---------------------------------------------------------------------------
-// Router.  G lanes share a token, each with V consecutive logits.
+// Router.  G lanes share a token; a lane has V of its logits in pieces of Q
+// neighbours, dealt out lane by lane, so that a load of all the lanes takes
+// neighbouring bytes.
 // ---------------------------------------------------------------------------
 constexpr float kMasked = -__builtin_inff();
 
-template <typename T, int V>
-__device__ __forceinline__ void load_logits(const T* row, int e0, int experts, float* l) {
-  constexpr int P = Elem<T>::kPer;
-  if constexpr (V % P == 0) {
-    if (e0 + V <= experts) {
+template <typename T, int G, int V>
+struct Deal {
+  static constexpr int Q = V < Elem<T>::kPer ? V : Elem<T>::kPer;
+  // expert of the lane's v-th logit
+  static __device__ __forceinline__ int expert(int g, int v) { return (v / Q * G + g) * Q + v % Q; }
+  // the lane's v of expert e, V or more if it is another lane's
+  static __device__ __forceinline__ uint32_t place(int g, int e) {
+    const uint32_t u = (uint32_t)e, v = u / (Q * G) * Q + u % Q;
+    return u / Q % G == (uint32_t)g ? v : 0xFFFFu;
+  }
+};
+
+template <typename T, int G, int V>
+__device__ __forceinline__ void load_logits(const T* row, int g, int experts, float* l) {
+  using D = Deal<T, G, V>;
+  if constexpr (D::Q == Elem<T>::kPer) {
+    if (D::expert(G - 1, V - 1) < experts) {
 #pragma unroll
-      for (int v = 0; v < V; v += P)
-        Elem<T>::unpack(*reinterpret_cast<const piece_t*>(row + e0 + v), l + v);
+      for (int v = 0; v < V; v += D::Q)
+        Elem<T>::unpack(*reinterpret_cast<const piece_t*>(row + D::expert(g, v)), l + v);
       return;
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) l[v] = e0 + v < experts ? Elem<T>::f32(row[e0 + v]) : kMasked;
+  for (int v = 0; v < V; ++v) {
+    const int e = D::expert(g, v);
+    l[v] = e < experts ? Elem<T>::f32(row[e]) : kMasked;
+  }
 }
 
-// Top-k by k rounds of a group maximum.  A logit's key orders as its value
-// (NaN above +inf, -0 equal to +0); 0 stands for masked, absent and taken.
-// A round is a maximum of keys over the lane's V and the group, then the
-// smallest index that has it: ties go to the lowest expert.
+// A logit's key orders as its value (NaN above +inf, -0 equal to +0); 0 stands
+// for masked, absent and taken.  A bf16 value takes half of it, and the other
+// half holds the expert, the lowest on top.
+template <typename T>
+__device__ __forceinline__ uint32_t logit_key(float l, uint32_t e) {
+  uint32_t k = f32_ordered(l + 0.0f);
+  if (l != l) k = 0xFFFFFFFFu;
+  if constexpr (sizeof(T) == 2) k = (k & 0xFFFF0000u) | (0xFFFFu - e);
+  return l == kMasked ? 0u : k;
+}
+template <typename T>
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  if constexpr (sizeof(T) == 2) k = (k & 0x80000000u) ? k & 0xFFFF0000u : k | 0xFFFFu;
+  return f32_from_ordered(k);
+}
+
+// Top-k by k rounds of a group maximum over the lane's V and the group.  bf16:
+// the key names the expert.  fp32: the smallest expert that has the key.
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int64_t tokens,
                                                int experts, int64_t ld, int topk, int renorm,
                                                int32_t* __restrict__ ids,
                                                float* __restrict__ weights) {
   constexpr int KO = kMaxTopk > G ? kMaxTopk / G : 1;
+  using D = Deal<T, G, V>;
   const int g = threadIdx.x % G;
   const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
   const bool live = t < tokens;   // the others repeat the last token, unstored
   const T* row = logits + (live ? t : tokens - 1) * ld;
   float l[V];
-  load_logits<T, V>(row, g * V, experts, l);
+  load_logits<T, G, V>(row, g, experts, l);
   uint32_t key[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    key[v] = f32_ordered(l[v] + 0.0f);
-    if (l[v] != l[v]) key[v] = 0xFFFFFFFFu;
-    if (l[v] == kMasked) key[v] = 0u;
-  }
+  for (int v = 0; v < V; ++v) key[v] = logit_key<T>(l[v], (uint32_t)D::expert(g, v));
   float top = 0.0f;          // the largest logit
   float val[KO];
   int id[KO];
@@ -188,13 +216,21 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int
 #pragma unroll
       for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
       best = group_max<G>(best);
-      uint32_t at = 0xFFFFu;
+      uint32_t at;
+      if constexpr (sizeof(T) == 2) {
+        at = 0xFFFFu - (best & 0xFFFFu);
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v) at = key[v] == best ? (uint32_t)(g * V + v) : at;
-      at = group_min<G>(at);
+        for (int v = 0; v < V; ++v) key[v] = key[v] == best ? 0u : key[v];
+      } else {
+        at = 0xFFFFu;
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = at == (uint32_t)(g * V + v) ? 0u : key[v];
-      const float x = f32_from_ordered(best);
+        for (int v = V - 1; v >= 0; --v) at = key[v] == best ? (uint32_t)D::expert(g, v) : at;
+        at = group_min<G>(at);
+        const uint32_t mine = D::place(g, (int)at);
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = mine == (uint32_t)v ? 0u : key[v];
+      }
+      const float x = key_logit<T>(best);
       if (o == 0 && r == 0 && best != 0u) top = x;
       if (r == g && best != 0u) {
         val[o] = x;
@@ -234,23 +270,35 @@ __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tok
                                                     const int32_t* __restrict__ ids,
                                                     const float* __restrict__ dweights,
                                                     T* dlogits, int64_t ldd) {
+  using D = Deal<T, G, V>;
   const int g = threadIdx.x % G;
   const int64_t t = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
   const bool live = t < tokens;
   const int64_t tr = live ? t : tokens - 1;
   float l[V], s[V];
-  load_logits<T, V>(logits + tr * ld, g * V, experts, l);
+  load_logits<T, G, V>(logits + tr * ld, g, experts, l);
   uint32_t chosen = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v) s[v] = 0.0f;
-  for (int j = 0; j < topk; ++j) {
-    const int e = ids[tr * topk + j] - g * V;
-    const float d = dweights[tr * topk + j];
+  for (int j0 = 0; j0 < topk; j0 += 8) {   // eight slots' loads in flight
+    int e[8];
+    float d[8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (e == v) {
-        s[v] = d;
-        chosen |= 1u << v;
+    for (int u = 0; u < 8; ++u) {
+      e[u] = -1;
+      d[u] = 0.0f;
+      if (j0 + u < topk) {
+        e[u] = ids[tr * topk + j0 + u];
+        d[u] = dweights[tr * topk + j0 + u];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t mine = D::place(g, e[u]);
+      if (j0 + u < topk && e[u] >= 0) {
+        chosen |= mine < (uint32_t)V ? 1u << (mine & 31u) : 0u;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = mine == (uint32_t)v ? d[u] : s[v];
       }
     }
   }
@@ -270,28 +318,27 @@ __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tok
   total = group_sum<G>(total);
   mean = group_sum<G>(mean);
   if (total == 0.0f) total = 1.0f;
-  mean = mean / total;
+  const float inv = 1.0f / total;
+  mean *= inv;
   if (!live) return;
   float d[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const bool in = (chosen >> v) & 1u;
-    d[v] = (in || !renorm) ? l[v] / total * (s[v] - mean) : 0.0f;
+    d[v] = (in || !renorm) ? l[v] * inv * (s[v] - mean) : 0.0f;
   }
   T* out = dlogits + t * ldd;
-  constexpr int P = Elem<T>::kPer;
-  const int e0 = g * V;
-  if constexpr (V % P == 0) {
-    if (e0 + V <= experts) {
+  if constexpr (D::Q == Elem<T>::kPer) {
+    if (D::expert(G - 1, V - 1) < experts) {
 #pragma unroll
-      for (int v = 0; v < V; v += P)
-        *reinterpret_cast<piece_t*>(out + e0 + v) = Elem<T>::pack(d + v);
+      for (int v = 0; v < V; v += D::Q)
+        *reinterpret_cast<piece_t*>(out + D::expert(g, v)) = Elem<T>::pack(d + v);
       return;
     }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (e0 + v < experts) out[e0 + v] = Elem<T>::from(d[v]);
+    if (D::expert(g, v) < experts) out[D::expert(g, v)] = Elem<T>::from(d[v]);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,7 +348,6 @@ __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tok
 // then wavefronts, in order), then it ranks its slots 64 at a time by ballots
 // over the bucket's bits.  No step depends on the order of atomics.
 // ---------------------------------------------------------------------------
-constexpr int kSortSteps = 8;   // 64-slot steps of a wavefront
 
 __device__ __forceinline__ int bucket_of(int32_t id, int experts) {
   return (uint32_t)id < (uint32_t)experts ? id : experts;
@@ -333,34 +379,35 @@ __device__ __forceinline__ int block_exclusive(int v, int* sh, int& total) {
 }
 
 // the wavefront's slots (registers) and its counts, in cnt[wave][bucket]
-template <int WAVES>
+template <int WAVES, int STEPS>
 __device__ __forceinline__ void sort_count(const int32_t* ids, int64_t first, int64_t n,
                                            int experts, int* cnt, int* b) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nb = experts + 1;
-  const int64_t s0 = first + (int64_t)w * (64 * kSortSteps);
+  const int64_t s0 = first + (int64_t)w * (64 * STEPS);
 #pragma unroll
-  for (int i = 0; i < kSortSteps; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     const int64_t s = s0 + 64 * i + lane;
     b[i] = s < n ? bucket_of(ids[s], experts) : -1;
   }
   for (int i = threadIdx.x; i < WAVES * nb; i += 64 * WAVES) cnt[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSortSteps; ++i)
+  for (int i = 0; i < STEPS; ++i)
     if (b[i] >= 0) atomicAdd(&cnt[w * nb + b[i]], 1);
   __syncthreads();
 }
 
 // rows of the wavefront's slots from its first rows in cnt[wave][bucket]
+template <int STEPS>
 __device__ __forceinline__ void sort_place(int64_t first, int64_t n, int experts, int* cnt,
                                            const int* b, int32_t* pos, int32_t* src) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nb = experts + 1;
-  const int64_t s0 = first + (int64_t)w * (64 * kSortSteps);
+  const int64_t s0 = first + (int64_t)w * (64 * STEPS);
   const uint64_t below = (1ull << lane) - 1ull;
   const int bits = 32 - __builtin_clz(experts);   // buckets 0 .. experts
   volatile int* row0 = cnt + w * nb;
 #pragma unroll
-  for (int i = 0; i < kSortSteps; ++i) {
+  for (int i = 0; i < STEPS; ++i) {
     if (s0 + 64 * i >= n) break;
     const bool ok = b[i] >= 0;
     uint64_t same = __ballot(ok);
@@ -383,19 +430,19 @@ __device__ __forceinline__ void sort_place(int64_t first, int64_t n, int experts
   }
 }
 
-constexpr int kSortWavesOne = 16;    // one workgroup for everything
-constexpr int kSortWavesMany = 4;    // workgroups of a larger sort
-constexpr int64_t kSortOne = (int64_t)kSortWavesOne * 64 * kSortSteps;     // 8192 slots
-constexpr int64_t kSortChunk = (int64_t)kSortWavesMany * 64 * kSortSteps;  // 2048 slots
+constexpr int kSortWavesOne = 16, kSortStepsOne = 8;     // one workgroup for everything
+constexpr int kSortWavesMany = 4, kSortStepsMany = 4;    // workgroups of a larger sort
+constexpr int64_t kSortOne = (int64_t)kSortWavesOne * 64 * kSortStepsOne;       // 8192 slots
+constexpr int64_t kSortChunk = (int64_t)kSortWavesMany * 64 * kSortStepsMany;   // 1024 slots
 
 __global__ __launch_bounds__(64 * kSortWavesOne) void k_sort_one(
     const int32_t* __restrict__ ids, int n, int experts, int64_t* __restrict__ offsets,
     int32_t* __restrict__ pos, int32_t* __restrict__ src) {
   extern __shared__ int cnt[];   // [waves][experts + 1]
   __shared__ int sh[kSortWavesOne];
-  int b[kSortSteps];
+  int b[kSortStepsOne];
   const int nb = experts + 1;
-  sort_count<kSortWavesOne>(ids, 0, n, experts, cnt, b);
+  sort_count<kSortWavesOne, kSortStepsOne>(ids, 0, n, experts, cnt, b);
   // thread e: expert e (experts <= the block's threads); the tail after them
   const int e = threadIdx.x;
   int mine = 0;
@@ -419,15 +466,15 @@ __global__ __launch_bounds__(64 * kSortWavesOne) void k_sort_one(
     offsets[experts] = kept;
   }
   __syncthreads();
-  sort_place(0, n, experts, cnt, b, pos, src);
+  sort_place<kSortStepsOne>(0, n, experts, cnt, b, pos, src);
 }
 
 // counts of a chunk -> hist[bucket][chunk]
 __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_hist(
     const int32_t* __restrict__ ids, int64_t n, int experts, int chunks, int* __restrict__ hist) {
   extern __shared__ int cnt[];
-  int b[kSortSteps];
-  sort_count<kSortWavesMany>(ids, (int64_t)blockIdx.x * kSortChunk, n, experts, cnt, b);
+  int b[kSortStepsMany];
+  sort_count<kSortWavesMany, kSortStepsMany>(ids, (int64_t)blockIdx.x * kSortChunk, n, experts, cnt, b);
   const int nb = experts + 1;
   for (int e = threadIdx.x; e < nb; e += 64 * kSortWavesMany) {
     int c = 0;
@@ -436,41 +483,50 @@ __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_hist(
   }
 }
 
-// exclusive prefix sum of hist, bucket by bucket, in place; a bucket's first
-// value is its offset.  One workgroup, each thread a contiguous run.
-__global__ __launch_bounds__(1024) void k_sort_scan(int* __restrict__ hist, int experts, int chunks,
-                                                    int64_t* __restrict__ offsets) {
-  __shared__ int sh[16];
-  const int64_t len = (int64_t)(experts + 1) * chunks;
-  const int64_t per = (len + 1023) / 1024;
-  const int64_t i0 = per * threadIdx.x, i1 = i0 + per < len ? i0 + per : len;
-  int sum = 0;
-  for (int64_t i = i0; i < i1; ++i) sum += hist[i];
-  int total;
-  int run = block_exclusive<16>(sum, sh, total);
-  if (i0 >= i1) return;
-  int64_t next = (i0 + chunks - 1) / chunks * chunks;   // the next bucket's first place
-  for (int64_t i = i0; i < i1; ++i) {
-    const int c = hist[i];
-    hist[i] = run;
-    if (i == next) {
-      offsets[i / chunks] = run;
-      next += chunks;
+// a bucket's counts -> the slots of it in the chunks before, and all of them in
+// totals[bucket]: a wavefront a bucket, 64 chunks at a time
+__global__ __launch_bounds__(256) void k_sort_scan(int* __restrict__ hist, int experts, int chunks,
+                                                   int* __restrict__ totals) {
+  const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (e > experts) return;
+  int* row = hist + (int64_t)e * chunks;
+  int run = 0;
+  for (int c0 = 0; c0 < chunks; c0 += 64) {
+    const int c = c0 + lane, v = c < chunks ? row[c] : 0;
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += u;
     }
-    run += c;
+    if (c < chunks) row[c] = run + incl - v;
+    run += __shfl(incl, 63, 64);
   }
+  if (lane == 0) totals[e] = run;
 }
 
+// each workgroup sums the buckets' totals for itself: the offsets
 __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_place(
     const int32_t* __restrict__ ids, int64_t n, int experts, int chunks,
-    const int* __restrict__ hist, int32_t* __restrict__ pos, int32_t* __restrict__ src) {
+    const int* __restrict__ hist, const int* __restrict__ totals, int64_t* __restrict__ offsets,
+    int32_t* __restrict__ pos, int32_t* __restrict__ src) {
   extern __shared__ int cnt[];
-  int b[kSortSteps];
+  __shared__ int sh[kSortWavesMany];
+  constexpr int T = 64 * kSortWavesMany;
+  int b[kSortStepsMany];
   const int64_t first = (int64_t)blockIdx.x * kSortChunk;
-  sort_count<kSortWavesMany>(ids, first, n, experts, cnt, b);
+  sort_count<kSortWavesMany, kSortStepsMany>(ids, first, n, experts, cnt, b);
   const int nb = experts + 1;
-  for (int e = threadIdx.x; e < nb; e += 64 * kSortWavesMany) {
-    int run = hist[(int64_t)e * chunks + blockIdx.x];
+  int before = 0;   // rows of the buckets of earlier rounds
+  for (int e0 = 0; e0 < nb; e0 += T) {
+    const int e = e0 + threadIdx.x;
+    int all;
+    const int mine = e < nb ? totals[e] : 0;
+    const int start = before + block_exclusive<kSortWavesMany>(mine, sh, all);
+    before += all;
+    if (e >= nb) continue;
+    if (blockIdx.x == 0) offsets[e] = start;   // offsets[experts]: the tail's first row
+    int run = start + hist[(int64_t)e * chunks + blockIdx.x];
     for (int w = 0; w < kSortWavesMany; ++w) {
       const int c = cnt[w * nb + e];
       cnt[w * nb + e] = run;
@@ -478,7 +534,7 @@ __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_place(
     }
   }
   __syncthreads();
-  sort_place(first, n, experts, cnt, b, pos, src);
+  sort_place<kSortStepsMany>(first, n, experts, cnt, b, pos, src);
 }
 
 __global__ void k_zero_offsets(int64_t* offsets, int count) {
@@ -620,11 +676,11 @@ dim3 exchange_block(int64_t cols, int per) {
   } else if (experts <= 64) {          \
     CALL(8, 8);                        \
   } else if (experts <= 128) {         \
-    CALL(16, 8);                       \
+    CALL(8, 16);                       \
   } else if (experts <= 256) {         \
-    CALL(32, 8);                       \
+    CALL(16, 16);                      \
   } else if (experts <= 512) {         \
-    CALL(64, 8);                       \
+    CALL(32, 16);                      \
   } else {                             \
     CALL(64, 16);                      \
   }
@@ -680,7 +736,8 @@ static int64_t sort_chunks(int64_t slots) { return (slots + kSortChunk - 1) / kS
 
 size_t moe_sort_ws_bytes(int64_t slots, int experts) {
   if (slots <= kSortOne) return 0;
-  return ((size_t)sort_chunks(slots) * (size_t)(experts + 1) * 4 + 255) & ~(size_t)255;
+  // counts [bucket][chunk], totals [bucket]
+  return (((size_t)sort_chunks(slots) + 1) * (size_t)(experts + 1) * 4 + 255) & ~(size_t)255;
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t slots, int experts, int64_t* offsets,
@@ -700,9 +757,10 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t slots, int experts, int64
   const size_t lds = (size_t)kSortWavesMany * (experts + 1) * 4;
   int* hist = static_cast<int*>(ws);
   k_sort_hist<<<chunks, 64 * kSortWavesMany, lds, st>>>(ids, slots, experts, chunks, hist);
-  k_sort_scan<<<1, 1024, 0, st>>>(hist, experts, chunks, offsets);
-  k_sort_place<<<chunks, 64 * kSortWavesMany, lds, st>>>(ids, slots, experts, chunks, hist, pos,
-                                                         src);
+  int* totals = hist + (int64_t)(experts + 1) * chunks;
+  k_sort_scan<<<dim3((unsigned)((experts + 4) / 4)), 256, 0, st>>>(hist, experts, chunks, totals);
+  k_sort_place<<<chunks, 64 * kSortWavesMany, lds, st>>>(ids, slots, experts, chunks, hist, totals,
+                                                         offsets, pos, src);
   return hipGetLastError();
 }
 
