@@ -225,6 +225,86 @@ def test_gemm_segments(offs, k, n):
         assert (got[offs[-1]:] == 7).all()
 
 
+@pytest.mark.parametrize("nseg", [64, 65, 200, 1024])
+def test_many_segments(nseg):
+    """More segments than a wavefront has lanes, many of them empty."""
+    rng = np.random.default_rng([nseg, 8])
+    rows, m, n = 3 * nseg, 72, 40
+    cuts = np.sort(rng.integers(0, rows + 1, nseg - 1))
+    offs = [0] + [int(v) for v in cuts] + [rows]
+    o = torch.tensor(offs, dtype=torch.int64, device="cuda")
+    x, d = (torch.from_numpy(rng.integers(-4, 5, (rows, c)).astype(np.float32)).cuda().to(BF16) for c in (m, n))
+    w = torch.from_numpy(rng.integers(-4, 5, (nseg, m, n)).astype(np.float32)).cuda().to(BF16)
+    xq, xt = av.averis_fp8_quant(x, transposed=True, offsets=o)
+    _, dt = av.averis_fp8_quant(d, transposed=True, offsets=o)
+    wt, _ = av.averis_fp8_quant_weight(w)
+    y = av.averis_fp8_gemm(xq, wt, F32, offsets=o)
+    g = av.averis_fp8_gemm_wgrad(xt, dt, F32, offsets=o)
+    xn, dn, wn = (t.double().cpu().numpy() for t in (x, d, w))
+    seg = np.searchsorted(np.array(offs[1:]), np.arange(rows), side="right")
+    np.testing.assert_array_equal(y.cpu().numpy(), np.einsum("ri,rio->ro", xn, wn[seg]))
+    np.testing.assert_array_equal(
+        g.cpu().numpy(), np.stack([xn[a:b].T @ dn[a:b] for a, b in zip(offs, offs[1:])]))
+
+
+# Sizes for the 256 x 256 tile: one tile a workgroup, several (the next one's
+# loads under the output), and K cut into fp32 partial sums.  The products are
+# of small integers, and the reference is theirs in float64.
+LARGE = [(3001, 3003, 3790), (12001, 2203, 800), (1001, 3003, 16300)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE)
+def test_large_products_are_exact(m, n, k):
+    rng = np.random.default_rng([m, n, k, 2])
+    a, va = exact_fp8(rng, m, k)
+    b, vb = exact_fp8(rng, n, k)
+    ref = torch.from_numpy(va).cuda() @ torch.from_numpy(vb).cuda().t()
+    for dt in (F32, BF16):
+        c = av.averis_fp8_gemm(a, b, dt)
+        assert torch.equal(c, ref.to(dt))
+        buf = torch.full((m + 2, n + 5), 9.0, dtype=dt, device="cuda")   # rows that start anywhere
+        av.averis_fp8_gemm(a, b, dt, out=buf[1:1 + m, 3:3 + n])
+        assert torch.equal(buf[1:1 + m, 3:3 + n], c)
+        buf[1:1 + m, 3:3 + n] = 9.0
+        assert (buf == 9).all()
+        a2 = av.averis_fp8_gemm(a, b, dt, out=torch.empty(m, n + 8, dtype=dt, device="cuda")[:, :n])
+        assert torch.equal(a2, c)                                        # whole 16-byte pieces
+
+
+@pytest.mark.parametrize("offs", [[0, 1, 1, 2500, 2756, 8000, 9000], [0, 0, 9000, 9000, 9000, 9000, 9000],
+                                  [0, 300, 556, 556, 557, 4000, 8900]])
+def test_large_row_segments_are_exact(offs):
+    rng = np.random.default_rng(offs)
+    nseg, rows, n, k = len(offs) - 1, 9000, 2103, 2100
+    a, va = exact_fp8(rng, rows, k)
+    b, vb = exact_fp8(rng, nseg * n, k)
+    va, vb = torch.from_numpy(va).cuda(), torch.from_numpy(vb).cuda()
+    ref = torch.full((rows, n), 7.0, dtype=torch.float64, device="cuda")
+    for s in range(nseg):
+        if offs[s] < offs[s + 1]:
+            ref[offs[s]:offs[s + 1]] = va[offs[s]:offs[s + 1]] @ vb[s * n:(s + 1) * n].t()
+    o = torch.tensor(offs, dtype=torch.int64, device="cuda")
+    for dt in (F32, BF16):
+        c = torch.full((rows, n), 7.0, dtype=dt, device="cuda")
+        av.averis_fp8_gemm(a, b, dt, offsets=o, out=c)
+        assert torch.equal(c, ref.to(dt))
+
+
+@pytest.mark.parametrize("offs", [[0, 4000, 4000, 4129, 9400], [0, 0, 0, 9400, 9400], [0, 2048, 4700, 7000, 9300]])
+def test_large_wgrad_segments_are_exact(offs):
+    rng = np.random.default_rng(offs)
+    rows, m, n, nseg = 9400, 2101, 2055, len(offs) - 1
+    x, d = (torch.from_numpy(rng.integers(-4, 5, (rows, c)).astype(np.float32)).cuda().to(BF16) for c in (m, n))
+    o = torch.tensor(offs, dtype=torch.int64, device="cuda")
+    _, xt = av.averis_fp8_quant(x, transposed=True, offsets=o, plain=False)
+    _, dt = av.averis_fp8_quant(d, transposed=True, offsets=o, plain=False)
+    for dtype in (F32, BF16):
+        w = av.averis_fp8_gemm_wgrad(xt, dt, dtype, offsets=o)
+        for s in range(nseg):
+            xs, ds = x[offs[s]:offs[s + 1]].double(), d[offs[s]:offs[s + 1]].double()
+            assert torch.equal(w[s], (xs.t() @ ds).to(dtype))
+
+
 @pytest.mark.parametrize("l,m,n", [(1, 16, 8), (300, 96, 200), (5000, 256, 300), (128, 1000, 64), (0, 20, 30)])
 def test_wgrad(l, m, n):
     rng = np.random.default_rng([l, m, n])
