@@ -14,6 +14,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;   // rows and columns of one operand
 constexpr int64_t kMaxGridY = 65535;
+constexpr int64_t kMaxTiles = (1 << 23) - 1;   // of 128 x 128: below 2^32 threads
 
 averis_status_t check_fp8(const averis_fp8_t* t, int64_t rows, int64_t cols) {
   if (!t) return AVERIS_E_NULL;
@@ -71,12 +72,12 @@ averis_status_t averis_fp8_quant(const void* a, averis_dtype_t dtype, int64_t ro
   if (out_t) {
     const int64_t tc = seg_offsets ? averis_fp8_seg_cols(rows, nseg) : rows;
     if ((s = check_fp8(out_t, cols, tc)) != AVERIS_OK) return s;
-    if ((cols + 127) / 128 > kMaxGridY) return AVERIS_E_SHAPE;
+    if ((cols + 127) / 128 * chunk_upper_bound(rows, nseg, 128) > kMaxTiles) return AVERIS_E_SHAPE;
     return hip_status(launch_fp8_tile(a, dtype == AVERIS_BF16, false, 1, rows, cols, lda, 0,
                                       seg_offsets, nseg, out_of(out), out_of(out_t), stream));
   }
   // a launch of one wavefront for every 4 rows x 512 columns
-  if ((rows + 3) / 4 * ((cols + 511) / 512) > INT32_MAX) return AVERIS_E_SHAPE;
+  if ((rows + 3) / 4 * ((cols + 511) / 512) >= 1 << 26) return AVERIS_E_SHAPE;
   return hip_status(launch_fp8_rows(a, dtype == AVERIS_BF16, rows, cols, lda, out_of(out), stream));
 }
 
@@ -87,7 +88,8 @@ averis_status_t averis_fp8_quant_weight(const void* w, averis_dtype_t dtype, int
   if (!dtype_ok(dtype)) return AVERIS_E_DTYPE;
   if (batch < 1 || batch > kMaxSeg) return AVERIS_E_ARG;
   if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxDim) return AVERIS_E_SHAPE;
-  if (ldw < cols || batch_stride < 0 || (cols + 127) / 128 > kMaxGridY) return AVERIS_E_SHAPE;
+  if (ldw < cols || batch_stride < 0) return AVERIS_E_SHAPE;
+  if ((cols + 127) / 128 * ((rows + 127) / 128) > kMaxTiles) return AVERIS_E_SHAPE;
   if (batch > 1 && batch_stride < rows * ldw) return AVERIS_E_SHAPE;
   if (!w || (!out && !out_t)) return AVERIS_E_NULL;
   if (!aligned(w, elem_size(dtype))) return AVERIS_E_ALIGN;

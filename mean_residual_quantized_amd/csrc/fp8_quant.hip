@@ -119,48 +119,69 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const T* __restrict__ a, int64
   }
 }
 
-// One 128 x 128 tile per workgroup.  Thread (r = t / 16, i = t % 16) holds
-// eight columns of rows r, r + 16, ..; a row's run is sixteen lanes, so the
-// plain copy comes from the registers.  The values go to LDS as loaded; for
-// the transposed copy a thread takes a column's (bf16: a column pair's) run of
-// rows from there, and the codes go back through LDS so that eight lanes store
-// a 128-byte row of the transposed copy.
+// One 128 x 128 tile per workgroup of eight wavefronts.  Thread (r = t / 16,
+// i = t % 16) holds eight columns of rows r, r + 32, ..; a row's run is sixteen
+// lanes, so the plain copy comes from the registers.  The values go to LDS as
+// loaded; for the transposed copy a thread takes a column's (bf16: a column
+// pair's) run of rows from there, and the codes go back through LDS (bf16: in
+// the place of the values, 36 KB in all, four workgroups a CU) so that eight
+// lanes store a 128-byte row of the transposed copy.  Bound by memory: each
+// value is read once and each code written once.  Neighbouring workgroups take
+// neighbouring tiles of the same rows.
 //
 // TILE: one scale for the tile (both copies then hold the same codes).
+//
+// Both copies, bf16, us (four wavefronts, row tiles first, values and codes
+// apart -> this; TB/s of reads and writes):
+//   16384 x 3072                  44.5 -> 39.3 (5.1)
+//   32768 x 2048, 64 segments     71.0 -> 53.5 (5.0)
+//   2999 x 1000                    9.0 ->  6.7 (latency)
+//   weight, 64 x 2048 x 768       77.5 -> 75.7 (5.3)
+constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
+
 template <typename T>
 constexpr size_t fp8_tile_lds() {
-  return (size_t)128 * 128 * sizeof(T) + 128 * 128 + 4 * 128 * 4;
+  return (size_t)128 * 128 * sizeof(T) + (sizeof(T) == 2 ? 0 : 128 * 128) + kTileWaves * 64 * 4;
 }
 
 template <typename T, bool TILE>
-__global__ __launch_bounds__(256) void k_fp8_tile(const T* __restrict__ a, int64_t rows,
-                                                  int64_t cols, int64_t lda, int64_t bstride,
-                                                  const int64_t* offs, int nseg, Fp8Out out,
-                                                  Fp8Out out_t) {
+__global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
+    const T* __restrict__ a, int64_t rows, int64_t cols, int64_t lda, int64_t bstride,
+    const int64_t* offs, int nseg, int tx, Fp8Out out, Fp8Out out_t) {
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
-  T* raw = reinterpret_cast<T*>(sm);                           // [128][128]
-  unsigned char* ct = sm + 128 * 128 * sizeof(T);              // [128 columns][128 rows] codes
-  uint32_t* red = reinterpret_cast<uint32_t*>(ct + 128 * 128);   // maxima of the four wavefronts
+  T* raw = reinterpret_cast<T*>(sm);   // [128][128]
+  // codes, [128 columns][128 rows]
+  unsigned char* ct = sm + (sizeof(T) == 2 ? 0 : 128 * 128 * sizeof(T));
+  // maxima: of rows, or a column's (column pair's) part of each wavefront
+  uint32_t* red = reinterpret_cast<uint32_t*>(sm + fp8_tile_lds<T>()) - kTileWaves * 64;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const int64_t c0 = (int64_t)blockIdx.y * 128;
+  const int chunk = (int)(blockIdx.x / (uint32_t)tx), block = (int)(blockIdx.x % (uint32_t)tx);
+  const int64_t c0 = (int64_t)block * 128;
   // a chunk of 128 rows, of one segment where there are several
-  const SegRange sr = locate_chunk(offs, nseg, rows, 128, blockIdx.x);
-  if (sr.seg < 0) return;
-  const int64_t r0 = sr.r0;
-  const int nr = (int)(sr.r1 - sr.r0);
+  int64_t r0 = 128 * (int64_t)chunk;
+  int nr = (int)(rows - r0 < 128 ? rows - r0 : 128);
+  if (offs) {
+    SegTable segs;
+    segs.init(offs, nseg, rows, 128);
+    int seg, ra, rb;
+    if (!segs.chunk(chunk, seg, ra, rb)) return;
+    r0 = ra;
+    nr = rb - ra;
+  }
   const int64_t b = blockIdx.z;
   a += b * bstride;
   const int i = t & 15, r = t >> 4;
-  Eight<T> v[8];
+  constexpr int PER = 32 / kTileWaves, STEP = 4 * kTileWaves;   // rows a thread
+  Eight<T> v[PER];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
+  for (int p = 0; p < PER; ++p) {
     v[p].zero();
-    if (r + 16 * p < nr) v[p].load(a + (r0 + r + 16 * p) * lda, c0 + 8 * i, cols);
+    if (r + STEP * p < nr) v[p].load(a + (r0 + r + STEP * p) * lda, c0 + 8 * i, cols);
   }
   uint32_t tile_max = 0;
   if constexpr (TILE) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < PER; ++p) {
       const uint32_t m = v[p].amax();
       tile_max = m > tile_max ? m : tile_max;
     }
@@ -168,25 +189,25 @@ __global__ __launch_bounds__(256) void k_fp8_tile(const T* __restrict__ a, int64
     if (i == 0) red[r] = tile_max;
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < 16; ++q) tile_max = red[q] > tile_max ? red[q] : tile_max;
+    for (int q = 0; q < STEP; ++q) tile_max = red[q] > tile_max ? red[q] : tile_max;
   }
   if (out.codes) {
     const int64_t row0 = b * rows + r0 + r;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
+    for (int p = 0; p < PER; ++p) {
       uint32_t byte;
       const uint32_t m = TILE ? tile_max : row16_max(v[p].amax());
       const u32x2_t q = eight_codes(v[p], m, byte);
-      if (r + 16 * p < nr) {
-        *reinterpret_cast<u32x2_t*>(out.codes + (row0 + 16 * p) * out.pitch + c0 + 8 * i) = q;
-        if (i == 0) out.scales[(row0 + 16 * p) * out.spitch + blockIdx.y] = (uint8_t)byte;
+      if (r + STEP * p < nr) {
+        *reinterpret_cast<u32x2_t*>(out.codes + (row0 + STEP * p) * out.pitch + c0 + 8 * i) = q;
+        if (i == 0) out.scales[(row0 + STEP * p) * out.spitch + block] = (uint8_t)byte;
       }
     }
   }
   if (!out_t.codes) return;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    T* dst = raw + (r + 16 * p) * 128 + 8 * i;
+  for (int p = 0; p < PER; ++p) {
+    T* dst = raw + (r + STEP * p) * 128 + 8 * i;
     if constexpr (sizeof(T) == 2) {
       *reinterpret_cast<u32x4_t*>(dst) = v[p].w;
     } else {
@@ -197,7 +218,7 @@ __global__ __launch_bounds__(256) void k_fp8_tile(const T* __restrict__ a, int64
   __syncthreads();
   const int64_t orow = b * cols + c0;   // row of the transposed copy
   auto scale_out = [&](int col, uint32_t byte) {
-    if (c0 + col < cols) out_t.scales[(orow + col) * out_t.spitch + blockIdx.x] = (uint8_t)byte;
+    if (c0 + col < cols) out_t.scales[(orow + col) * out_t.spitch + chunk] = (uint8_t)byte;
   };
   // piece q (16 rows) of a column's codes is kept at q ^ (column / 2 mod 8):
   // neighbouring lanes' writes go to different banks
@@ -205,27 +226,28 @@ __global__ __launch_bounds__(256) void k_fp8_tile(const T* __restrict__ a, int64
     *reinterpret_cast<u32x4_t*>(ct + col * 128 + 16 * (q ^ ((col >> 1) & 7))) = x;
   };
   if constexpr (sizeof(T) == 2) {
-    // columns 2 lane, 2 lane + 1, rows 32 w .. 32 w + 31
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(raw) + 32 * w * 64 + lane;
-    uint32_t x[32];
+    constexpr int WR = 128 / kTileWaves;   // rows a wavefront
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(raw) + WR * w * 64 + lane;
+    uint32_t x[WR];
 #pragma unroll
-    for (int q = 0; q < 32; ++q) x[q] = src[q * 64];
+    for (int q = 0; q < WR; ++q) x[q] = src[q * 64];
     uint32_t m0 = tile_max, m1 = tile_max;
+    if constexpr (TILE) __syncthreads();   // the codes take the values' place
     if constexpr (!TILE) {
       uint32_t m = 0;
 #pragma unroll
-      for (int q = 0; q < 32; ++q) m = pk_max_u16(m, x[q] & 0x7FFF7FFFu);
+      for (int q = 0; q < WR; ++q) m = pk_max_u16(m, x[q] & 0x7FFF7FFFu);
       red[w * 64 + lane] = m;
       __syncthreads();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) m = pk_max_u16(m, red[q * 64 + lane]);
+      for (int q = 0; q < kTileWaves; ++q) m = pk_max_u16(m, red[q * 64 + lane]);
       m0 = m << 16;
       m1 = m & 0xFFFF0000u;
     }
     const uint32_t b0 = f8_not_finite(m0) ? kF8One : f8_scale_byte(m0);
     const uint32_t b1 = f8_not_finite(m1) ? kF8One : f8_scale_byte(m1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < WR / 16; ++h) {
       u32x4_t y0, y1;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -238,47 +260,48 @@ __global__ __launch_bounds__(256) void k_fp8_tile(const T* __restrict__ a, int64
         if (f8_not_finite(m0)) y0[q] = kF8NanCodes;
         if (f8_not_finite(m1)) y1[q] = kF8NanCodes;
       }
-      put(2 * lane, 2 * w + h, y0);
-      put(2 * lane + 1, 2 * w + h, y1);
+      put(2 * lane, WR / 16 * w + h, y0);
+      put(2 * lane + 1, WR / 16 * w + h, y1);
     }
     if (w == 0) {
       scale_out(2 * lane, b0);
       scale_out(2 * lane + 1, b1);
     }
   } else {
-    // column t mod 128, rows 64 (t / 128) .. + 63
-    const int col = t & 127, half = t >> 7;
-    const float* src = reinterpret_cast<const float*>(raw) + 64 * half * 128 + col;
+    // column t mod 128, rows PR (t / 128) .. PR (t / 128) + PR - 1
+    constexpr int PARTS = kTileWaves / 2, PR = 128 / PARTS;
+    const int col = t & 127, part = t >> 7;
+    const float* src = reinterpret_cast<const float*>(raw) + PR * part * 128 + col;
     uint32_t m = tile_max;
     if constexpr (!TILE) {
-      for (int q = 0; q < 64; ++q) {
+      for (int q = 0; q < PR; ++q) {
         const uint32_t z = __float_as_uint(src[q * 128]) & 0x7FFFFFFFu;
         m = z > m ? z : m;
       }
-      red[half * 128 + col] = m;
+      red[part * 128 + col] = m;
       __syncthreads();
-      const uint32_t o = red[(half ^ 1) * 128 + col];
-      m = o > m ? o : m;
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q) m = red[q * 128 + col] > m ? red[q * 128 + col] : m;
     }
     const uint32_t byte = f8_not_finite(m) ? kF8One : f8_scale_byte(m);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < PR / 16; ++h) {
       u32x4_t y;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float* z = src + (16 * h + 4 * q) * 128;
         y[q] = f8_not_finite(m) ? kF8NanCodes : f8_codes4(z[0], z[128], z[256], z[384], byte);
       }
-      put(col, 4 * half + h, y);
+      put(col, PR / 16 * part + h, y);
     }
-    if (half == 0) scale_out(col, byte);
+    if (part == 0) scale_out(col, byte);
   }
   __syncthreads();
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int col = (t >> 3) + 32 * p, q = t & 7;
+  for (int p = 0; p < 16 / kTileWaves; ++p) {
+    const int col = (t >> 3) + 8 * kTileWaves * p, q = t & 7;
     if (c0 + col < cols)
-      *reinterpret_cast<u32x4_t*>(out_t.codes + (orow + col) * out_t.pitch + (int64_t)blockIdx.x * 128 +
+      *reinterpret_cast<u32x4_t*>(out_t.codes + (orow + col) * out_t.pitch + (int64_t)chunk * 128 +
                                   16 * q) =
           *reinterpret_cast<const u32x4_t*>(ct + col * 128 + 16 * (q ^ ((col >> 1) & 7)));
   }
@@ -291,10 +314,10 @@ hipError_t tile_t(const void* a, int batch, int64_t rows, int64_t cols, int64_t 
   constexpr size_t lds = fp8_tile_lds<T>();
   const hipError_t e = lds_attr_once<&k_fp8_tile<T, TILE>>((int)lds);
   if (e != hipSuccess) return e;
-  const dim3 g((unsigned)chunk_upper_bound(rows, offs ? nseg : 1, 128),
-               (unsigned)((cols + 127) / 128), (unsigned)batch);
-  k_fp8_tile<T, TILE><<<g, 256, lds, st>>>(static_cast<const T*>(a), rows, cols, lda, bstride,
-                                           offs, nseg, out, out_t);
+  const int64_t tx = (cols + 127) / 128;
+  const dim3 g((unsigned)(tx * chunk_upper_bound(rows, offs ? nseg : 1, 128)), 1u, (unsigned)batch);
+  k_fp8_tile<T, TILE><<<g, kTileThreads, lds, st>>>(static_cast<const T*>(a), rows, cols, lda, bstride,
+                                           offs, nseg, (int)tx, out, out_t);
   return hipGetLastError();
 }
 

@@ -70,78 +70,6 @@ __device__ __forceinline__ void f8_wait_vm() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// Chunks of the segments, 64 segments at a time, one a lane: the segment of a
-// chunk (of `ch` rows) or a segment's chunks come from a ballot, with no LDS
-// and no barrier.  Up to 64 segments are read once for a whole kernel.
-struct SegTable {
-  const int64_t* offs;
-  int nseg, ch;
-  int64_t rows;
-  int base;       // first segment of the loaded 64
-  int r0, r1;     // this lane's segment's rows
-  int c0, c1;     // its chunks
-
-  __device__ __forceinline__ void load(int b, int before) {
-    const int lane = threadIdx.x & 63;
-    base = b;
-    int64_t a = 0, e = 0;
-    if (b + lane < nseg) seg_bounds(offs, b + lane, rows, a, e);
-    r0 = (int)a;
-    r1 = (int)e;
-    const int n = (r1 - r0 + ch - 1) / ch;
-    int incl = n;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int t = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += t;
-    }
-    c1 = before + incl;
-    c0 = c1 - n;
-  }
-  __device__ __forceinline__ void init(const int64_t* o, int ns, int64_t r, int c) {
-    offs = o;
-    nseg = ns;
-    rows = r;
-    ch = c;
-    load(0, 0);
-  }
-  // the next 64 segments (false past the last)
-  __device__ __forceinline__ bool advance() {
-    if (base + 64 >= nseg) return false;
-    load(base + 64, __builtin_amdgcn_readlane(c1, 63));
-    return true;
-  }
-  // rows [a, b) of chunk c and its segment; false past the last chunk
-  __device__ __forceinline__ bool chunk(int c, int& seg, int& a, int& b) {
-    if (c < (int)__builtin_amdgcn_readfirstlane(c0)) load(0, 0);
-    do {
-      const uint64_t hit = __ballot(c >= c0 && c < c1);
-      if (hit) {
-        const int l = __builtin_ctzll(hit);
-        seg = base + l;
-        a = (int)__builtin_amdgcn_readlane(r0, l) + (c - (int)__builtin_amdgcn_readlane(c0, l)) * ch;
-        b = __builtin_amdgcn_readlane(r1, l);
-        b = a + ch < b ? a + ch : b;
-        return true;
-      }
-    } while (advance());
-    return false;
-  }
-  // chunks of all segments
-  __device__ __forceinline__ int count() {
-    while (advance()) {}
-    const int n = __builtin_amdgcn_readlane(c1, 63);
-    if (base != 0) load(0, 0);
-    return n;
-  }
-  // chunks [a, b) of a segment
-  __device__ __forceinline__ void segment(int s, int& a, int& b) {
-    if (s < base) load(0, 0);
-    while (s >= base + 64 && advance()) {}
-    a = __builtin_amdgcn_readlane(c0, (s - base) & 63);
-    b = __builtin_amdgcn_readlane(c1, (s - base) & 63);
-  }
-};
-
 // One output tile: rows m0 .. m0 + rows - 1, columns n0 .. n0 + cols - 1 and
 // the blocks kb0 .. kb0 + nk - 1 it contracts (all uniform).
 struct F8Tile {
