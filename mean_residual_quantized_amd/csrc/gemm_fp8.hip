@@ -31,7 +31,7 @@ constexpr int kF8Cus = 256;       // CUs of the card: one workgroup each
 
 // two slots of a stage's codes (128 bytes a row), two of scale words (four
 // stages, 4 bytes a row), and 4 KB a wavefront for its output (in the small
-// tile, which is its workgroup's only one, over the slots)
+// tile, two of which fill a CU's LDS, in the second slot)
 constexpr int kF8Stage = 4096;
 constexpr size_t f8_lds_bytes(int f) {
   return (size_t)(2 * 64 * f) * (2 * 128 + 2 * 4) + (f == 4 ? 4 * kF8Stage : 0);
@@ -92,7 +92,8 @@ struct F8Tile {
 // sched_group_barrier.  Scale bytes come four stages at a time, one aligned
 // word a row, the same way.
 //
-// A workgroup takes several tiles.  The barrier inside a tile's last stage
+// A workgroup takes several tiles (block segments, of very different lengths:
+// one, the longest segments' first).  The barrier inside a tile's last stage
 // frees both slots, so the next tile's first two stages are on their way
 // before this tile's output is; the output goes through 4 KB of LDS of the
 // wavefront's own (no barrier) to whole 128-byte lines, and its stores drain
@@ -102,7 +103,8 @@ template <int F, bool OUT_BF16, int MODE>
 __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     Fp8Operand A, Fp8Operand B, int m, int n, int k_blocks, const int64_t* offs, int nseg,
     int64_t seg_rows, int splits, int tx, int ty, void* c, int64_t ldc, int64_t c_split) {
-  constexpr bool MANY = F == 4 && MODE != kF8BlockSegs;   // several tiles a workgroup
+  constexpr bool MANY = MODE != kF8BlockSegs;   // several tiles a workgroup
+  constexpr int SLOTS = F == 4 ? kF8Cus : 2 * kF8Cus;   // workgroups the card holds
   constexpr int BM = 64 * F, BN = 64 * F, ROWS = BM + BN;
   constexpr int SLOT = ROWS * 128, SSLOT = ROWS * 4;
   constexpr int CPW = ROWS / 8 / 4;    // code loads a wavefront issues for a stage
@@ -118,7 +120,12 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  unsigned char* stg = smem_f8 + (F == 4 ? 2 * SLOT + 2 * SSLOT : 0) + wave * kF8Stage;
+  // output: 4 KB in rows of 128 bytes, eight rows every STG_STEP: the
+  // wavefront's own, or the part of the second slot that its last HELD loads
+  // of a stage fill
+  constexpr int HELD = F == 4 ? 0 : 4, STG_STEP = F == 4 ? 1024 : 4096;
+  unsigned char* stg = F == 4 ? smem_f8 + 2 * SLOT + 2 * SSLOT + wave * kF8Stage
+                              : smem_f8 + SLOT + (wave + 4 * (CPW - HELD)) * 1024;
 
   SegTable segs;
   if constexpr (MODE == kF8RowSegs) segs.init(offs, nseg, m, BM);
@@ -128,14 +135,14 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   // groups of four tile rows, column by column.  Workgroup w runs on die w
   // mod 8; with a workgroup a CU each die takes an eighth of the numbers, its
   // workgroups side by side, so the tiles a die runs together share operand
-  // rows in its L2.  With a workgroup a tile (segments of very different
-  // lengths are better left to the dispatcher) that is done plane by plane.
+  // rows in its L2.  With a workgroup a tile (fewer tiles than the card holds,
+  // or block segments, left to the dispatcher) that is done plane by plane.
   if constexpr (MODE == kF8RowSegs) ty = segs.count();   // the grid is for as many as there may be
   const int txy = tx * ty, total = txy * (MODE == kF8BlockSegs ? nseg : splits);
   const int w = blockIdx.x, grid = gridDim.x;
   int id, id_end, id_step;
-  if (MANY && grid == kF8Cus) {
-    const int x = w % kXcds, per = kF8Cus / kXcds;
+  if (MANY && grid == SLOTS) {
+    const int x = w % kXcds, per = SLOTS / kXcds;
     id = total / kXcds * x + total % kXcds * x / kXcds + w / kXcds;
     id_end = total / kXcds * (x + 1) + total % kXcds * (x + 1) / kXcds;
     id_step = per;
@@ -165,7 +172,8 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
         if (!segs.chunk(y, tl.seg, tl.m0, m_end)) continue;
       } else if constexpr (MODE == kF8BlockSegs) {
         int kb1;
-        segs.segment(z, tl.kb0, kb1);
+        tl.seg = segs.by_length(z);
+        segs.segment(tl.seg, tl.kb0, kb1);
         tl.nk = kb1 - tl.kb0;
       } else {
         // (k_blocks < 2^23, splits <= 16)
@@ -333,8 +341,9 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   // passes each issue a share of them and then four stores: behind them are
   // the stores of the pass that issued the last one and all that followed.
   constexpr int OUT_PASSES = F * PASSES;
-  constexpr int AFTER0 = CPW + 4 * (OUT_PASSES - step_of<FIRST, OUT_PASSES>(FIRST0 - 1));
-  static_assert(step_of<FIRST, OUT_PASSES>(FIRST - 1) == OUT_PASSES - 1, "stage 1's last load is the last pass's");
+  constexpr int AFTER0 = CPW + 4 * (OUT_PASSES - step_of<FIRST - HELD, OUT_PASSES>(FIRST0 - 1));
+  static_assert(HELD > 0 || step_of<FIRST, OUT_PASSES>(FIRST - 1) == OUT_PASSES - 1,
+                "stage 1's last load is the last pass's");
   bool behind = false;   // the first loads went out with a whole tile's output
   auto wait_loads = [&](auto firstc) __attribute__((always_inline)) {
     if (behind) f8_wait_vm<(decltype(firstc)::value != 0 ? AFTER0 : 4)>();
@@ -405,17 +414,17 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     // write of its own.  A wavefront's LDS accesses are in order.
     char* cb = static_cast<char*>(c) +
                ((MODE == kF8RowSegs ? 0 : cur.seg * c_split) + cur.m0 * ldc + cur.n0) * ES;
-    const bool whole = (ldc * ES) % 16 == 0 && (c_split * ES) % 16 == 0 && ldc <= (1 << 24) &&
-                       (reinterpret_cast<uintptr_t>(c) & 15) == 0 && cur.rows == BM &&
-                       cur.cols == BN;
+    // whole pieces: stores through a descriptor of the tile's bytes, which
+    // drops those past its rows and columns and counts them all the same
+    const bool pieces = (ldc * ES) % 16 == 0 && (c_split * ES) % 16 == 0 && ldc <= (1 << 21) &&
+                        (reinterpret_cast<uintptr_t>(c) & 15) == 0 && cur.cols * ES % 16 == 0;
     // the lane's places are formed anew for each tile: kept over the products
     // they would not fit the registers
     int ln = lane;
     asm volatile("" : "+v"(ln));
-    const uint32_t wr = (uint32_t)(uintptr_t)(lds_void*)stg + (ln & 31) * 128 +
-                        16 * ((ln & 7) ^ (ln >> 5));   // piece h; piece p + h at ^ 16 p
+    const uint32_t wr = (uint32_t)(uintptr_t)(lds_void*)stg + ((ln & 31) >> 3) * STG_STEP +
+                        (ln & 7) * 128 + 16 * ((ln & 7) ^ (ln >> 5));   // piece h; piece p + h at ^ 16 p
     const unsigned char* src = stg + (ln >> 3) * 128 + 16 * ((ln & 7) ^ (ln >> 3));
-    const uint32_t off = (uint32_t)(ln >> 3) * (uint32_t)(ldc * ES) + 16 * (ln & 7);
     constexpr int FPP = GROUP / 32;   // fragments of a pass
     static_assert(F % FPP == 0, "whole passes");
     u32x4_t out[4];   // a bf16 pass's values: pieces of two fragments
@@ -451,74 +460,87 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
         }
       }
     };
-    char* base = cb + ((int64_t)(wm * 32 * F) * ldc + wn * 32 * F) * ES;   // of the wavefront
-    const int64_t step8 = 8 * ldc * ES;
+    const int row0 = wm * 32 * F + (ln >> 3), col0 = wn * 32 * F + (ln & 7) * (16 / ES);
     auto clear = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
 #pragma unroll
       for (int f = 0; f < FPP; ++f) zero(i, p * FPP + f);
     };
-    if (whole) {
+    if (pieces) {
+      const uint32_t ldb = (uint32_t)(ldc * ES);
+      // below 2^31: a lane past the columns goes to 2^31 and on
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(scalar_base(reinterpret_cast<const uint8_t*>(cb))), 0,
+          (int)((uint32_t)(cur.rows - 1) * ldb + (uint32_t)(cur.cols * ES)), 0x00027000);
+      const uint32_t off = (uint32_t)row0 * ldb + (uint32_t)(col0 * ES);
       form(F8Step<0>{});
       each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
-        constexpr int P = decltype(pc)::value;
+        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
         to_lds(pc);
         clear(pc);
         u32x4_t v[4];   // row 8 it + lane / 8, piece lane mod 8
 #pragma unroll
-        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const u32x4_t*>(src + it * 1024);
+        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const u32x4_t*>(src + it * STG_STEP);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (P + 1 < OUT_PASSES) form(F8Step<P + 1>{});
         if (loads) {
 #pragma unroll
-          for (int k = P * FIRST / OUT_PASSES; k < (P + 1) * FIRST / OUT_PASSES; ++k)
+          for (int k = P * (FIRST - HELD) / OUT_PASSES; k < (P + 1) * (FIRST - HELD) / OUT_PASSES; ++k)
             first_load(k, nxt.nk);
+          if constexpr (HELD > 0 && P + 1 == OUT_PASSES) {
+            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the last values are out of their place
+#pragma unroll
+            for (int k = FIRST - HELD; k < FIRST; ++k) first_load(k, nxt.nk);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
+        const uint32_t at = (off + 128 * p) | (col0 + p * GROUP < cur.cols ? 0u : 0x80000000u);
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          u32x4_t* dst = reinterpret_cast<u32x4_t*>(base + P % PASSES * 128 + off);
-          if constexpr (OUT_BF16) store_stream(v[it], dst);
-          else store_out(v[it], dst);
-          if (it + 1 < 4 || P % PASSES + 1 == PASSES) base += step8;
-          else base -= 3 * step8;
-        }
+        for (int it = 0; it < 4; ++it)
+          // bf16 streaming (2), as store_stream
+          __builtin_amdgcn_raw_buffer_store_b128(v[it], rsrc, (int)(at + (uint32_t)(32 * i + 8 * it) * ldb),
+                                                 0, OUT_BF16 ? 2 : 0);
         __builtin_amdgcn_sched_barrier(0);
       });
     } else {
-      // rows and columns past the edge left out, any alignment
-      if (loads) first_loads(nxt.nk);
+      // any alignment and size
+      if (HELD == 0 && loads) first_loads(nxt.nk);
       each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
         constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
         form(pc);
         to_lds(pc);
         clear(pc);
-        const int left = cur.cols - wn * 32 * F - p * GROUP - (ln & 7) * (16 / ES);
-        int r = wm * 32 * F + 32 * i + (ln >> 3);
-        char* dst = base + (32 * i + (ln >> 3)) * ldc * ES + p * 128 + 16 * (ln & 7);
-#pragma unroll 1
-        for (int it = 0; it < 4; ++it, r += 8, dst += step8) {
-          const unsigned char* from = src + it * 1024;
-          if (r < cur.rows && left > 0) {
-            if (left >= 16 / ES) {
-              *reinterpret_cast<f8_piece_t*>(dst) = *reinterpret_cast<const u32x4_t*>(from);
-            } else {
-#pragma unroll 1
-              for (int x = 0; x < left; ++x) {
-                if constexpr (OUT_BF16)
-                  reinterpret_cast<uint16_t*>(dst)[x] = reinterpret_cast<const uint16_t*>(from)[x];
-                else
-                  reinterpret_cast<uint32_t*>(dst)[x] = reinterpret_cast<const uint32_t*>(from)[x];
-              }
+        const int left = cur.cols - col0 - p * GROUP;
+        char* dst = cb + ((int64_t)(row0 + 32 * i) * ldc + col0 + p * GROUP) * ES;
+        u32x4_t v[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const u32x4_t*>(src + it * STG_STEP);
+#pragma unroll
+        for (int it = 0; it < 4; ++it, dst += 8 * ldc * ES) {
+          if (row0 + 32 * i + 8 * it >= cur.rows) continue;
+          if (left >= 16 / ES) {
+            *reinterpret_cast<f8_piece_t*>(dst) = v[it];
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16 / ES; ++x) {
+              if (x >= left) continue;
+              if constexpr (OUT_BF16)
+                reinterpret_cast<uint16_t*>(dst)[x] = (uint16_t)(v[it][x / 2] >> (16 * (x & 1)));
+              else
+                reinterpret_cast<uint32_t*>(dst)[x] = v[it][x];
             }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
       });
+      if constexpr (HELD > 0) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        if (loads) first_loads(nxt.nk);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     if (!more) break;
-    behind = whole;
+    behind = pieces;
     cur = nxt;
   }
 }
@@ -655,15 +677,22 @@ struct Fp8Plan {
 };
 
 // The choice minimises an estimate in microseconds, fitted to this card: the
-// 256 x 256 tile (a workgroup a CU) takes 1.46 a stage and 9.3 a round of 256
-// tiles, the 128 x 128 tile (two a CU) 1.05 and 2.5 a round of 512, or 0.62 a
-// stage alone on its CU; a split output costs another launch and 8 bytes a
-// value and split at 9.5 TB/s; the few-rows kernel reads both operands once a
-// workgroup at 6.5 TB/s.  Measured either side (us, large / small tile):
-// 8192^3 414 / 558, 16384 x 1024 x 3072 48.5 / 58.2, 2048 x 1024 x 2048 24.0 /
-// 12.4; 64 segments of 512 rows, 768 x 2048: 71.5 / 73.9, of 64 rows: 33.4 /
-// 23.5; weight gradient over 16384 tokens, 1024 x 3072: 140 in one split, 66
-// in five; 16 rows x 1024 x 2048: 9.9 small tile, 4.4 few-rows kernel.
+// 256 x 256 tile (a workgroup a CU) takes 1.37 a stage and 7 a round of 256
+// tiles, the 128 x 128 tile (two a CU) 1.02 and 2 a round of 512, or 0.62 a
+// stage alone on its CU.  Row segments make the small tile's stages a fifth
+// longer (it reads a segment's weights twice as often); block segments, each
+// tile on its own, cost 2.3 (3.0) more a round.  A split output costs another launch
+// and 8 bytes a value and split at 9.5 TB/s; the few-rows kernel reads both
+// operands once a workgroup at 6.5 TB/s.
+// Measured either side (us, large / small tile):
+//   16384 x 1024 x 3072  44.6 / 55.4    8192 x 2048 x 512     15.8 / 14.4
+//   16384 x 3072 x 1024  58.1 / 78.8    65536 x 1024 x 256    38.8 / 34.8
+//   32768 rows in 64 segments, 768 x 2048: 73.8 / 86.5, 2048 x 768: 88.9 / 98.6
+//   8192 rows in 128 segments, 768 x 2048: 66.9 / 55.0
+//   weight gradients of 32768 rows in 64 segments, 2048 x 768: 100.8 / 110.3,
+//   of 16384 rows in 8, 1024 x 3072: 72.9 / 67.7
+//   weight gradient over 16384 tokens, 1024 x 3072: 140 in one split, 64 in five
+//   16 rows x 1024 x 2048: 9.9 small tile, 4.4 few-rows kernel
 Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg) {
   Fp8Plan best{0, 4, 1};
   double best_us = 1e300;
@@ -687,10 +716,15 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg)
     for (int splits = 1; splits <= 16; ++splits) {
       if (splits > 1 && (mode != kF8All || k_blocks < 2 * splits)) break;
       const double t = tiles * splits;
-      const double stage = f == 4 ? 1.46 : t <= kF8Cus ? 0.62 : 1.05;
-      const double tile = f == 4 ? 9.3 : t <= kF8Cus ? 1.5 : 2.5;
-      const double rounds = t <= slots ? 1.0 : mode == kF8All ? (double)(int64_t)((t + slots - 1) / slots) : t / slots;
-      offer(Fp8Plan{0, f, splits}, 3.0 + rounds * ((double)((int64_t)(stages + splits - 1) / splits) * stage + tile) +
+      const double stage = f == 4 ? 1.37 : (t <= kF8Cus ? 0.62 : 1.02) * (mode == kF8RowSegs ? 1.2 : 1.0);
+      const double alone = mode != kF8BlockSegs ? 0.0 : f == 4 ? 2.3 : 3.0;
+      const double tile = (f == 4 ? 7.0 : t <= kF8Cus ? 1.5 : 2.0) + alone;
+      // the last round is not full; how full, the segments leave open
+      const double rounds = t <= slots       ? 1.0
+                            : mode == kF8All ? (double)(int64_t)((t + slots - 1) / slots)
+                                             : t / slots + 0.35;
+      const double per = (double)((int64_t)(stages + splits - 1) / splits);
+      offer(Fp8Plan{0, f, splits}, 3.0 + rounds * (per * stage + tile) +
                                        (splits > 1 ? 5.0 + splits * dm * dn * 8.0 / 9.5e6 : 0.0));
     }
   }
@@ -716,8 +750,8 @@ hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t
   const int64_t tx = (g.n + 64 * F - 1) / (64 * F);
   const int64_t tiles = tx * ty * (MODE == kF8BlockSegs ? g.nseg : splits);
   if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
-  const bool many = F == 4 && MODE != kF8BlockSegs;
-  const int64_t grid = many && tiles > kF8Cus ? kF8Cus : tiles;
+  constexpr int slots = F == 4 ? kF8Cus : 2 * kF8Cus;
+  const int64_t grid = MODE != kF8BlockSegs && tiles > slots ? slots : tiles;
   k_gemm_f8<F, OB, MODE><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(
       g.a, g.b, (int)g.m, (int)g.n, (int)g.k_blocks, g.offs, g.nseg, g.rows, splits, (int)tx,
       (int)ty, c, ldc, c_split);

@@ -189,6 +189,28 @@ struct SegTable {
     if (base != 0) load(0, 0);
     return n;
   }
+  // the segment that is number s when the 64 around it go by length, longest
+  // first (lengths within a factor of two by index)
+  __device__ __forceinline__ int by_length(int s) {
+    while (base > s || s >= base + 64) {
+      if (base > s) load(0, 0);
+      else if (!advance()) break;
+    }
+    int left = s - base;
+    const int n = c1 - c0, cls = n > 0 ? 32 - __builtin_clz(n) : 0;   // chunks below 2^24
+    for (int k = 24; k > 0; --k) {
+      const uint64_t of = __ballot(cls == k);
+      const int many = __builtin_popcountll(of);
+      if (left < many) return base + nth_bit(of, left);
+      left -= many;
+    }
+    return base + nth_bit(__ballot(cls == 0), left);
+  }
+  // the place of set bit number i
+  __device__ __forceinline__ int nth_bit(uint64_t bits, int i) {
+    const int below = __builtin_amdgcn_mbcnt_hi((uint32_t)(bits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)bits, 0));
+    return __builtin_ctzll(__ballot(below == i && (bits >> (threadIdx.x & 63) & 1)));
+  }
   // chunks [a, b) of a segment
   __device__ __forceinline__ void segment(int s, int& a, int& b) {
     if (s < base) load(0, 0);
