@@ -186,7 +186,10 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 }
 
 // Top-k by k rounds of a group maximum over the lane's V and the group.  bf16:
-// the key names the expert.  fp32: the smallest expert that has the key.
+// the key names the expert.  fp32: the smallest expert that has the key; all
+// that have it are taken out as they are found, and put back where there were
+// several (the wavefront's count of them says so), against one search and one
+// removal: 65521 tokens, 128 experts, top 6, 16.0 -> 15.0 us.
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int64_t tokens,
                                                int experts, int64_t ld, int topk, int renorm,
@@ -222,13 +225,23 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int
 #pragma unroll
         for (int v = 0; v < V; ++v) key[v] = key[v] == best ? 0u : key[v];
       } else {
+        const uint32_t pick = best != 0u ? best : 1u;   // (1 is no logit's key)
         at = 0xFFFFu;
+        int hits = 0;   // of all the wavefront's tokens
 #pragma unroll
-        for (int v = V - 1; v >= 0; --v) at = key[v] == best ? (uint32_t)D::expert(g, v) : at;
+        for (int v = V - 1; v >= 0; --v) {
+          const bool hit = key[v] == pick;
+          hits += __builtin_popcountll(__ballot(hit));
+          at = hit ? (uint32_t)D::expert(g, v) : at;
+          key[v] = hit ? 0u : key[v];
+        }
         at = group_min<G>(at);
-        const uint32_t mine = D::place(g, (int)at);
+        if (hits != __builtin_popcountll(__ballot(best != 0u)) / G) {
+          // equal logits: those behind the lowest expert go back
 #pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = mine == (uint32_t)v ? 0u : key[v];
+          for (int v = 0; v < V; ++v)
+            if (logit_key<T>(l[v], 0u) == pick && (uint32_t)D::expert(g, v) > at) key[v] = pick;
+        }
       }
       const float x = key_logit<T>(best);
       if (o == 0 && r == 0 && best != 0u) top = x;
