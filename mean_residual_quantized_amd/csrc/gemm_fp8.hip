@@ -174,6 +174,9 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
         int kb1;
         tl.seg = segs.by_length(z);
         segs.segment(tl.seg, tl.kb0, kb1);
+        // within the operands whatever the offsets hold
+        kb1 = kb1 < k_blocks ? kb1 : k_blocks;
+        tl.kb0 = tl.kb0 < kb1 ? tl.kb0 : kb1;
         tl.nk = kb1 - tl.kb0;
       } else {
         // (k_blocks < 2^23, splits <= 16)

@@ -290,6 +290,27 @@ def test_large_row_segments_are_exact(offs):
         assert torch.equal(c, ref.to(dt))
 
 
+@pytest.mark.parametrize("m,n,offs", [
+    (2101, 2055, [0, 4000, 4000, 4129, 9400]), (130, 70, [0, 100, 9000, 9000, 9200]), (256, 512, [0, 8192, 9000]),
+    (300, 2048, [0, 10, 20, 4500, 4510, 9300]), (1000, 1001, [0] * 70 + [50, 100, 6000, 6001, 9400] + [9400] * 10)])
+def test_wgrad_long_segments_are_exact(m, n, offs):
+    rng = np.random.default_rng(offs + [m, n])
+    rows, nseg = 9400, len(offs) - 1
+    x, d = (torch.from_numpy(rng.integers(-4, 5, (rows, c)).astype(np.float32)).cuda().to(BF16) for c in (m, n))
+    o = torch.tensor(offs, dtype=torch.int64, device="cuda")
+    _, xt = av.averis_fp8_quant(x, transposed=True, offsets=o, plain=False)
+    _, dt = av.averis_fp8_quant(d, transposed=True, offsets=o, plain=False)
+    for dtype in (F32, BF16):
+        out = torch.full((nseg + 1, m, n), 9.0, dtype=dtype, device="cuda")
+        av.averis_fp8_gemm_wgrad(xt, dt, dtype, offsets=o, rows=rows, out=out[:nseg])
+        for s in range(nseg):
+            xs, ds = x[offs[s]:offs[s + 1]].double(), d[offs[s]:offs[s + 1]].double()
+            assert torch.equal(out[s], (xs.t() @ ds).to(dtype))
+        assert (out[nseg] == 9).all()
+        again = av.averis_fp8_gemm_wgrad(xt, dt, dtype, offsets=o, rows=rows)
+        assert torch.equal(again, out[:nseg])
+
+
 @pytest.mark.parametrize("offs", [[0, 4000, 4000, 4129, 9400], [0, 0, 0, 9400, 9400], [0, 2048, 4700, 7000, 9300]])
 def test_large_wgrad_segments_are_exact(offs):
     rng = np.random.default_rng(offs)
