@@ -189,7 +189,9 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 // the key names the expert.  fp32: the smallest expert that has the key; all
 // that have it are taken out as they are found, and put back where there were
 // several (the wavefront's count of them says so), against one search and one
-// removal: 65521 tokens, 128 experts, top 6, 16.0 -> 15.0 us.
+// removal: 65521 tokens, 128 experts, top 6, 16.0 -> 15.0 us (33.5 MB, 2.2
+// TB/s).  Bound by vector instructions at many tokens, by latency at few (16
+// tokens 2.7 us).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int64_t tokens,
                                                int experts, int64_t ld, int topk, int renorm,
@@ -276,7 +278,8 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int
 
 // w = softmax over the chosen (renorm) or all logits.  With s_e = dweights of
 // the slot that chose e (0 if none) and m = sum over the chosen of w s:
-// dl_e = w_e (s_e - m), zero outside the chosen when renorm.
+// dl_e = w_e (s_e - m), zero outside the chosen when renorm.  65521 tokens, 128
+// experts fp32: 15.4 us (67 MB, 4.4 TB/s).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tokens,
                                                     int experts, int64_t ld, int topk, int renorm,
@@ -359,7 +362,9 @@ __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tok
 // goes to bucket `experts`, the tail.  Each wavefront owns a run of slots:
 // its counts per bucket are turned into its first rows per bucket (buckets,
 // then wavefronts, in order), then it ranks its slots 64 at a time by ballots
-// over the bucket's bits.  No step depends on the order of atomics.
+// over the bucket's bits.  No step depends on the order of atomics.  Bound by
+// the latency of its launches: 32768 slots, 64 experts 8.7 us (0.4 MB), 393126
+// slots, 128 experts 14.1 us.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ int bucket_of(int32_t id, int experts) {
@@ -443,6 +448,8 @@ __device__ __forceinline__ void sort_place(int64_t first, int64_t n, int experts
   }
 }
 
+// One workgroup does everything up to 8192 slots (one / several workgroups, us,
+// 64 experts: 128 slots 4.4 / 7.5, 4096 7.8 / 9.3, 8192 9.2 / 9.7).
 constexpr int kSortWavesOne = 16, kSortStepsOne = 8;     // one workgroup for everything
 constexpr int kSortWavesMany = 4, kSortStepsMany = 4;    // workgroups of a larger sort
 constexpr int64_t kSortOne = (int64_t)kSortWavesOne * 64 * kSortStepsOne;       // 8192 slots
@@ -496,7 +503,7 @@ __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_hist(
   }
 }
 
-// a bucket's counts -> the slots of it in the chunks before, and all of them in
+// many chunks: a bucket's counts -> the slots of it in the chunks before, and all of them in
 // totals[bucket]: a wavefront a bucket, 64 chunks at a time
 __global__ __launch_bounds__(256) void k_sort_scan(int* __restrict__ hist, int experts, int chunks,
                                                    int* __restrict__ totals) {
@@ -518,7 +525,8 @@ __global__ __launch_bounds__(256) void k_sort_scan(int* __restrict__ hist, int e
   if (lane == 0) totals[e] = run;
 }
 
-// each workgroup sums the buckets' totals for itself: the offsets
+// each workgroup sums the buckets' totals for itself: the offsets.  hist and
+// totals as k_sort_scan left them, or the counts and no totals
 __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_place(
     const int32_t* __restrict__ ids, int64_t n, int experts, int chunks,
     const int* __restrict__ hist, const int* __restrict__ totals, int64_t* __restrict__ offsets,
@@ -534,12 +542,31 @@ __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_place(
   for (int e0 = 0; e0 < nb; e0 += T) {
     const int e = e0 + threadIdx.x;
     int all;
-    const int mine = e < nb ? totals[e] : 0;
+    // slots of the bucket: all, and in the chunks before
+    int mine = 0, pre = 0;
+    if (e < nb) {
+      const int* row = hist + (int64_t)e * chunks;
+      if (totals) {
+        mine = totals[e];
+        pre = row[blockIdx.x];
+      } else {
+        for (int c0 = 0; c0 < chunks; c0 += 16) {   // sixteen loads in flight
+          int v[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) v[u] = c0 + u < chunks ? row[c0 + u] : 0;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            pre += c0 + u < (int)blockIdx.x ? v[u] : 0;
+            mine += v[u];
+          }
+        }
+      }
+    }
     const int start = before + block_exclusive<kSortWavesMany>(mine, sh, all);
     before += all;
     if (e >= nb) continue;
     if (blockIdx.x == 0) offsets[e] = start;   // offsets[experts]: the tail's first row
-    int run = start + hist[(int64_t)e * chunks + blockIdx.x];
+    int run = start + pre;
     for (int w = 0; w < kSortWavesMany; ++w) {
       const int c = cnt[w * nb + e];
       cnt[w * nb + e] = run;
@@ -559,7 +586,8 @@ __global__ void k_zero_offsets(int64_t* offsets, int count) {
 // Token exchange.  blockDim.x lanes (whole wavefronts) go along a token's
 // columns in 16-byte pieces, blockDim.y tokens to a workgroup.  Rows outside
 // the tokens * topk there are, which only malformed positions name, are
-// neither read nor written.
+// neither read nor written.  All four are bound by memory: a row is read or
+// written once, whole, in lines; sums are fp32, rounded once.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
@@ -567,7 +595,10 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// a token is read once and written to its k rows
+// A token is read once and written to its k rows.  4096 tokens, top 8, 2048
+// bf16: 26.3 us (151 MB, 5.7 TB/s).  Streaming stores made the rows 10 % sooner
+// written, and what reads them next slower by more (4096 tokens and their fp8
+// quantization 55.2 us, with streaming stores 57.3).
 template <typename T>
 __global__ __launch_bounds__(256) void k_dispatch(const T* __restrict__ x, int64_t tokens,
                                                   int64_t cols, int64_t ldx,
@@ -588,7 +619,8 @@ __global__ __launch_bounds__(256) void k_dispatch(const T* __restrict__ x, int64
   }
 }
 
-// y_t = sum_j w_tj rows[pos_tj], slots in order, fp32; eight rows in flight
+// y_t = sum_j w_tj rows[pos_tj], slots in order, fp32; eight rows in flight.
+// 4096 tokens, top 8, 2048 bf16: 35.8 us (151 MB, 4.2 TB/s).
 template <typename T, bool WEIGHTED>
 __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ rows, int64_t tokens,
                                                  int64_t cols, int64_t ldr,
@@ -630,7 +662,8 @@ __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ rows, int
 }
 
 // drows[pos_tj] = w_tj dy_t and dweights_tj = <dy_t, rows[pos_tj]>: one
-// wavefront a slot, neighbouring slots share dy_t through the cache
+// wavefront a slot, neighbouring slots share dy_t through the cache.  4096
+// tokens, top 8, 2048 bf16: 50.9 us (285 MB, 5.6 TB/s).
 template <typename T>
 __global__ __launch_bounds__(256) void k_combine_grad(const T* __restrict__ dy, int64_t slots,
                                                       int64_t cols, int64_t ldy,
@@ -680,7 +713,12 @@ dim3 exchange_block(int64_t cols, int per) {
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-// lanes per token and logits per lane by the number of experts
+// Lanes per token and logits per lane by the number of experts: as few lanes as
+// keep the logits in registers.  Twice the lanes (half the logits) is faster
+// for few tokens and slower for many, half the lanes the other way round (us,
+// half / these / twice the lanes, bf16, route and gradient): 4096 tokens of 64
+// experts 4.4 4.7 / 3.6 3.8 / 3.3 3.6, of 256 5.8 6.6 / 4.3 5.0 / 4.0 4.3; 65536
+// of 64 7.7 8.2 / 8.0 8.6 / 10.5 11.9, of 256 18.4 23.7 / 18.7 24.3 / 23.4 26.1.
 #define AVERIS_ROUTE_SHAPES(CALL)      \
   if (experts <= 8) {                  \
     CALL(8, 1);                        \
@@ -771,7 +809,14 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t slots, int experts, int64
   int* hist = static_cast<int*>(ws);
   k_sort_hist<<<chunks, 64 * kSortWavesMany, lds, st>>>(ids, slots, experts, chunks, hist);
   int* totals = hist + (int64_t)(experts + 1) * chunks;
-  k_sort_scan<<<dim3((unsigned)((experts + 4) / 4)), 256, 0, st>>>(hist, experts, chunks, totals);
+  // few counts: every workgroup reads its buckets' whole rows, a launch less
+  // (scanned / unscanned, us, 64 experts: 16384 slots 9.6 / 8.0, 32768 9.7 /
+  // 8.7, 65536 9.7 / 10.2; 256 experts: 8200 slots 10.8 / 9.3, 32768 11.4 /
+  // 13.1; 8 experts: 65536 slots 9.1 / 8.5, 131072 9.7 / 10.4)
+  if (chunks > 64 || chunks * (experts + 1) > 4096)
+    k_sort_scan<<<dim3((unsigned)((experts + 4) / 4)), 256, 0, st>>>(hist, experts, chunks, totals);
+  else
+    totals = nullptr;
   k_sort_place<<<chunks, 64 * kSortWavesMany, lds, st>>>(ids, slots, experts, chunks, hist, totals,
                                                          offsets, pos, src);
   return hipGetLastError();

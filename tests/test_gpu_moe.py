@@ -124,7 +124,7 @@ def test_route_gradient_against_differences():
 
 
 SORTS = [(1, 1, 1), (1, 8, 64), (16, 8, 64), (7, 3, 5), (1024, 8, 64), (1025, 8, 64), (2731, 3, 1000),
-         (8192, 1, 1024), (20000, 2, 3), (4096, 8, 128)]
+         (8192, 1, 1024), (20000, 2, 3), (4096, 8, 128), (2048, 5, 63), (9000, 8, 6), (50000, 8, 128)]
 
 
 @pytest.mark.parametrize("t,k,e", SORTS)
