@@ -89,7 +89,7 @@ struct F8Tile {
 // k-step 1's fragments; then (its slot read out, stage s + 1 landed) one
 // barrier; then k-step 1 while stage s + 2 is loaded into the slot and stage s
 // + 1's first fragments are read.  Per MFMA one LDS read and one load, by
-// sched_group_barrier.  Scale bytes come four stages at a time, one aligned
+// barriers for the scheduler after each.  Scale bytes come four stages at a time, one aligned
 // word a row, the same way.
 //
 // A workgroup takes several tiles (block segments, of very different lengths:
@@ -98,6 +98,16 @@ struct F8Tile {
 // before this tile's output is; the output goes through 4 KB of LDS of the
 // wavefront's own (no barrier) to whole 128-byte lines, and its stores drain
 // under the next tile's products (the waits of the first stage count them).
+//
+// Bound by the matrix pipes' power on large products: 8192^3 395 us (2.78
+// PFLOP/s; the instruction alone, from registers, 3.26 on random operands),
+// 16384 x 1024 x 3072 45 us (2.3); by the output of each round of tiles where K
+// is short (16384 x 3072 x 1024 57 us, 1.8: 9 us of products, 7 of the rest a
+// round); and by memory by expert segments (32768 rows in 64 segments, 768 x
+// 2048: 62 us with its operands in the last-level cache, 77 without).
+// Four slots of 64 k instead of two of 128, loads twice as far ahead: 10 %
+// slower on large products (half lines a load, a barrier more a block) and no
+// faster where the operands come from memory.
 // ---------------------------------------------------------------------------
 template <int F, bool OUT_BF16, int MODE>
 __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
@@ -552,7 +562,9 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
 // Few rows: 16 columns (rows of b) and 16 MF rows of a to a workgroup of eight
 // wavefronts that divide the blocks among them; a wavefront's operands come
 // straight to registers (a block of a row: 32 bytes a lane), several blocks'
-// loads in flight, and the partial sums meet in LDS.
+// loads in flight, and the partial sums meet in LDS.  Bound by latency at small
+// weights (16 rows x 1024 x 2048: 4.6 us), by reading the weight at large ones
+// (16 x 8192 x 4096: 10.4 us, 3.3 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyWaves = 8;
 
