@@ -399,3 +399,24 @@ def test_linear_step_stream_and_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, ref))
         step()
+
+
+def test_offsets_past_32_bits():
+    """Operands and outputs of more than 2^32 bytes: products of small integers,
+    exact, at the first and the last rows."""
+    rows, cols, n = 70001, 65536, 17
+    small = lambda *s: torch.randint(-4, 5, s, dtype=torch.int8, device="cuda").to(BF16)
+    a, b, d = small(rows, cols), small(n, cols), small(rows, n)
+    q, qt = av.averis_fp8_quant(a, transposed=True)
+    some = [0, 1, 32767, 65536, rows - 2, rows - 1]
+    c = av.averis_fp8_gemm(q, av.averis_fp8_quant(b), F32)
+    assert torch.equal(c[some].double(), a[some].double() @ b.double().t())
+    _, dt = av.averis_fp8_quant(d, transposed=True)
+    w = av.averis_fp8_gemm_wgrad(qt, dt, F32)
+    some = [0, 1, 32769, cols - 2, cols - 1]
+    assert torch.equal(w[some].double(), a[:, some].double().t() @ d.double())
+    del a, q, qt, c, w
+    x, y = small(rows, 128), small(40000, 128)
+    c = av.averis_fp8_gemm(av.averis_fp8_quant(x), av.averis_fp8_quant(y), F32)   # 11 GB
+    some = [0, 255, 26843, 53687, rows - 1]
+    assert torch.equal(c[some].double(), x[some].double() @ y.double().t())
