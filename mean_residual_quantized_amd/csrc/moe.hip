@@ -57,15 +57,18 @@ template <typename T>
 __device__ __forceinline__ u32x4_t load_piece(const T* row, int64_t c, int64_t cols) {
   constexpr int P = Elem<T>::kPer;
   if (c + P <= cols) return *reinterpret_cast<const piece_t*>(row + c);
+  // the row's last elements: all loads at once, those past the end of its last
+  // element
   u32x4_t v = {0u, 0u, 0u, 0u};
+  T e[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) e[i] = row[c + i < cols ? c + i : cols - 1];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    if (c + i < cols) {
-      if constexpr (sizeof(T) == 2)
-        v[i / 2] |= (uint32_t)row[c + i] << (16 * (i & 1));
-      else
-        v[i] = __float_as_uint(row[c + i]);
-    }
+    if constexpr (sizeof(T) == 2)
+      v[i / 2] |= (c + i < cols ? (uint32_t)e[i] : 0u) << (16 * (i & 1));
+    else
+      v[i] = c + i < cols ? __float_as_uint(e[i]) : 0u;
   }
   return v;
 }
