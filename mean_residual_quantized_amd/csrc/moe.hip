@@ -366,8 +366,8 @@ __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tok
 // its counts per bucket are turned into its first rows per bucket (buckets,
 // then wavefronts, in order), then it ranks its slots 64 at a time by ballots
 // over the bucket's bits.  No step depends on the order of atomics.  Bound by
-// the latency of its launches: 32768 slots, 64 experts 8.7 us (0.4 MB), 393126
-// slots, 128 experts 14.1 us.
+// the latency of its launches: 32768 slots, 64 experts 8.7 us (0.4 MB), 393120
+// slots, 128 experts 13.2 us.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ int bucket_of(int32_t id, int experts) {
@@ -507,23 +507,34 @@ __global__ __launch_bounds__(64 * kSortWavesMany) void k_sort_hist(
 }
 
 // many chunks: a bucket's counts -> the slots of it in the chunks before, and all of them in
-// totals[bucket]: a wavefront a bucket, 64 chunks at a time
+// totals[bucket]: a wavefront a bucket, 64 chunks at a time, eight such loads in
+// flight
 __global__ __launch_bounds__(256) void k_sort_scan(int* __restrict__ hist, int experts, int chunks,
                                                    int* __restrict__ totals) {
   const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (e > experts) return;
   int* row = hist + (int64_t)e * chunks;
   int run = 0;
-  for (int c0 = 0; c0 < chunks; c0 += 64) {
-    const int c = c0 + lane, v = c < chunks ? row[c] : 0;
-    int incl = v;
+  for (int c0 = 0; c0 < chunks; c0 += 64 * 8) {
+    int v[8];   // all loads at once
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += u;
+    for (int u = 0; u < 8; ++u) {
+      const int c = c0 + 64 * u + lane;
+      v[u] = c < chunks ? row[c] : 0;
     }
-    if (c < chunks) row[c] = run + incl - v;
-    run += __shfl(incl, 63, 64);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      if (c0 + 64 * u >= chunks) break;
+      const int c = c0 + 64 * u + lane;
+      int incl = v[u];
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int t = __shfl_up(incl, d, 64);
+        if (lane >= d) incl += t;
+      }
+      if (c < chunks) row[c] = run + incl - v[u];
+      run += __shfl(incl, 63, 64);
+    }
   }
   if (lane == 0) totals[e] = run;
 }
