@@ -841,12 +841,13 @@ def _one_device(a, b):
     return dev
 
 
-def _fp8_product(ws, op, dims, dev):
-    """The workspace of a product: the caller's, a new one, or none."""
+def _fp8_ws(ws, op, dims, dev):
+    """The workspace of a product: the caller's, a new one, or None.  The tensor
+    itself, which the caller holds until its call has returned."""
     if ws is None:
         need = workspace_bytes(op, *dims)
         ws = _workspace(need, dev) if need else None
-    return (ws.data_ptr(), ws.numel()) if ws is not None else (None, 0)
+    return ws
 
 
 def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=None):
@@ -862,9 +863,11 @@ def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=N
         ldc = _matrix(c, c, "out", (m, n))
         if c.device != dev:
             raise ValueError("out: expected a tensor on %s" % dev)
-    wp, wn = _fp8_product(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
+    ws = _fp8_ws(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm", lib().averis_fp8_gemm(
-        a.c, b.c, offs, nseg, c.data_ptr(), _dtype_code(c), ldc, wp, wn, _stream_on(c)))
+        a.c, b.c, offs, nseg, c.data_ptr(), _dtype_code(c), ldc,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _stream_on(c)))
     return c
 
 
@@ -884,9 +887,11 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
     c = out if out is not None else torch.empty(shape, dtype=out_dtype, device=dev)
     if out is not None and (c.shape != shape or not c.is_contiguous() or c.device != dev):
         raise ValueError("out: expected a contiguous tensor of shape %s on %s" % (shape, dev))
-    wp, wn = _fp8_product(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
+    ws = _fp8_ws(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm_wgrad", lib().averis_fp8_gemm_wgrad(
-        xt.c, dt.c, rows, offs, nseg, c.data_ptr(), _dtype_code(c), n, wp, wn, _stream_on(c)))
+        xt.c, dt.c, rows, offs, nseg, c.data_ptr(), _dtype_code(c), n,
+        ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
+        _stream_on(c)))
     return c
 
 
