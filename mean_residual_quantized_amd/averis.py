@@ -762,20 +762,40 @@ class FP8:
     """Device fp8 tensor with one power-of-two scale for 128 elements along the
     columns: codes u8[rows, cols rounded up to 128] (E4M3, zero past cols),
     scales u8[rows, ceil(cols / 128) rounded up to 4] (E8M0)."""
-    __slots__ = ("codes", "scales", "rows", "cols", "c")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols")
 
     def __init__(self, codes, scales, rows, cols):
-        pitch, spitch = FP8.pitches(cols)
-        if codes.shape != (rows, pitch) or scales.shape != (rows, spitch):
-            raise ValueError("expected codes %s and scales %s" % ((rows, pitch), (rows, spitch)))
-        if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8
-                or not codes.is_contiguous() or not scales.is_contiguous()):
-            raise ValueError("expected contiguous uint8 codes and scales")
-        self._set(codes, scales, rows, cols)
+        self._rows, self._cols = rows, cols
+        self.codes, self.scales = codes, scales
 
-    def _set(self, codes, scales, rows, cols):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
-        self.c = _FP8(codes.data_ptr(), scales.data_ptr(), rows, cols)   # the C descriptor
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @codes.setter
+    def codes(self, t):
+        self._codes = FP8._bytes(t, "codes", (self._rows, FP8.pitches(self._cols)[0]))
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @scales.setter
+    def scales(self, t):
+        self._scales = FP8._bytes(t, "scales", (self._rows, FP8.pitches(self._cols)[1]))
+
+    @staticmethod
+    def _bytes(t, what, shape):
+        if t.shape != shape or t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous uint8 tensor of shape %s" % (what, shape))
+        return t
+
+    def c(self):
+        # formed at each call: the tensors may have been replaced since the last
+        return _FP8(self._codes.data_ptr(), self._scales.data_ptr(), self._rows, self._cols)
 
     @staticmethod
     def pitches(cols):
@@ -786,7 +806,9 @@ class FP8:
     def empty(rows, cols, device="cuda"):
         p, s = FP8.pitches(cols)
         q = FP8.__new__(FP8)
-        q._set(_new(rows, p, torch.uint8, device), _new(rows, s, torch.uint8, device), rows, cols)
+        q._rows, q._cols = rows, cols
+        q._codes = _new(rows, p, torch.uint8, device)
+        q._scales = _new(rows, s, torch.uint8, device)
         return q
 
 
@@ -814,7 +836,7 @@ def averis_fp8_quant(a, transposed=False, offsets=None, plain=True):
         qt = FP8.empty(cols, tc, a.device)
     _check("averis_fp8_quant", lib().averis_fp8_quant(
         a.data_ptr(), _dtype_code(a), rows, cols, lda, offs, nseg,
-        q.c if q is not None else None, qt.c if qt is not None else None, _stream_on(a)))
+        q.c() if q is not None else None, qt.c() if qt is not None else None, _stream_on(a)))
     return (q, qt) if transposed else q
 
 
@@ -830,7 +852,7 @@ def averis_fp8_quant_weight(w):
     wt = FP8.empty(batch * cols, rows, w.device)
     _check("averis_fp8_quant_weight", lib().averis_fp8_quant_weight(
         a.data_ptr(), _dtype_code(a), batch, rows, cols, a.stride(1), a.stride(0),
-        wd.c, wt.c, _stream_on(w)))
+        wd.c(), wt.c(), _stream_on(w)))
     return wt, wd
 
 
@@ -865,7 +887,7 @@ def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=N
             raise ValueError("out: expected a tensor on %s" % dev)
     ws = _fp8_ws(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm", lib().averis_fp8_gemm(
-        a.c, b.c, offs, nseg, c.data_ptr(), _dtype_code(c), ldc,
+        a.c(), b.c(), offs, nseg, c.data_ptr(), _dtype_code(c), ldc,
         ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
         _stream_on(c)))
     return c
@@ -889,7 +911,7 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
         raise ValueError("out: expected a contiguous tensor of shape %s on %s" % (shape, dev))
     ws = _fp8_ws(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm_wgrad", lib().averis_fp8_gemm_wgrad(
-        xt.c, dt.c, rows, offs, nseg, c.data_ptr(), _dtype_code(c), n,
+        xt.c(), dt.c(), rows, offs, nseg, c.data_ptr(), _dtype_code(c), n,
         ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
         _stream_on(c)))
     return c

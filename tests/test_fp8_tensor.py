@@ -1,0 +1,59 @@
+"""What the fp8 calls hand to the library for a tensor of codes and scales (a
+stub in place of the library: no GPU needed)."""
+
+import pytest
+import torch
+
+from mean_residual_quantized_amd import averis as av
+
+REAL = av.lib
+
+
+@pytest.fixture
+def sent(monkeypatch):
+    """The descriptors of the last product."""
+    got = []
+
+    class Stub:
+        def __getattr__(self, name):
+            if name in ("averis_workspace_bytes", "averis_fp8_seg_cols"):
+                return getattr(REAL(), name)
+
+            def call(*args):
+                got[:] = [(a.codes, a.scales, a.rows, a.cols) for a in args if isinstance(a, av._FP8)]
+                return 0
+            return call
+    monkeypatch.setattr(av, "lib", lambda: Stub())
+    monkeypatch.setattr(av, "_stream_on", lambda t: None)
+    return got
+
+
+def describe(q):
+    return q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols
+
+
+@pytest.mark.parametrize("call", [av.averis_fp8_gemm, av.averis_fp8_gemm_wgrad])
+def test_replaced_codes_and_scales_are_the_ones_used(sent, call):
+    a, b = av.FP8.empty(4, 200, "cpu"), av.FP8.empty(8, 200, "cpu")
+    call(a, b)
+    assert sent == [describe(a), describe(b)]
+    a.codes, b.scales = a.codes.clone(), b.scales.clone()
+    call(a, b)
+    assert sent == [describe(a), describe(b)]
+    a.scales.data = a.scales.clone()          # the same tensor, its memory elsewhere
+    call(a, b)
+    assert sent == [describe(a), describe(b)]
+
+
+def test_replacements_are_checked():
+    q = av.FP8.empty(4, 200, "cpu")
+    for bad in (q.codes[:3], q.codes.int(), torch.zeros(4, 512, dtype=torch.uint8)[:, ::2]):
+        with pytest.raises(ValueError):
+            q.codes = bad
+    for bad in (q.scales[:3], q.scales.int(), torch.zeros(4, 8, dtype=torch.uint8)[:, :4]):
+        with pytest.raises(ValueError):
+            q.scales = bad
+    for field in ("rows", "cols"):
+        with pytest.raises(AttributeError):
+            setattr(q, field, 100)
+    assert (q.rows, q.cols) == (4, 200)
