@@ -767,6 +767,8 @@ class FP8:
     def __init__(self, codes, scales, rows, cols):
         self._rows, self._cols = rows, cols
         self.codes, self.scales = codes, scales
+        if codes.device != scales.device:
+            raise ValueError("expected codes and scales on one device")
 
     rows = property(lambda self: self._rows)
     cols = property(lambda self: self._cols)
@@ -858,8 +860,8 @@ def averis_fp8_quant_weight(w):
 
 def _one_device(a, b):
     dev = a.codes.device
-    if b.codes.device != dev:
-        raise ValueError("expected operands on one device")
+    if a.scales.device != dev or b.codes.device != dev or b.scales.device != dev:
+        raise ValueError("expected the operands' codes and scales on one device")
     return dev
 
 

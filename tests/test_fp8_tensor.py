@@ -57,3 +57,17 @@ def test_replacements_are_checked():
         with pytest.raises(AttributeError):
             setattr(q, field, 100)
     assert (q.rows, q.cols) == (4, 200)
+
+
+def test_codes_and_scales_on_one_device(sent):
+    """(meta stands for another device than the CPU.)"""
+    q, far = av.FP8.empty(4, 200, "cpu"), av.FP8.empty(4, 200, "meta")
+    with pytest.raises(ValueError, match="one device"):
+        av.FP8(q.codes, far.scales, 4, 200)
+    half = av.FP8.empty(4, 200, "cpu")
+    half.scales = far.scales
+    for call in (av.averis_fp8_gemm, av.averis_fp8_gemm_wgrad):
+        for a, b in ((half, q), (q, half), (q, far), (far, q)):
+            with pytest.raises(ValueError, match="one device"):
+                call(a, b)
+    assert sent == []
