@@ -646,6 +646,18 @@ def _new(rows, cols, dtype, device):
     return torch.empty_strided((rows, cols), (cols or 1, 1), dtype=dtype, device=device)
 
 
+def _ws(ws, op, dims, dev):
+    """A call's workspace: the caller's, checked to be contiguous memory on dev,
+    a new one, or None where none is needed.  The tensor itself, which the caller
+    holds until its call has returned."""
+    if ws is None:
+        need = workspace_bytes(op, *dims)
+        return _workspace(need, dev) if need else None
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws: expected a contiguous tensor on %s" % dev)
+    return ws
+
+
 def averis_moe_route(logits, topk, renorm=True):
     """Top-k experts of each token and their softmax weights; returns
     (expert_ids int32 [tokens, topk], weights float32 [tokens, topk]).  -inf
@@ -691,9 +703,7 @@ def averis_moe_sort(ids, experts, ws=None):
     offsets = ids.new_empty(experts + 1, dtype=torch.int64)
     pos = torch.empty_like(ids)
     src = ids.new_empty(tokens * topk)
-    need = workspace_bytes(OP_MOE_SORT, tokens * topk, 0, experts)
-    if ws is None and need:
-        ws = _workspace(need, dev)
+    ws = _ws(ws, OP_MOE_SORT, (tokens * topk, 0, experts), dev)
     _check("averis_moe_sort", lib().averis_moe_sort(
         ids.data_ptr(), tokens, topk, experts, offsets.data_ptr(), pos.data_ptr(), src.data_ptr(),
         ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
@@ -865,15 +875,6 @@ def _one_device(a, b):
     return dev
 
 
-def _fp8_ws(ws, op, dims, dev):
-    """The workspace of a product: the caller's, a new one, or None.  The tensor
-    itself, which the caller holds until its call has returned."""
-    if ws is None:
-        need = workspace_bytes(op, *dims)
-        ws = _workspace(need, dev) if need else None
-    return ws
-
-
 def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=None):
     """c = deq(a) deq(b)^T; with offsets the rows of segment s times the s-th
     of the matrices stacked in b."""
@@ -887,7 +888,7 @@ def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=N
         ldc = _matrix(c, c, "out", (m, n))
         if c.device != dev:
             raise ValueError("out: expected a tensor on %s" % dev)
-    ws = _fp8_ws(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
+    ws = _ws(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm", lib().averis_fp8_gemm(
         a.c(), b.c(), offs, nseg, c.data_ptr(), _dtype_code(c), ldc,
         ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
@@ -911,7 +912,7 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
     c = out if out is not None else torch.empty(shape, dtype=out_dtype, device=dev)
     if out is not None and (c.shape != shape or not c.is_contiguous() or c.device != dev):
         raise ValueError("out: expected a contiguous tensor of shape %s on %s" % (shape, dev))
-    ws = _fp8_ws(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
+    ws = _ws(ws, OP_FP8_WGRAD, (m, rows, n, 0 if offsets is None else nseg), dev)
     _check("averis_fp8_gemm_wgrad", lib().averis_fp8_gemm_wgrad(
         xt.c(), dt.c(), rows, offs, nseg, c.data_ptr(), _dtype_code(c), n,
         ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
@@ -944,8 +945,7 @@ def _grad_call(grads, out, ws):
     arr = _grad_list(grads, out)
     dev = grads[0].device if len(grads) else "cuda"
     norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws = ws if ws is not None else _workspace(workspace_bytes(OP_GRAD_NORM, 0, 0, len(grads)), dev)
-    return arr, norm, ws
+    return arr, norm, _ws(ws, OP_GRAD_NORM, (0, 0, len(grads)), norm.device)
 
 
 def averis_grad_norm(grads, ws=None):

@@ -94,3 +94,26 @@ CALLS = {
 def test_workspace_lives_through_the_call(stub, name):
     CALLS[name]()
     assert stub.alive and all(stub.alive)
+
+
+GIVEN = {
+    "averis_fp8_gemm": lambda ws: av.averis_fp8_gemm(fp8(1024, 1 << 14), fp8(1024, 1 << 14), ws=ws),
+    "averis_fp8_gemm_wgrad": lambda ws: av.averis_fp8_gemm_wgrad(fp8(1024, 1 << 14), fp8(1024, 1 << 14), ws=ws),
+    "averis_moe_sort": lambda ws: av.averis_moe_sort(torch.zeros(5000, 4, dtype=torch.int32), 16, ws=ws),
+    "averis_grad_norm": lambda ws: av.averis_grad_norm([X], ws=ws),
+    "averis_grad_clip": lambda ws: av.averis_grad_clip([X], 1.0, ws=ws),
+}
+
+
+@pytest.mark.parametrize("name", sorted(GIVEN))
+def test_given_workspace_is_checked(stub, name):
+    """The caller's workspace: contiguous memory where the other tensors are
+    (meta stands for another device), or a refusal before the library call."""
+    flat = torch.zeros(1 << 20, dtype=torch.uint8)
+    stub.made.append(weakref.ref(flat))
+    for bad in (flat.to("meta"), flat[::2], flat[:1].expand(1 << 20)):
+        with pytest.raises(ValueError, match="ws"):
+            GIVEN[name](bad)
+    assert not stub.alive
+    GIVEN[name](flat)
+    assert stub.alive == [True]
