@@ -599,9 +599,9 @@ __global__ void k_zero_offsets(int64_t* offsets, int count) {
 // ---------------------------------------------------------------------------
 // Token exchange.  blockDim.x lanes (whole wavefronts) go along a token's
 // columns in 16-byte pieces, blockDim.y tokens to a workgroup.  Rows outside
-// the tokens * topk there are, which only malformed positions name, are
-// neither read nor written.  All four are bound by memory: a row is read or
-// written once, whole, in lines; sums are fp32, rounded once.
+// the slots there are (those of all the call's launches), which only malformed
+// positions name, are neither read nor written.  All four are bound by memory:
+// a row is read or written once, whole, in lines; sums are fp32, rounded once.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
@@ -617,12 +617,11 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_dispatch(const T* __restrict__ x, int64_t tokens,
                                                   int64_t cols, int64_t ldx,
                                                   const int32_t* __restrict__ pos, int topk,
-                                                  T* __restrict__ rows, int64_t ldr) {
+                                                  T* __restrict__ rows, int64_t ldr, int64_t slots) {
   constexpr int P = Elem<T>::kPer;
   const int64_t t = uniform64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= tokens) return;
   const int32_t* pt = pos + t * topk;
-  const int64_t slots = tokens * topk;
   for (int64_t c = (int64_t)threadIdx.x * P; c < cols; c += (int64_t)blockDim.x * P) {
     const u32x4_t v = load_piece(x + t * ldx, c, cols);
     for (int j = 0; j < topk; ++j) {
@@ -640,11 +639,10 @@ __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ rows, int
                                                  int64_t cols, int64_t ldr,
                                                  const int32_t* __restrict__ pos,
                                                  const float* __restrict__ weights, int topk,
-                                                 T* __restrict__ y, int64_t ldy) {
+                                                 T* __restrict__ y, int64_t ldy, int64_t slots) {
   constexpr int P = Elem<T>::kPer, U = 8;
   const int64_t t = uniform64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= tokens) return;
-  const int64_t slots = tokens * topk;
   for (int64_t c = (int64_t)threadIdx.x * P; c < cols; c += (int64_t)blockDim.x * P) {
     float acc[P];
 #pragma unroll
@@ -679,17 +677,17 @@ __global__ __launch_bounds__(256) void k_combine(const T* __restrict__ rows, int
 // wavefront a slot, neighbouring slots share dy_t through the cache.  4096
 // tokens, top 8, 2048 bf16: 50.9 us (285 MB, 5.6 TB/s).
 template <typename T>
-__global__ __launch_bounds__(256) void k_combine_grad(const T* __restrict__ dy, int64_t slots,
+__global__ __launch_bounds__(256) void k_combine_grad(const T* __restrict__ dy, int64_t here,
                                                       int64_t cols, int64_t ldy,
                                                       const T* rows, int64_t ldr,
                                                       const int32_t* __restrict__ pos,
                                                       const float* __restrict__ weights, int topk,
                                                       T* drows, int64_t lddr,
-                                                      float* __restrict__ dweights) {
+                                                      float* __restrict__ dweights, int64_t slots) {
   constexpr int P = Elem<T>::kPer;
   const int lane = threadIdx.x & 63;
   const uint32_t s = __builtin_amdgcn_readfirstlane(blockIdx.x * 4u + (threadIdx.x >> 6));
-  if (s >= (uint64_t)slots) return;
+  if (s >= (uint64_t)here) return;
   const int p = pos[s];
   const bool kept = p >= 0 && p < slots;
   const int64_t r = p < 0 ? ~p : p;
@@ -755,12 +753,22 @@ dim3 exchange_block(int64_t cols, int per) {
     CALL(64, 16);                      \
   }
 
+// A grid has fewer than 2^32 threads (workgroups of 256 here): f(first, many)
+// for each launch of n tokens, `per` of them a workgroup.
+template <typename F>
+static void in_launches(int64_t n, int64_t per, F f) {
+  const int64_t most = ((1 << 24) - 1) * per;
+  for (int64_t i = 0; i < n; i += most) f(i, n - i < most ? n - i : most);
+}
+
 template <typename T>
 static void route_t(const T* l, int64_t tokens, int experts, int64_t ld, int topk, bool renorm,
                     int32_t* ids, float* w, hipStream_t st) {
 #define AVERIS_ROUTE(G, V)                                                                      \
-  k_route<T, G, V><<<dim3((unsigned)((tokens + 256 / G - 1) / (256 / G))), 256, 0, st>>>(        \
-      l, tokens, experts, ld, topk, renorm, ids, w)
+  in_launches(tokens, 256 / G, [&](int64_t t, int64_t n) {                                      \
+    k_route<T, G, V><<<dim3((unsigned)((n + 256 / G - 1) / (256 / G))), 256, 0, st>>>(           \
+        l + t * ld, n, experts, ld, topk, renorm, ids + t * topk, w + t * topk);                \
+  })
   AVERIS_ROUTE_SHAPES(AVERIS_ROUTE)
 #undef AVERIS_ROUTE
 }
@@ -770,8 +778,11 @@ static void route_grad_t(const T* l, int64_t tokens, int experts, int64_t ld, in
                          bool renorm, const int32_t* ids, const float* dw, T* dl, int64_t ldd,
                          hipStream_t st) {
 #define AVERIS_ROUTE(G, V)                                                                      \
-  k_route_grad<T, G, V><<<dim3((unsigned)((tokens + 256 / G - 1) / (256 / G))), 256, 0, st>>>(   \
-      l, tokens, experts, ld, topk, renorm, ids, dw, dl, ldd)
+  in_launches(tokens, 256 / G, [&](int64_t t, int64_t n) {                                      \
+    k_route_grad<T, G, V><<<dim3((unsigned)((n + 256 / G - 1) / (256 / G))), 256, 0, st>>>(      \
+        l + t * ld, n, experts, ld, topk, renorm, ids + t * topk, dw + t * topk, dl + t * ldd,  \
+        ldd);                                                                                   \
+  })
   AVERIS_ROUTE_SHAPES(AVERIS_ROUTE)
 #undef AVERIS_ROUTE
 }
@@ -841,18 +852,25 @@ hipError_t launch_moe_sort(const int32_t* ids, int64_t slots, int experts, int64
   return hipGetLastError();
 }
 
+template <typename T>
+static void dispatch_t(const void* x, int64_t tokens, int64_t cols, int64_t ldx, const int32_t* pos,
+                       int topk, void* rows, int64_t ldr, hipStream_t st) {
+  const dim3 b = exchange_block(cols, Elem<T>::kPer);
+  in_launches(tokens, b.y, [&](int64_t t, int64_t n) {
+    k_dispatch<T><<<dim3((unsigned)((n + b.y - 1) / b.y)), b, 0, st>>>(
+        static_cast<const T*>(x) + t * ldx, n, cols, ldx, pos + t * topk, topk,
+        static_cast<T*>(rows), ldr, tokens * topk);
+  });
+}
+
 hipError_t launch_moe_dispatch(const void* x, bool bf16, int64_t tokens, int64_t cols, int64_t ldx,
                                const int32_t* pos, int topk, void* rows, int64_t ldr,
                                hipStream_t st) {
   if (tokens == 0) return hipSuccess;
-  const dim3 b = exchange_block(cols, bf16 ? 8 : 4);
-  const dim3 g((unsigned)((tokens + b.y - 1) / b.y));
   if (bf16)
-    k_dispatch<uint16_t><<<g, b, 0, st>>>(static_cast<const uint16_t*>(x), tokens, cols, ldx, pos,
-                                          topk, static_cast<uint16_t*>(rows), ldr);
+    dispatch_t<uint16_t>(x, tokens, cols, ldx, pos, topk, rows, ldr, st);
   else
-    k_dispatch<float><<<g, b, 0, st>>>(static_cast<const float*>(x), tokens, cols, ldx, pos, topk,
-                                       static_cast<float*>(rows), ldr);
+    dispatch_t<float>(x, tokens, cols, ldx, pos, topk, rows, ldr, st);
   return hipGetLastError();
 }
 
@@ -861,13 +879,17 @@ static void combine_t(const void* rows, int64_t tokens, int64_t cols, int64_t ld
                       const int32_t* pos, const float* weights, int topk, void* y, int64_t ldy,
                       hipStream_t st) {
   const dim3 b = exchange_block(cols, Elem<T>::kPer);
-  const dim3 g((unsigned)((tokens + b.y - 1) / b.y));
-  if (weights)
-    k_combine<T, true><<<g, b, 0, st>>>(static_cast<const T*>(rows), tokens, cols, ldr, pos,
-                                        weights, topk, static_cast<T*>(y), ldy);
-  else
-    k_combine<T, false><<<g, b, 0, st>>>(static_cast<const T*>(rows), tokens, cols, ldr, pos,
-                                         nullptr, topk, static_cast<T*>(y), ldy);
+  in_launches(tokens, b.y, [&](int64_t t, int64_t n) {
+    const dim3 g((unsigned)((n + b.y - 1) / b.y));
+    const T* r = static_cast<const T*>(rows);
+    T* out = static_cast<T*>(y) + t * ldy;
+    if (weights)
+      k_combine<T, true><<<g, b, 0, st>>>(r, n, cols, ldr, pos + t * topk, weights + t * topk, topk,
+                                          out, ldy, tokens * topk);
+    else
+      k_combine<T, false><<<g, b, 0, st>>>(r, n, cols, ldr, pos + t * topk, nullptr, topk, out, ldy,
+                                           tokens * topk);
+  });
 }
 
 hipError_t launch_moe_combine(const void* rows, bool bf16, int64_t tokens, int64_t cols,
@@ -885,10 +907,15 @@ template <typename T>
 static void combine_grad_t(const void* dy, int64_t tokens, int64_t cols, int64_t ldy,
                            const void* rows, int64_t ldr, const int32_t* pos, const float* weights,
                            int topk, void* drows, int64_t lddr, float* dweights, hipStream_t st) {
-  const int64_t slots = tokens * topk;
-  k_combine_grad<T><<<dim3((unsigned)((slots + 3) / 4)), 256, 0, st>>>(
-      static_cast<const T*>(dy), slots, cols, ldy, static_cast<const T*>(rows), ldr, pos, weights,
-      topk, static_cast<T*>(drows), lddr, dweights);
+  // whole tokens a launch: as many as have four slots for each workgroup (topk <= 32)
+  const int64_t most = (int64_t)((1 << 24) - 1) * 4 / topk;
+  for (int64_t t = 0; t < tokens; t += most) {
+    const int64_t here = (tokens - t < most ? tokens - t : most) * topk;
+    k_combine_grad<T><<<dim3((unsigned)((here + 3) / 4)), 256, 0, st>>>(
+        static_cast<const T*>(dy) + t * ldy, here, cols, ldy, static_cast<const T*>(rows), ldr,
+        pos + t * topk, weights + t * topk, topk, static_cast<T*>(drows), lddr, dweights + t * topk,
+        tokens * topk);
+  }
 }
 
 hipError_t launch_moe_combine_grad(const void* dy, bool bf16, int64_t tokens, int64_t cols,
