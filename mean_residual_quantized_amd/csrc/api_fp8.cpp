@@ -76,8 +76,6 @@ averis_status_t averis_fp8_quant(const void* a, averis_dtype_t dtype, int64_t ro
     return hip_status(launch_fp8_tile(a, dtype == AVERIS_BF16, false, 1, rows, cols, lda, 0,
                                       seg_offsets, nseg, out_of(out), out_of(out_t), stream));
   }
-  // a launch of one wavefront for every 4 rows x 512 columns
-  if ((rows + 3) / 4 * ((cols + 511) / 512) >= 1 << 26) return AVERIS_E_SHAPE;
   return hip_status(launch_fp8_rows(a, dtype == AVERIS_BF16, rows, cols, lda, out_of(out), stream));
 }
 

@@ -344,15 +344,23 @@ hipError_t tile_t(const void* a, int batch, int64_t rows, int64_t cols, int64_t 
 hipError_t launch_fp8_rows(const void* a, bool bf16, int64_t rows, int64_t cols, int64_t lda,
                            const Fp8Out& out, hipStream_t st) {
   if (rows == 0) return hipSuccess;
-  const int groups = (int)((cols + 511) / 512);
-  const int64_t tasks = (rows + kRowsPerWave - 1) / kRowsPerWave * groups;
-  const dim3 g((unsigned)((tasks + 3) / 4));
-  if (bf16)
-    k_fp8_rows<uint16_t><<<g, 256, 0, st>>>(static_cast<const uint16_t*>(a), rows, cols, lda,
-                                            groups, out.codes, out.pitch, out.scales, out.spitch);
-  else
-    k_fp8_rows<float><<<g, 256, 0, st>>>(static_cast<const float*>(a), rows, cols, lda, groups,
-                                         out.codes, out.pitch, out.scales, out.spitch);
+  const int64_t groups = (cols + 511) / 512;
+  // a grid has fewer than 2^32 threads: 2^24 - 1 workgroups of four tasks each;
+  // further rows in further launches (groups <= 2^21)
+  const int64_t most = (int64_t)((1 << 24) - 1) * 4 / groups * kRowsPerWave;
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t here = rows - r < most ? rows - r : most;
+    const int64_t tasks = (here + kRowsPerWave - 1) / kRowsPerWave * groups;
+    const dim3 g((unsigned)((tasks + 3) / 4));
+    uint8_t* codes = out.codes + r * out.pitch;
+    uint8_t* scales = out.scales + r * out.spitch;
+    if (bf16)
+      k_fp8_rows<uint16_t><<<g, 256, 0, st>>>(static_cast<const uint16_t*>(a) + r * lda, here, cols,
+                                              lda, (int)groups, codes, out.pitch, scales, out.spitch);
+    else
+      k_fp8_rows<float><<<g, 256, 0, st>>>(static_cast<const float*>(a) + r * lda, here, cols, lda,
+                                           (int)groups, codes, out.pitch, scales, out.spitch);
+  }
   return hipGetLastError();
 }
 
