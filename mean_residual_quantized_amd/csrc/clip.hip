@@ -6,9 +6,14 @@
 // Both passes walk the same 32 KiB chunks of the listed tensors.  A launch
 // takes a table of up to kClipTensors tensors by value (nothing is copied to
 // the device first); a workgroup finds its next chunk's tensor from its last
-// one's.  The first pass leaves one fp64 partial per workgroup; every workgroup
-// of the second sums all the partials itself, in the same fixed order, so there
-// is no launch between the two, no atomic, and the same bits on every call.
+// one's.  The first pass leaves one fp64 partial per workgroup.  Up to
+// kClipTensors tensors (one launch a pass, at most 16 KB of partials) every
+// workgroup of the second pass sums them all itself, and there is no launch
+// between the two; past that one workgroup does it once, since partials and
+// workgroups both grow with the launches (graph replay, all summed by each /
+// once: 2 launches of 256 tensors of 100 24.8 / 25.2 us, 2000 tensors of 256 KB
+// 601 / 431 us, 12000 of 512 KB 21.3 / 4.0 ms).  The order is the same and
+// fixed: no atomic, and the same bits on every call.
 // Squares and sums are fp64: exact squares, and no overflow for any finite
 // gradient.
 //
@@ -17,8 +22,7 @@
 // them, last chunk first, so that what the first pass read last is taken from
 // the last-level cache.  1 GiB of fp32 in 310 tensors: 0.18 ms (6.1
 // TB/s) and 0.41 ms (5.3 TB/s); 7 bf16 tensors of 31 MB together: 9 and 16 us.
-// Up to 2048 workgroups: eight on a CU keep enough loads in flight, and the
-// partials (16 KB) stay in every CU's reach.
+// Up to 2048 workgroups a launch: eight on a CU keep enough loads in flight.
 #include <hip/hip_runtime.h>
 #include <alloca.h>
 #include <stdint.h>
@@ -174,11 +178,16 @@ __device__ __forceinline__ double norm_of(const double* part, int parts, double*
   return sqrt(block_sum((s[0] + s[1]) + (s[2] + s[3]), sh));
 }
 
+// whole (optional): the norm before its rounding
 __global__ __launch_bounds__(kClipThreads) void k_norm(const double* __restrict__ part, int parts,
-                                                       float* __restrict__ norm) {
+                                                       float* __restrict__ norm,
+                                                       double* __restrict__ whole) {
   __shared__ double sh[4];
   const double r = norm_of(part, parts, sh);
-  if (threadIdx.x == 0) *norm = (float)r;
+  if (threadIdx.x == 0) {
+    *norm = (float)r;
+    if (whole) *whole = r;
+  }
 }
 
 __device__ __forceinline__ u32x4_t scaled(u32x4_t v, bool bf16, float coef) {
@@ -189,6 +198,7 @@ __device__ __forceinline__ u32x4_t scaled(u32x4_t v, bool bf16, float coef) {
   return v;
 }
 
+// parts 0: part holds the norm itself
 __global__ __launch_bounds__(kClipThreads) void k_clip(ClipTable t, const double* __restrict__ part,
                                                        int parts, double max_norm, double eps,
                                                        float* __restrict__ norm) {
@@ -199,7 +209,7 @@ __global__ __launch_bounds__(kClipThreads) void k_clip(ClipTable t, const double
   Chunk k = chunk_of(t, (uint32_t)c, i);
   u32x4_t v[kClipPieces];
   load_chunk(k, v);
-  const double r = norm_of(part, parts, sh);
+  const double r = parts > 0 ? norm_of(part, parts, sh) : *part;
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
   const double c64 = max_norm / (r + eps);
   const float coef = c64 > 1.0 ? 1.0f : (float)c64;   // NaN stays NaN
@@ -264,7 +274,7 @@ inline unsigned clip_grid(const ClipTable& t) {
 
 size_t grad_norm_ws_bytes(int n) {
   const size_t launches = ((size_t)n + kClipTensors - 1) / kClipTensors;
-  return (launches ? launches : 1) * kClipBlocks * sizeof(double);
+  return ((launches ? launches : 1) * kClipBlocks + 1) * sizeof(double);   // partials, the norm
 }
 
 hipError_t launch_grad_clip(int n, const GradTensor* w, bool scale, double max_norm, double eps,
@@ -282,9 +292,15 @@ hipError_t launch_grad_clip(int n, const GradTensor* w, bool scale, double max_n
     k_square_sums<<<g, kClipThreads, 0, st>>>(t, part + parts);
     parts += (int)g;
   }
-  if (!scale || parts == 0) {
-    k_norm<<<1, kClipThreads, 0, st>>>(part, parts, norm);
-    return hipGetLastError();
+  double* whole = launches > 1 ? part + parts : nullptr;
+  if (!scale || parts == 0 || whole) {
+    k_norm<<<1, kClipThreads, 0, st>>>(part, parts, norm, whole);
+    if (!scale || parts == 0) return hipGetLastError();
+    if (whole) {
+      part = whole;
+      parts = 0;
+      norm = nullptr;
+    }
   }
   // the last launch's tensors first: what was read last
   for (int l = launches - 1; l >= 0; --l) {
