@@ -1,7 +1,7 @@
 // The global norm over a list of gradients and the clipped gradients.
 //
 //   norm = sqrt(sum over tensors and elements of g^2)
-//   coef = min(1, max_norm / (norm + eps)),  out = g coef
+//   coef = min(1, max_norm / (norm + eps)) (1 for 0 / 0),  out = g coef
 //
 // Both passes walk the same 32 KiB chunks of the listed tensors.  A launch
 // takes a table of up to kClipTensors tensors by value (nothing is copied to
@@ -211,7 +211,8 @@ __global__ __launch_bounds__(kClipThreads) void k_clip(ClipTable t, const double
   load_chunk(k, v);
   const double r = parts > 0 ? norm_of(part, parts, sh) : *part;
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
-  const double c64 = max_norm / (r + eps);
+  // (a norm of 0 without eps leaves zeros as they are)
+  const double c64 = r + eps == 0.0 ? 1.0 : max_norm / (r + eps);
   const float coef = c64 > 1.0 ? 1.0f : (float)c64;   // NaN stays NaN
   while (true) {
     if (coef != 1.0f || k.g != k.out) {   // else in place and unchanged

@@ -1,4 +1,5 @@
-"""The gradient norm and clipping over thousands of tensors (many launches)."""
+"""The gradient norm and clipping over thousands of tensors (many launches),
+and at the edges of norm, max_norm and eps."""
 
 import numpy as np
 import pytest
@@ -61,3 +62,15 @@ def test_clipping_grows_with_the_data_alone():
             best = min(best, start.elapsed_time(end))
         times.append(best)
     assert times[1] < 6.0 * times[0], times
+
+
+@pytest.mark.parametrize("n", [1, 200])
+def test_zero_gradients_without_eps(n):
+    """0 / 0 is no factor: gradients of zero stay zero."""
+    for max_norm in (0.0, 1.0, float("inf")):
+        grads = [torch.zeros(1000, device="cuda") for _ in range(n)]
+        out = [torch.full_like(g, 9.0) for g in grads]
+        assert float(av.averis_grad_clip(grads, max_norm, eps=0.0, out=out)) == 0.0
+        assert all(bool((o == 0).all()) for o in out)
+        av.averis_grad_clip(grads, max_norm, eps=0.0)
+        assert all(bool((g == 0).all()) for g in grads)
