@@ -631,7 +631,8 @@ averis_status_t averis_grad_norm(int n, const averis_grad_t* grads, float* norm,
                                  size_t ws_bytes, hipStream_t stream);
 
 /* averis_grad_norm, and out = grad * min(1, max_norm / (norm + eps)) for each
- * tensor, rounded once.  A norm that is not finite is not hidden: an infinite
+ * tensor: the factor rounded to fp32's 24 bits, the product rounded to fp32
+ * and, for BF16, from there.  A norm that is not finite is not hidden: an infinite
  * one scales by 0 (which leaves NaN in place of infinite elements; by NaN if
  * max_norm is infinite too), NaN scales by NaN.  max_norm, eps >= 0; with
  * norm + eps = 0 the gradients, all zero, stay so. */

@@ -190,11 +190,12 @@ __global__ __launch_bounds__(kClipThreads) void k_norm(const double* __restrict_
   }
 }
 
-__device__ __forceinline__ u32x4_t scaled(u32x4_t v, bool bf16, float coef) {
+// times pre coef
+__device__ __forceinline__ u32x4_t scaled(u32x4_t v, bool bf16, float pre, float coef) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    v[j] = bf16 ? bf16x2_rne(bf16_lo(v[j]) * coef, bf16_hi(v[j]) * coef)
-                : __float_as_uint(__uint_as_float(v[j]) * coef);
+    v[j] = bf16 ? bf16x2_rne(bf16_lo(v[j]) * pre * coef, bf16_hi(v[j]) * pre * coef)
+                : __float_as_uint(__uint_as_float(v[j]) * pre * coef);
   return v;
 }
 
@@ -213,11 +214,15 @@ __global__ __launch_bounds__(kClipThreads) void k_clip(ClipTable t, const double
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)r;
   // (a norm of 0 without eps leaves zeros as they are)
   const double c64 = r + eps == 0.0 ? 1.0 : max_norm / (r + eps);
-  const float coef = c64 > 1.0 ? 1.0f : (float)c64;   // NaN stays NaN
+  // A factor that is no normal fp32 number would lose bits (a norm past 2^126
+  // max_norm: finite gradients reach 2^148): a power of two, which is exact on
+  // every value that does not end below fp32's range, takes 2^-64 of it.
+  const float pre = c64 < 0x1p-64 ? 0x1p-64f : 1.0f;
+  const float coef = c64 > 1.0 ? 1.0f : (float)(c64 < 0x1p-64 ? c64 * 0x1p64 : c64);   // NaN stays NaN
   while (true) {
     if (coef != 1.0f || k.g != k.out) {   // else in place and unchanged
 #pragma unroll
-      for (int p = 0; p < kClipPieces; ++p) v[p] = scaled(v[p], k.bf16, coef);
+      for (int p = 0; p < kClipPieces; ++p) v[p] = scaled(v[p], k.bf16, pre, coef);
       if (k.bytes == kClipBytes) {
         char* o = k.out + threadIdx.x * 16;
 #pragma unroll

@@ -74,3 +74,23 @@ def test_zero_gradients_without_eps(n):
         assert all(bool((o == 0).all()) for o in out)
         av.averis_grad_clip(grads, max_norm, eps=0.0)
         assert all(bool((g == 0).all()) for g in grads)
+
+
+@pytest.mark.parametrize("max_norm", [1.0, 1e-3, 1e6])
+@pytest.mark.parametrize("value", [3e38, 1.7e35, 1e20])
+def test_factors_below_fp32s_normal_numbers(value, max_norm):
+    """Norms up to 2^138: the factor, under 2^-126 for the largest, keeps its 24
+    bits (2^-23 with the product's rounding; the norm's own is 2^-53)."""
+    n = 1 << 20
+    g = torch.full((n,), value, device="cuda")
+    g[1::2] *= 2.0 ** -20
+    ref = g.double().cpu().numpy()
+    ref = ref * (max_norm / (np.sqrt(np.sum(ref ** 2)) + 1e-6))
+    out = torch.empty_like(g)
+    av.averis_grad_clip([g], max_norm, out=[out])
+    assert np.all(np.abs(out.double().cpu().numpy() - ref) <= 1.01 * 2.0 ** -23 * np.abs(ref))
+    b = g.to(torch.bfloat16)
+    ref = b.double().cpu().numpy()
+    ref = ref * (max_norm / (np.sqrt(np.sum(ref ** 2)) + 1e-6))
+    av.averis_grad_clip([b], max_norm)
+    assert np.all(np.abs(b.double().cpu().numpy() - ref) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(ref))
