@@ -274,7 +274,8 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int
     const int j = o * G + g;
     if (live && j < topk) {
       ids[t * topk + j] = id[o];
-      weights[t * topk + j] = val[o] / total;
+      // (without an expert 0, also where a NaN or an infinity makes the others' NaN)
+      weights[t * topk + j] = id[o] < 0 ? 0.0f : val[o] / total;
     }
   }
 }
