@@ -28,6 +28,11 @@ __device__ __forceinline__ uint32_t f8_scale_byte(uint32_t amax_bits) {
 __device__ __forceinline__ bool f8_not_finite(uint32_t amax_bits) { return amax_bits >= 0x7F800000u; }
 constexpr uint32_t kF8NanCodes = 0x7F7F7F7Fu;
 constexpr uint32_t kF8One = 127;
+// four codes of which the first `left` are elements, the rest pad: 0 (as they
+// are already, but in a block of NaN codes)
+__device__ __forceinline__ uint32_t f8_without_pad(uint32_t codes, int left) {
+  return left >= 4 ? codes : left > 0 ? codes & (0xFFFFFFFFu >> (8 * (4 - left))) : 0u;
+}
 
 // four fp32 values times 2^(127 - byte) -> four codes.  The product is exact:
 // it is at most 448, and what falls below fp32's range is far below half the

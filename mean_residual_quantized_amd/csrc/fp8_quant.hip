@@ -91,6 +91,12 @@ __device__ __forceinline__ u32x2_t eight_codes(const Eight<T>& v, uint32_t amax,
   return v.codes(byte);
 }
 
+// the codes of eight elements from column c on, those past the row's end 0
+__device__ __forceinline__ u32x2_t without_pad(u32x2_t q, int64_t c, int64_t cols) {
+  const int left = (int)(cols - c < 8 ? cols - c : 8);
+  return u32x2_t{f8_without_pad(q[0], left), f8_without_pad(q[1], left - 4)};
+}
+
 // A wavefront takes 512 columns (four blocks, sixteen lanes each, eight
 // elements a lane) of kRowsPerWave rows: all rows' loads in flight, then per
 // row the blocks' maxima by four DPP steps, the codes (8 bytes a lane, 512
@@ -119,7 +125,8 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const T* __restrict__ a, int64
 #pragma unroll
   for (int i = 0; i < kRowsPerWave; ++i) {
     uint32_t byte;
-    const u32x2_t q = eight_codes(v[i], row16_max(v[i].amax()), byte);
+    u32x2_t q = eight_codes(v[i], row16_max(v[i].amax()), byte);
+    if (512 * (int64_t)(g + 1) > cols) q = without_pad(q, c, cols);
     const uint32_t word = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
                           __builtin_amdgcn_readlane(byte, 32) << 16 |
                           __builtin_amdgcn_readlane(byte, 48) << 24;
@@ -212,7 +219,8 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
     for (int p = 0; p < PER; ++p) {
       uint32_t byte;
       const uint32_t m = TILE ? tile_max : row16_max(v[p].amax());
-      const u32x2_t q = eight_codes(v[p], m, byte);
+      u32x2_t q = eight_codes(v[p], m, byte);
+      if (c0 + 128 > cols) q = without_pad(q, c0 + 8 * i, cols);
       if (r + STEP * p < nr) {
         *reinterpret_cast<u32x2_t*>(out.codes + (row0 + STEP * p) * out.pitch + c0 + 8 * i) = q;
         if (i == 0) out.scales[(row0 + STEP * p) * out.spitch + block] = (uint8_t)byte;
@@ -275,6 +283,14 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
         if (f8_not_finite(m0)) y0[q] = kF8NanCodes;
         if (f8_not_finite(m1)) y1[q] = kF8NanCodes;
       }
+      if (nr < 128) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int left = nr - (WR * w + 16 * h + 4 * q);
+          y0[q] = f8_without_pad(y0[q], left);
+          y1[q] = f8_without_pad(y1[q], left);
+        }
+      }
       put(2 * lane, WR / 16 * w + h, y0);
       put(2 * lane + 1, WR / 16 * w + h, y1);
     }
@@ -306,6 +322,10 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
       for (int q = 0; q < 4; ++q) {
         const float* z = src + (16 * h + 4 * q) * 128;
         y[q] = f8_not_finite(m) ? kF8NanCodes : f8_codes4(z[0], z[128], z[256], z[384], byte);
+      }
+      if (nr < 128) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = f8_without_pad(y[q], nr - (PR * part + 16 * h + 4 * q));
       }
       put(col, PR / 16 * part + h, y);
     }
