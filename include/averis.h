@@ -568,7 +568,8 @@ int64_t averis_fp8_seg_cols(int64_t rows, int64_t nseg);
  * with nseg = 1: with segments out_t is cols x averis_fp8_seg_cols(rows,
  * nseg), segment s from the multiple of 128 after those before it, the rest
  * of its last run 0; with out_t and segments, rows outside every segment are
- * not written to out. */
+ * not written to out.  rows, cols <= 2^30; with out_t fewer than 2^23 tiles of
+ * 128 x 128 (with segments, for any division of the rows). */
 averis_status_t averis_fp8_quant(const void* a, averis_dtype_t dtype, int64_t rows, int64_t cols,
                                  int64_t lda, const int64_t* seg_offsets, int nseg,
                                  const averis_fp8_t* out, const averis_fp8_t* out_t,
@@ -587,9 +588,10 @@ averis_status_t averis_fp8_quant_weight(const void* w, averis_dtype_t dtype, int
 /* c = deq(a) deq(b)^T: a m x k, b n x k, c m x n (F32 or BF16, row stride
  * ldc).  With seg_offsets: rows of segment s times the s-th of nseg stacked n
  * x k matrices b (rows of a outside every segment give no output).  Forward:
- * a = Q(X), b = out_t of the weight; dgrad: a = Q(D), b = out of it.  From
- * one row (a token) to 2^23.  Workspace: AVERIS_OP_FP8_GEMM (m, k, n, nseg
- * or 0 without segments; may be 0 bytes). */
+ * a = Q(X), b = out_t of the weight; dgrad: a = Q(D), b = out of it.  m (from
+ * one row, a token) and n <= 2^30, k <= 2^22, at most 2^30 tiles of 128 x 128.
+ * Workspace: AVERIS_OP_FP8_GEMM (m, k, n, nseg or 0 without segments; may be 0
+ * bytes). */
 averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
                                 const int64_t* seg_offsets, int nseg, void* c,
                                 averis_dtype_t cdtype, int64_t ldc, void* ws, size_t ws_bytes,
@@ -600,8 +602,12 @@ averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
  * seg_offsets (those of the quantization; xt and dt then have
  * averis_fp8_seg_cols(rows, nseg) columns): nseg matrices one after the
  * other, matrix s (at dw + s * m * lddw elements) over segment s's tokens;
- * zeros for a segment without any.  Workspace: AVERIS_OP_FP8_WGRAD (m, rows,
- * n, nseg or 0). */
+ * zeros for a segment without any.  At most 2^22 rows (with segments,
+ * averis_fp8_seg_cols of them: each segment's last run counts whole), which is
+ * fewer than averis_fp8_quant takes: longer ones go in parts, added in F32.  m, n
+ * <= 2^30, at most 2^30 tiles of 128 x 128 (with segments fewer than 2^24, of
+ * all their matrices).  Workspace: AVERIS_OP_FP8_WGRAD (m, rows, n, nseg or
+ * 0). */
 averis_status_t averis_fp8_gemm_wgrad(const averis_fp8_t* xt, const averis_fp8_t* dt,
                                       int64_t rows, const int64_t* seg_offsets, int nseg,
                                       void* dw, averis_dtype_t dwdtype, int64_t lddw, void* ws,

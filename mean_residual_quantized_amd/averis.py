@@ -877,7 +877,7 @@ def _one_device(a, b):
 
 def averis_fp8_gemm(a, b, out_dtype=torch.bfloat16, offsets=None, out=None, ws=None):
     """c = deq(a) deq(b)^T; with offsets the rows of segment s times the s-th
-    of the matrices stacked in b."""
+    of the matrices stacked in b.  Up to 2^30 rows, and 2^22 columns (k)."""
     dev = _one_device(a, b)
     offs, nseg = _segments(offsets, a.codes)
     m, k, n = a.rows, a.cols, b.rows // nseg
@@ -901,7 +901,8 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
     """dw = deq(xt) deq(dt)^T over the tokens (m x n), from averis_fp8_quant's
     transposed copies; with the offsets of the quantization and its number of
     rows (by default the largest that the copies can hold) one matrix a
-    segment (nseg x m x n)."""
+    segment (nseg x m x n).  Up to 2^22 tokens, each segment's last run of 128
+    counted whole (fewer than averis_fp8_quant takes)."""
     dev = _one_device(xt, dt)
     offs, nseg = _segments(offsets, xt.codes)
     m, n = xt.rows, dt.rows

@@ -2,6 +2,7 @@
 // Every check runs before the first HIP call.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "api_common.hpp"
@@ -13,8 +14,8 @@ using namespace averis;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;   // rows and columns of one operand
-constexpr int64_t kMaxGridY = 65535;
-constexpr int64_t kMaxTiles = (1 << 23) - 1;   // of 128 x 128: below 2^32 threads
+constexpr int64_t kMaxK = kMaxDim / 256;        // a tile's 256 rows of codes in 32-bit offsets
+constexpr int64_t kMaxTiles = (1 << 23) - 1;   // of 128 x 128, 512 threads each: below 2^32 threads
 
 averis_status_t check_fp8(const averis_fp8_t* t, int64_t rows, int64_t cols) {
   if (!t) return AVERIS_E_NULL;
@@ -36,13 +37,14 @@ averis_status_t check_segs(const int64_t* offs, int nseg) {
   return aligned(offs, 8) ? AVERIS_OK : AVERIS_E_ALIGN;
 }
 
-// an output of `stack` matrices m x n one after the other
 averis_status_t check_c(const void* c, averis_dtype_t dtype, int64_t m, int64_t n, int64_t ldc) {
   if (!dtype_ok(dtype)) return AVERIS_E_DTYPE;
   if (ldc < n) return AVERIS_E_SHAPE;
   if (m > 0 && n > 0 && !c) return AVERIS_E_NULL;
   return aligned(c, elem_size(dtype)) ? AVERIS_OK : AVERIS_E_ALIGN;
 }
+
+int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
 
 averis_status_t check_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (need && (!ws || ws_bytes < need)) return AVERIS_E_WORKSPACE;
@@ -72,7 +74,7 @@ averis_status_t averis_fp8_quant(const void* a, averis_dtype_t dtype, int64_t ro
   if (out_t) {
     const int64_t tc = seg_offsets ? averis_fp8_seg_cols(rows, nseg) : rows;
     if ((s = check_fp8(out_t, cols, tc)) != AVERIS_OK) return s;
-    if ((cols + 127) / 128 * chunk_upper_bound(rows, nseg, 128) > kMaxTiles) return AVERIS_E_SHAPE;
+    if (tiles_of(cols) * chunk_upper_bound(rows, nseg, 128) > kMaxTiles) return AVERIS_E_SHAPE;
     return hip_status(launch_fp8_tile(a, dtype == AVERIS_BF16, false, 1, rows, cols, lda, 0,
                                       seg_offsets, nseg, out_of(out), out_of(out_t), stream));
   }
@@ -87,7 +89,7 @@ averis_status_t averis_fp8_quant_weight(const void* w, averis_dtype_t dtype, int
   if (batch < 1 || batch > kMaxSeg) return AVERIS_E_ARG;
   if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxDim) return AVERIS_E_SHAPE;
   if (ldw < cols || batch_stride < 0) return AVERIS_E_SHAPE;
-  if ((cols + 127) / 128 * ((rows + 127) / 128) > kMaxTiles) return AVERIS_E_SHAPE;
+  if (tiles_of(cols) * tiles_of(rows) > kMaxTiles) return AVERIS_E_SHAPE;
   if (batch > 1 && batch_stride < rows * ldw) return AVERIS_E_SHAPE;
   if (!w || (!out && !out_t)) return AVERIS_E_NULL;
   if (!aligned(w, elem_size(dtype))) return AVERIS_E_ALIGN;
@@ -106,10 +108,11 @@ averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
   averis_status_t s = check_segs(seg_offsets, nseg);
   if (s != AVERIS_OK) return s;
   const int64_t m = a->rows, k = a->cols;
-  if (m < 0 || m > kMaxDim || k <= 0 || k > kMaxDim / 256 || b->cols != k) return AVERIS_E_SHAPE;
+  if (m < 0 || m > kMaxDim || k <= 0 || k > kMaxK || b->cols != k) return AVERIS_E_SHAPE;
   if (b->rows < 0 || b->rows % nseg != 0) return AVERIS_E_SHAPE;
   const int64_t n = b->rows / nseg;
-  if (n > kMaxDim || chunk_upper_bound(m, nseg, 256) > kMaxGridY) return AVERIS_E_SHAPE;
+  // tiles are numbered in 32 bits
+  if (n > kMaxDim || tiles_of(n) * chunk_upper_bound(m, nseg, 128) > 1 << 30) return AVERIS_E_SHAPE;
   if ((s = check_fp8(a, m, k)) != AVERIS_OK) return s;
   if ((s = check_fp8(b, b->rows, k)) != AVERIS_OK) return s;
   if ((s = check_c(c, cdtype, m, n, ldc)) != AVERIS_OK) return s;
@@ -131,8 +134,12 @@ averis_status_t averis_fp8_gemm_wgrad(const averis_fp8_t* xt, const averis_fp8_t
   const int64_t m = xt->rows, n = dt->rows;
   if (m < 0 || n < 0 || m > kMaxDim || n > kMaxDim || rows < 0) return AVERIS_E_SHAPE;
   const int64_t k = seg_offsets ? averis_fp8_seg_cols(rows, nseg) : rows;
-  // a tile's rows are addressed in 32 bits: 256 rows of k bytes
-  if (k < 0 || k > kMaxDim / 256 || (m + 255) / 256 > kMaxGridY) return AVERIS_E_SHAPE;
+  if (k < 0 || k > kMaxK) return AVERIS_E_SHAPE;
+  // tiles are numbered in 32 bits; by segment each is a workgroup of 256 threads,
+  // fewer than 2^32 in all
+  const int64_t most = seg_offsets ? (1 << 24) - 1 : 1 << 30;
+  if (tiles_of(n) > most || tiles_of(m) > most / std::max<int64_t>(tiles_of(n), 1) / nseg)
+    return AVERIS_E_SHAPE;
   if ((s = check_fp8(xt, m, k)) != AVERIS_OK) return s;
   if ((s = check_fp8(dt, n, k)) != AVERIS_OK) return s;
   if ((s = check_c(dw, dwdtype, m, n, lddw)) != AVERIS_OK) return s;

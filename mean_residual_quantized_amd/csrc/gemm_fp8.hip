@@ -746,8 +746,8 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg)
   }
   if (mode == kF8All) {
     for (int mf = 1; mf <= 4; mf *= 2) {
-      const double wgs = (double)((n + 15) / 16) * (double)((m + 16 * mf - 1) / (16 * mf));
-      if (wgs > 65536.0) continue;
+      const double rows = (double)((m + 16 * mf - 1) / (16 * mf)), wgs = (double)((n + 15) / 16) * rows;
+      if (wgs > 65536.0 || rows > 65535.0) continue;   // (the grid's y)
       offer(Fp8Plan{mf, 0, 1}, 3.0 + wgs * (double)k_blocks * 128.0 * (16.0 + 16.0 * mf) / 6.5e6 + 0.5 * mf);
     }
   }
@@ -765,7 +765,6 @@ hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t
                                         : (g.m + 64 * F - 1) / (64 * F);
   const int64_t tx = (g.n + 64 * F - 1) / (64 * F);
   const int64_t tiles = tx * ty * (MODE == kF8BlockSegs ? g.nseg : splits);
-  if (tiles > INT32_MAX / 2) return hipErrorInvalidValue;
   constexpr int slots = F == 4 ? kF8Cus : 2 * kF8Cus;
   const int64_t grid = MODE != kF8BlockSegs && tiles > slots ? slots : tiles;
   k_gemm_f8<F, OB, MODE><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(

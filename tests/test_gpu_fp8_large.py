@@ -22,3 +22,32 @@ def test_rows_past_one_launch():
     del a, q, e
     torch.cuda.empty_cache()
     assert all(ok), ok
+
+
+def small(*shape):
+    g = torch.Generator(device="cuda").manual_seed(shape[0])
+    return torch.randint(-4, 5, shape, dtype=torch.int8, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def test_products_of_many_rows():
+    """More than 65535 tiles of 256 rows; small integers, exact."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    m, n = (1 << 24) + 1000, 8
+    a, b = small(m, 1), small(n, 1)
+    qa = av.averis_fp8_quant(a)
+    c = av.averis_fp8_gemm(qa, av.averis_fp8_quant(b), torch.float32)
+    ok = [bool((c == a.float() @ b.float().t()).all())]
+    cuts, w = [0, 5, (1 << 24) + 900, m], small(3 * n, 1)
+    c = av.averis_fp8_gemm(qa, av.averis_fp8_quant(w), torch.float32, offsets=torch.tensor(cuts, device="cuda"))
+    for s in range(3):
+        ok.append(bool((c[cuts[s]:cuts[s + 1]] == a[cuts[s]:cuts[s + 1]].float() @ w[s * n:(s + 1) * n].float().t()).all()))
+    del c, qa
+    x, d = small(2, m), small(2, n)
+    _, xt = av.averis_fp8_quant(x, transposed=True, plain=False)
+    _, dt = av.averis_fp8_quant(d, transposed=True, plain=False)
+    g = av.averis_fp8_gemm_wgrad(xt, dt, torch.float32)
+    ok.append(bool((g == x[0].float()[:, None] * d[0].float() + x[1].float()[:, None] * d[1].float()).all()))
+    del g, xt
+    torch.cuda.empty_cache()
+    assert all(ok), ok
