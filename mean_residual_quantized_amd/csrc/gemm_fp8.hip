@@ -119,7 +119,8 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   constexpr int BM = 64 * F, BN = 64 * F, ROWS = BM + BN;
   constexpr int SLOT = ROWS * 128, SSLOT = ROWS * 4;
   constexpr int CPW = ROWS / 8 / 4;    // code loads a wavefront issues for a stage
-  constexpr int SPW = (ROWS / 64 + 3) / 4;   // scale loads for four stages, at most
+  constexpr int SPW = ROWS / 64 / 4;   // scale loads for four stages
+  static_assert(SPW * 256 == ROWS, "every wavefront's loads are whole");
   constexpr int NF = 2 * F;
   constexpr int ES = OUT_BF16 ? 2 : 4;
   constexpr int GROUP = 128 / ES;      // columns of an output pass: 128 bytes
@@ -263,11 +264,9 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   // the wavefront's scale load q of word g
   auto load_scale = [&](int g, int q) __attribute__((always_inline)) {
     const int gl = g < g_last ? g : g_last;
-    if (ROWS / 64 % 4 == 0 || wave + 4 * q < ROWS / 64) {
-      const uint8_t* base = scalar_base((64 * (wave + 4 * q) < BM ? a_s : b_s) + 4 * (int64_t)gl);
-      __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
-                                       (lds_void*)(sring + (g & 1) * SSLOT + (wave + 4 * q) * 256), 4, 0, 0);
-    }
+    const uint8_t* base = scalar_base((64 * (wave + 4 * q) < BM ? a_s : b_s) + 4 * (int64_t)gl);
+    __builtin_amdgcn_global_load_lds((const void*)(base + sofs[q]),
+                                     (lds_void*)(sring + (g & 1) * SSLOT + (wave + 4 * q) * 256), 4, 0, 0);
   };
   auto load_scales = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
