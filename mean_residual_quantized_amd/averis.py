@@ -772,42 +772,27 @@ class FP8:
     """Device fp8 tensor with one power-of-two scale for 128 elements along the
     columns: codes u8[rows, cols rounded up to 128] (E4M3, zero past cols),
     scales u8[rows, ceil(cols / 128) rounded up to 4] (E8M0)."""
-    __slots__ = ("_codes", "_scales", "_rows", "_cols")
+    __slots__ = ("codes", "scales", "rows", "cols")
 
     def __init__(self, codes, scales, rows, cols):
-        self._rows, self._cols = rows, cols
+        object.__setattr__(self, "rows", rows)
+        object.__setattr__(self, "cols", cols)
         self.codes, self.scales = codes, scales
         if codes.device != scales.device:
             raise ValueError("expected codes and scales on one device")
 
-    rows = property(lambda self: self._rows)
-    cols = property(lambda self: self._cols)
-
-    @property
-    def codes(self):
-        return self._codes
-
-    @codes.setter
-    def codes(self, t):
-        self._codes = FP8._bytes(t, "codes", (self._rows, FP8.pitches(self._cols)[0]))
-
-    @property
-    def scales(self):
-        return self._scales
-
-    @scales.setter
-    def scales(self, t):
-        self._scales = FP8._bytes(t, "scales", (self._rows, FP8.pitches(self._cols)[1]))
-
-    @staticmethod
-    def _bytes(t, what, shape):
+    def __setattr__(self, name, t):
+        # codes and scales may be replaced by others of their form
+        if name not in ("codes", "scales"):
+            raise AttributeError("%s cannot be set" % name)
+        shape = (self.rows, FP8.pitches(self.cols)[name == "scales"])
         if t.shape != shape or t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError("%s: expected a contiguous uint8 tensor of shape %s" % (what, shape))
-        return t
+            raise ValueError("%s: expected a contiguous uint8 tensor of shape %s" % (name, shape))
+        object.__setattr__(self, name, t)
 
     def c(self):
         # formed at each call: the tensors may have been replaced since the last
-        return _FP8(self._codes.data_ptr(), self._scales.data_ptr(), self._rows, self._cols)
+        return _FP8(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
 
     @staticmethod
     def pitches(cols):
@@ -818,10 +803,16 @@ class FP8:
     def empty(rows, cols, device="cuda"):
         p, s = FP8.pitches(cols)
         q = FP8.__new__(FP8)
-        q._rows, q._cols = rows, cols
-        q._codes = _new(rows, p, torch.uint8, device)
-        q._scales = _new(rows, s, torch.uint8, device)
+        _fp8_rows(q, rows)
+        _fp8_cols(q, cols)
+        _fp8_codes(q, _new(rows, p, torch.uint8, device))
+        _fp8_scales(q, _new(rows, s, torch.uint8, device))
         return q
+
+
+# the fields' own setters, for tensors that are made to fit
+_fp8_codes, _fp8_scales, _fp8_rows, _fp8_cols = (
+    getattr(FP8, name).__set__ for name in ("codes", "scales", "rows", "cols"))
 
 
 def _segments(offsets, ref):
