@@ -283,7 +283,9 @@ __global__ __launch_bounds__(256) void k_route(const T* __restrict__ logits, int
 // w = softmax over the chosen (renorm) or all logits.  With s_e = dweights of
 // the slot that chose e (0 if none) and m = sum over the chosen of w s:
 // dl_e = w_e (s_e - m), zero outside the chosen when renorm.  65521 tokens, 128
-// experts fp32: 15.4 us (67 MB, 4.4 TB/s).
+// experts fp32: 15.4 us (67 MB, 4.4 TB/s).  w is exp times the sum's reciprocal,
+// a rounding more than the quotient of k_route (quotients here: 14.5 -> 15.9 us
+// back to back, error 6.8e-8 -> 6.7e-8 of the norm).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route_grad(const T* logits, int64_t tokens,
                                                     int experts, int64_t ld, int topk, int renorm,
