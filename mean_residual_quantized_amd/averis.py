@@ -772,27 +772,38 @@ class FP8:
     """Device fp8 tensor with one power-of-two scale for 128 elements along the
     columns: codes u8[rows, cols rounded up to 128] (E4M3, zero past cols),
     scales u8[rows, ceil(cols / 128) rounded up to 4] (E8M0)."""
-    __slots__ = ("codes", "scales", "rows", "cols")
+    __slots__ = ("codes", "scales", "rows", "cols", "_c")
 
     def __init__(self, codes, scales, rows, cols):
-        object.__setattr__(self, "rows", rows)
-        object.__setattr__(self, "cols", cols)
-        self.codes, self.scales = codes, scales
+        pitch, spitch = FP8.pitches(cols)
+        _fp8_bytes(codes, "codes", (rows, pitch))
+        _fp8_bytes(scales, "scales", (rows, spitch))
         if codes.device != scales.device:
             raise ValueError("expected codes and scales on one device")
+        self._set(codes, scales, rows, cols)
+
+    def _set(self, codes, scales, rows, cols):
+        _set_codes(self, codes)
+        _set_scales(self, scales)
+        _set_rows(self, rows)
+        _set_cols(self, cols)
+        _set_c(self, _FP8(None, None, rows, cols))
 
     def __setattr__(self, name, t):
         # codes and scales may be replaced by others of their form
         if name not in ("codes", "scales"):
             raise AttributeError("%s cannot be set" % name)
-        shape = (self.rows, FP8.pitches(self.cols)[name == "scales"])
-        if t.shape != shape or t.dtype != torch.uint8 or not t.is_contiguous():
-            raise ValueError("%s: expected a contiguous uint8 tensor of shape %s" % (name, shape))
+        _fp8_bytes(t, name, (self.rows, FP8.pitches(self.cols)[name == "scales"]))
         object.__setattr__(self, name, t)
 
+    def __reduce__(self):   # copies and pickles
+        return FP8, (self.codes, self.scales, self.rows, self.cols)
+
     def c(self):
-        # formed at each call: the tensors may have been replaced since the last
-        return _FP8(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+        # the addresses of this call: the tensors may have been replaced since the last
+        c = self._c
+        c.codes, c.scales = self.codes.data_ptr(), self.scales.data_ptr()
+        return c
 
     @staticmethod
     def pitches(cols):
@@ -803,16 +814,18 @@ class FP8:
     def empty(rows, cols, device="cuda"):
         p, s = FP8.pitches(cols)
         q = FP8.__new__(FP8)
-        _fp8_rows(q, rows)
-        _fp8_cols(q, cols)
-        _fp8_codes(q, _new(rows, p, torch.uint8, device))
-        _fp8_scales(q, _new(rows, s, torch.uint8, device))
+        q._set(_new(rows, p, torch.uint8, device), _new(rows, s, torch.uint8, device), rows, cols)
         return q
 
 
-# the fields' own setters, for tensors that are made to fit
-_fp8_codes, _fp8_scales, _fp8_rows, _fp8_cols = (
-    getattr(FP8, name).__set__ for name in ("codes", "scales", "rows", "cols"))
+def _fp8_bytes(t, what, shape):
+    if t.shape != shape or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError("%s: expected a contiguous uint8 tensor of shape %s" % (what, shape))
+
+
+# the fields' own setters, for what has been checked or made to fit
+_set_codes, _set_scales, _set_rows, _set_cols, _set_c = (
+    getattr(FP8, name).__set__ for name in FP8.__slots__)
 
 
 def _segments(offsets, ref):

@@ -1,6 +1,9 @@
 """What the fp8 calls hand to the library for a tensor of codes and scales (a
 stub in place of the library: no GPU needed)."""
 
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -71,3 +74,16 @@ def test_codes_and_scales_on_one_device(sent):
             with pytest.raises(ValueError, match="one device"):
                 call(a, b)
     assert sent == []
+
+
+def test_copies(sent):
+    q = av.FP8.empty(4, 200, "cpu")
+    q.codes.fill_(3)
+    q.scales.fill_(5)
+    shallow, deep, loaded = copy.copy(q), copy.deepcopy(q), pickle.loads(pickle.dumps(q))
+    assert describe(shallow) == describe(q)
+    for other in (deep, loaded):
+        assert (other.rows, other.cols) == (4, 200) and describe(other)[0] != describe(q)[0]
+        assert torch.equal(other.codes, q.codes) and torch.equal(other.scales, q.scales)
+        av.averis_fp8_gemm(other, q)
+        assert sent == [describe(other), describe(q)]
