@@ -145,9 +145,10 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const T* __restrict__ a, int64
 // lanes store a 128-byte row of the transposed copy.  Bound by memory: each
 // value is read once and each code written once.  Neighbouring workgroups take
 // neighbouring tiles of the same rows.  Workgroup w runs on die w mod 8; where
-// tiles share lines (`near`) eight in a row go to one die, which then reads the
-// lines once (16384 x 3068 45.5 -> 42.5 us, 2999 x 1333 9.2 -> 8.7; where they
-// share none 16384 x 3072 38.3 -> 39.8, and it is left).
+// tiles share lines (`near`) eight in a row go to one die, which then reads most
+// of the lines once (16384 x 3068: 148 -> 107 MB into the L2s, 45.5 -> 42.5 us;
+// 2999 x 1333 9.2 -> 8.7; where they share none 16384 x 3072 38.3 -> 39.8, and it
+// is left).
 //
 // TILE: one scale for the tile (both copies then hold the same codes).
 //

@@ -701,9 +701,10 @@ struct Fp8Plan {
 // tile on its own, cost 2.3 (3.0) more a round.  A split output costs another launch
 // and 8 bytes a value and split at 9.5 TB/s; the few-rows kernel reads both
 // operands once a workgroup at 6.5 TB/s.
-// Measured either side, one product over and over, its operands in the
-// last-level cache (us, large / small tile); between other kernels, with
-// operands from memory, products by segments take 20 to 50 % longer:
+// Measured either side, one product over and over (us, large / small tile).
+// Between a step's other kernels, with operands that have left the caches, the
+// three by 64 segments take 80, 98 and 149 on the large tile; which side wins
+// there was not measured:
 //   16384 x 1024 x 3072  44.6 / 55.4    8192 x 2048 x 512     15.8 / 14.4
 //   16384 x 3072 x 1024  58.1 / 78.8    65536 x 1024 x 256    38.8 / 34.8
 //   32768 rows in 64 segments, 768 x 2048: 73.8 / 86.5, 2048 x 768: 88.9 / 98.6
