@@ -862,13 +862,15 @@ def averis_fp8_quant_weight(w):
     operand) and wd = Q(w) (the dgrad operand).  w: 2-D, or 3-D (a stack)."""
     a = w if w.dim() == 3 else w.unsqueeze(0)
     batch, rows, cols = a.shape
-    if a.stride(2) != 1:
+    bstride, ld, step = a.stride()
+    if cols > 1 and step != 1:
         raise ValueError("expected unit innermost stride")
+    if rows == 1:
+        ld = cols   # (the stride of a single row does not matter)
     wd = FP8.empty(batch * rows, cols, w.device)
     wt = FP8.empty(batch * cols, rows, w.device)
     _check("averis_fp8_quant_weight", lib().averis_fp8_quant_weight(
-        a.data_ptr(), _dtype_code(a), batch, rows, cols, a.stride(1), a.stride(0),
-        wd.c(), wt.c(), _stream_on(w)))
+        a.data_ptr(), _dtype_code(a), batch, rows, cols, ld, bstride, wd.c(), wt.c(), _stream_on(w)))
     return wt, wd
 
 

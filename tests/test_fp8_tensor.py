@@ -87,3 +87,27 @@ def test_copies(sent):
         assert torch.equal(other.codes, q.codes) and torch.equal(other.scales, q.scales)
         av.averis_fp8_gemm(other, q)
         assert sent == [describe(other), describe(q)]
+
+
+@pytest.mark.parametrize("shape,strides", [((1, 40), (1, 1)), ((1, 1), (7, 9)), ((40, 1), (3, 5)), ((5, 40), (48, 1)),
+                                           ((1, 1, 40), (2, 1, 1)), ((2, 1, 40), (64, 1, 1)), ((2, 3, 1), (9, 3, 2))])
+def test_weight_of_one_row_or_column(monkeypatch, shape, strides):
+    """A dimension of one element has no stride that matters."""
+    sent = []
+
+    class Stub:
+        @staticmethod
+        def averis_fp8_quant_weight(w, dtype, batch, rows, cols, ld, batch_stride, out, out_t, stream):
+            sent.append((batch, rows, cols, ld, batch_stride))
+            return 0
+    monkeypatch.setattr(av, "lib", lambda: Stub)
+    monkeypatch.setattr(av, "_stream_on", lambda t: None)
+    w = torch.zeros(4096).as_strided(shape, strides)
+    av.averis_fp8_quant_weight(w)
+    (batch, rows, cols, ld, batch_stride), = sent
+    assert (batch, rows, cols) == ((1,) * (3 - len(shape)) + shape)
+    assert ld >= cols and (batch == 1 or batch_stride >= rows * ld)
+    if rows > 1:
+        assert ld == strides[-2]
+    if batch > 1:
+        assert batch_stride == strides[0]

@@ -95,3 +95,15 @@ def test_exchange_of_wide_rows():
     for c in (0, h - 1):
         same(x[:, c], mark)
     every(x[-5:, 1:-1] == 0)
+
+
+def test_order_of_2_30_slots():
+    """Each token takes experts 0 .. 7 in turn: slot (t, j) is row j T + t."""
+    t, k = (1 << 27) + 5, 8
+    ids = torch.arange(k, dtype=torch.int32, device="cuda").repeat(t, 1)
+    offsets, pos, src = av.averis_moe_sort(ids, k)
+    assert offsets.tolist() == [j * t for j in range(k + 1)]
+    row = torch.arange(t, dtype=torch.int32, device="cuda")
+    for j in range(k):
+        same(pos[:, j], row + j * t)
+        same(src[j * t:(j + 1) * t], row * k + j)
