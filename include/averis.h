@@ -472,8 +472,8 @@ averis_status_t averis_split_quant_noalloc(const void* a, averis_dtype_t dtype, 
 
 /* expert_ids[t][j], weights[t][j] (tokens x topk): the topk largest of token
  * t's logits in descending order and their softmax weights.  Ties go to the
- * lowest expert; a NaN logit counts as the largest (and makes the weights
- * NaN).  A logit of -inf is masked: never chosen, and a slot for which no
+ * lowest expert; a NaN logit counts as the largest; it and +inf make the
+ * weights of the token's experts NaN.  A logit of -inf is masked: never chosen, and a slot for which no
  * open expert is left gets id -1 and weight 0 (every slot of a token whose
  * logits are all -inf).  renorm = 1: softmax over the chosen logits; 0: over
  * all of them.  logits: tokens x experts, row stride ld >= experts;
@@ -540,8 +540,9 @@ averis_status_t averis_moe_combine_grad(const void* dy, averis_dtype_t dtype, in
 /*   and scale 1.                                                          */
 /* Products: fp32 accumulation.  The matrix instruction adds the products  */
 /* of eight consecutive k with each term cut at 2^-13 of the largest of    */
-/* them, so |error| <= 2^-10 sum |a b| at worst (1e-5 of the result's norm */
-/* on random operands), before the output's rounding.                      */
+/* them, so |error| <= 2^-10 sum |a b| at worst (1.5e-5 of the result's    */
+/* norm on random operands), before the output's rounding: one BF16 value  */
+/* in 90 is rounded to the neighbour of what an exact sum would give.      */
 /* ---------------------------------------------------------------------- */
 
 /* rows x cols logical elements.  codes: rows of cols rounded up to 128
