@@ -473,9 +473,9 @@ averis_status_t averis_split_quant_noalloc(const void* a, averis_dtype_t dtype, 
 /* expert_ids[t][j], weights[t][j] (tokens x topk): the topk largest of token
  * t's logits in descending order and their softmax weights.  Ties go to the
  * lowest expert; a NaN logit counts as the largest; it and +inf make the
- * weights of the token's experts NaN.  A logit of -inf is masked: never chosen, and a slot for which no
- * open expert is left gets id -1 and weight 0 (every slot of a token whose
- * logits are all -inf).  renorm = 1: softmax over the chosen logits; 0: over
+ * weights of the token's experts NaN.  A logit of -inf is masked: never chosen,
+ * and a slot for which no open expert is left gets id -1 and weight 0 (every
+ * slot of a token whose logits are all -inf).  renorm = 1: softmax over the chosen logits; 0: over
  * all of them.  logits: tokens x experts, row stride ld >= experts;
  * 1 <= topk <= min(experts, AVERIS_MAX_TOPK). */
 averis_status_t averis_moe_route(const void* logits, averis_dtype_t dtype, int64_t tokens,

@@ -20,8 +20,9 @@
 // Both are bound by memory: the first reads every gradient, with the next
 // chunk's loads in flight while a chunk is squared; the second reads and writes
 // them, last chunk first, so that what the first pass read last may still be in
-// a cache.  1 GiB of fp32 in 310 tensors: 0.18 ms (6.1
-// TB/s) and 0.41 ms (5.3 TB/s); 7 bf16 tensors of 31 MB together: 9 and 16 us.
+// a cache.  1 GiB of fp32 in 310 tensors: 0.22 ms (4.9 TB/s; without a second
+// pass between, 0.19) and 0.41 ms (5.3 TB/s); 7 bf16 tensors of 31 MB together:
+// 9 and 16 us.
 // Up to 2048 workgroups a launch: eight on a CU keep enough loads in flight.
 #include <hip/hip_runtime.h>
 #include <alloca.h>
