@@ -87,7 +87,9 @@ typedef enum {
   AVERIS_OP_MOE_SORT = 5,     /* rows = tokens * topk slots, n = experts (cols unused) */
   AVERIS_OP_GRAD_NORM = 6,    /* n = number of tensors (rows, cols unused)    */
   AVERIS_OP_FP8_GEMM = 7,     /* rows = m, cols = k, n, nseg (0: not grouped) */
-  AVERIS_OP_FP8_WGRAD = 8     /* rows = m, cols = tokens, n, nseg             */
+  AVERIS_OP_FP8_WGRAD = 8,    /* rows = m, cols = tokens, n, nseg             */
+  AVERIS_OP_RMSNORM_GRAD = 9, /* rows, cols                                   */
+  AVERIS_OP_FP8_ACT_GRAD = 10 /* rows, cols, nseg (0: not grouped)            */
 } averis_op_t;
 
 /* An NVFP4-style tensor of rows x cols logical elements, 16-blocks along
@@ -492,6 +494,46 @@ averis_status_t averis_moe_route_grad(const void* logits, averis_dtype_t dtype, 
                                       const int32_t* expert_ids, const float* dweights,
                                       void* dlogits, int64_t ldd, hipStream_t stream);
 
+#define AVERIS_MAX_GROUPS 64
+
+/* What a token's experts are chosen and weighted by: s_e = e^l_e / sum e^l
+ * over the open experts, or 1 / (1 + e^-l_e). */
+typedef enum { AVERIS_SCORE_SOFTMAX = 0, AVERIS_SCORE_SIGMOID = 1 } averis_score_t;
+
+/* Routing by scores, with a bias that balances the experts' load and with
+ * groups of experts.  Experts are chosen by c_e = s_e + bias[e] (bias:
+ * `experts` floats, NULL: 0) and weighted by s_e:
+ *   the experts divide in order into `groups` equal groups (at most
+ *   AVERIS_MAX_GROUPS); where topk_groups < groups only the topk_groups with
+ *   the largest scores stay, a group's score being the sum of its group_top
+ *   (1 or 2) largest c_e (of its one open expert, c_e);
+ *   of theirs, expert_ids[t][j] are the topk largest c_e in descending order,
+ *   weights[t][j] = scale s_e, divided by the sum of the chosen s_e with renorm = 1.
+ * The choice is by the exact values of c_e (and, without a bias and with
+ * group_top = 1 or all groups, of l_e, which order alike), equal ones by the
+ * lowest index first.  A logit of -inf, or c_e = -inf, is closed: never chosen, and a
+ * slot for which none is left gets id -1 and weight 0; a group without an open
+ * expert does not stay.  A NaN logit counts as the largest and makes its weight NaN
+ * (with renorm or softmax scores all of the token's; so does +inf with softmax).
+ * Other arguments as for averis_moe_route; topk <= topk_groups experts / groups. */
+averis_status_t averis_moe_route_groups(const void* logits, averis_dtype_t dtype, int64_t tokens,
+                                        int experts, int64_t ld, int topk, const float* bias,
+                                        averis_score_t score, int groups, int topk_groups,
+                                        int group_top, int renorm, float scale,
+                                        int32_t* expert_ids, float* weights, hipStream_t stream);
+
+/* dlogits from dweights: the gradient of averis_moe_route_groups' weights with
+ * the choice held fixed (the bias has none).  expert_ids as that call wrote them for the
+ * same logits, topk, score, renorm and scale; an id outside the experts
+ * contributes nothing.  Zeros outside the chosen, but for softmax without
+ * renorm.  dlogits (the logits' type, row stride ldd >= experts) may be
+ * logits. */
+averis_status_t averis_moe_route_groups_grad(const void* logits, averis_dtype_t dtype,
+                                             int64_t tokens, int experts, int64_t ld, int topk,
+                                             averis_score_t score, int renorm, float scale,
+                                             const int32_t* expert_ids, const float* dweights,
+                                             void* dlogits, int64_t ldd, hipStream_t stream);
+
 /* The order of the slots by expert, stable (within an expert by slot):
  *   seg_offsets[experts + 1]: expert e owns rows seg_offsets[e] ..
  *                seg_offsets[e + 1] - 1 (the array the grouped calls take);
@@ -613,6 +655,72 @@ averis_status_t averis_fp8_gemm_wgrad(const averis_fp8_t* xt, const averis_fp8_t
                                       int64_t rows, const int64_t* seg_offsets, int nseg,
                                       void* dw, averis_dtype_t dwdtype, int64_t lddw, void* ws,
                                       size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Around a block's linears: the norm before them, with the residual's     */
+/* addition and its output in fp8, and the way back through the activation */
+/* and bias after them.                                                    */
+/* ---------------------------------------------------------------------- */
+
+#define AVERIS_MAX_NORM_COLS 16384
+
+/* h = x + residual (rounded to the type; x itself without a residual),
+ * rstd[i] = 1 / sqrt(mean of row i's squares of h + eps) (the sum in fp64,
+ * rstd rounded to fp32), y = h rstd weight (fp32, rounded to the type).  Each of y
+ * (rows x cols, the type of x), out (rows x cols) and out_t (cols x rows, runs
+ * along the rows) may be NULL, not all three; out and out_t are what
+ * averis_fp8_quant gives of y, bit for bit, whether y is written or not.
+ * x, residual, h, y: F32 or BF16, row strides ldx, ldres, ldh, ldy >= cols,
+ * element aligned.  residual may be NULL, h is then NULL too and ldh unused;
+ * else h is written (it may be x or residual; y overlaps none of the three).  weight:
+ * cols elements, F32 or BF16.  rstd: rows floats.  cols <= AVERIS_MAX_NORM_COLS,
+ * rows <= 2^30; with out_t fewer than 2^23 tiles of 128 x 128.  eps >= 0; a row
+ * whose mean square + eps is 0 gives NaN, as one with a value that is not
+ * finite does. */
+averis_status_t averis_rmsnorm(const void* x, averis_dtype_t dtype, int64_t rows, int64_t cols,
+                               int64_t ldx, const void* residual, int64_t ldres,
+                               const void* weight, averis_dtype_t wdtype, double eps, void* h,
+                               int64_t ldh, void* y, int64_t ldy, float* rstd,
+                               const averis_fp8_t* out, const averis_fp8_t* out_t,
+                               hipStream_t stream);
+
+/* The gradients of averis_rmsnorm from dy (of y) and dres (of h, by what else
+ * reads it; may be NULL): with v = h rstd (h, rstd as that call left them)
+ *   dh = rstd (dy weight - v mean(dy weight v)) + dres: that of x and of residual,
+ *   dweight[j] = sum over the rows of dy v (cols floats, may be NULL; a fixed
+ *   order: the same bits on every call; zeros for no rows).
+ * fp32, dh rounded once to the type; dh may be dy or dres.  Workspace:
+ * AVERIS_OP_RMSNORM_GRAD (unused without dweight). */
+averis_status_t averis_rmsnorm_grad(const void* dy, averis_dtype_t dtype, int64_t rows,
+                                    int64_t cols, int64_t lddy, const void* h, int64_t ldh,
+                                    const void* weight, averis_dtype_t wdtype, const float* rstd,
+                                    const void* dres, int64_t lddres, void* dh, int64_t lddh,
+                                    float* dweight, void* ws, size_t ws_bytes,
+                                    hipStream_t stream);
+
+/* Activations: z, max(z, 0), z / (1 + e^-z), and the tanh form of gelu,
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum {
+  AVERIS_ACT_NONE = 0,
+  AVERIS_ACT_RELU = 1,
+  AVERIS_ACT_SILU = 2,
+  AVERIS_ACT_GELU = 3
+} averis_act_t;
+
+/* dz = dy act'(z) (rows x cols; fp32, relu's slope at 0 is 0, the smooth ones'
+ * at +-inf 1 and 0): rounded to the type of dy and z and quantized into out and
+ * out_t as averis_fp8_quant does, segments included, from one read; dbias[s][j]
+ * = sum of dz (before it is rounded) over segment s's rows, nseg x cols floats
+ * in a fixed order, zeros for a segment without any.  Each of the three may be
+ * NULL, not all.  z is not read (and may be NULL) for AVERIS_ACT_NONE.  With
+ * segments, rows outside every one are not written to out.  cols <= 2^27,
+ * rows <= 2^30, fewer than 2^23 tiles of 128 x 128 (with segments, for any division
+ * of the rows).  Workspace: AVERIS_OP_FP8_ACT_GRAD (unused without dbias). */
+averis_status_t averis_fp8_act_grad(const void* dy, averis_dtype_t dtype, int64_t rows,
+                                    int64_t cols, int64_t lddy, const void* z, int64_t ldz,
+                                    averis_act_t act, const int64_t* seg_offsets, int nseg,
+                                    const averis_fp8_t* out, const averis_fp8_t* out_t,
+                                    float* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* The global gradient norm over many tensors, and clipping                */

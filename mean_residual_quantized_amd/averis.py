@@ -23,9 +23,13 @@ F32, BF16 = 0, 1
 RN, SR = 0, 1
 OP_SPLIT_QUANT, OP_QUANT, OP_GEMM, OP_WGRAD, OP_QUANT_PAIR_MULTI = 0, 1, 2, 3, 4
 OP_MOE_SORT, OP_GRAD_NORM, OP_FP8_GEMM, OP_FP8_WGRAD = 5, 6, 7, 8
+OP_RMSNORM_GRAD, OP_FP8_ACT_GRAD = 9, 10
 MAX_WEIGHTS = 16
 MAX_RANK1 = 4
 MAX_EXPERTS, MAX_TOPK, MAX_GRADS = 1024, 32, 1 << 20
+MAX_GROUPS, MAX_NORM_COLS = 64, 16384
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+SCORES = {"softmax": 0, "sigmoid": 1}
 STREAM_ACT, STREAM_MEAN, STREAM_WEIGHT, STREAM_RESIDUAL_T = 0, 1, 2, 3
 
 # every symbol include/averis.h declares
@@ -41,7 +45,8 @@ EXPORTS = [
     "averis_moe_route", "averis_moe_route_grad", "averis_moe_sort", "averis_moe_dispatch",
     "averis_moe_combine", "averis_moe_combine_grad", "averis_grad_norm", "averis_grad_clip",
     "averis_fp8_seg_cols", "averis_fp8_quant", "averis_fp8_quant_weight", "averis_fp8_gemm",
-    "averis_fp8_gemm_wgrad",
+    "averis_fp8_gemm_wgrad", "averis_rmsnorm", "averis_rmsnorm_grad", "averis_fp8_act_grad",
+    "averis_moe_route_groups", "averis_moe_route_groups_grad",
     "averis_workspace_bytes", "averis_status_str",
     "averis_abi_version", "averis_last_error",
 ]
@@ -124,6 +129,14 @@ def lib():
             "averis_fp8_quant_weight": [P, I, I, I64, I64, I64, I64, F8, F8, P],
             "averis_fp8_gemm": [F8, F8, P, I, P, I, I64, P, SZ, P],
             "averis_fp8_gemm_wgrad": [F8, F8, I64, P, I, P, I, I64, P, SZ, P],
+            "averis_rmsnorm": [P, I, I64, I64, I64, P, I64, P, I, ctypes.c_double, P, I64, P, I64, P,
+                               F8, F8, P],
+            "averis_rmsnorm_grad": [P, I, I64, I64, I64, P, I64, P, I, P, P, I64, P, I64, P, P, SZ, P],
+            "averis_fp8_act_grad": [P, I, I64, I64, I64, P, I64, I, P, I, F8, F8, P, P, SZ, P],
+            "averis_moe_route_groups": [P, I, I64, I, I64, I, P, I, I, I, I, I, ctypes.c_float, P, P,
+                                        P],
+            "averis_moe_route_groups_grad": [P, I, I64, I, I64, I, I, I, ctypes.c_float, P, P, P, I64,
+                                             P],
             "averis_grad_norm": [I, P, P, P, SZ, P],
             "averis_grad_clip": [I, P, ctypes.c_double, ctypes.c_double, P, P, SZ, P],
         }
@@ -690,6 +703,55 @@ def averis_moe_route_grad(logits, ids, dweights, renorm=True, out=None):
     return out
 
 
+def _choice(table, name, what):
+    if name not in table:
+        raise ValueError("%s: expected one of %s, got %r" % (what, ", ".join(table), name))
+    return table[name]
+
+
+def averis_moe_route_groups(logits, topk, bias=None, score="sigmoid", groups=1, topk_groups=None,
+                            group_top=2, renorm=True, scale=1.0):
+    """Experts of each token by score ("sigmoid" or "softmax" of its logits) plus
+    bias (float32 [experts]), within the topk_groups of `groups` equal groups
+    (default: all) whose group_top best sum highest; returns (expert_ids int32,
+    weights float32), both [tokens, topk], weights = scale * score without the
+    bias, over the chosen ones' sum with renorm.  -inf closes an expert; a slot
+    without an open one has id -1 and weight 0."""
+    ld = _matrix(logits, logits, "logits")
+    tokens, experts = logits.shape
+    if bias is not None:
+        _like(bias, logits, torch.float32, "bias", (experts,))
+    ids = _new(tokens, topk, torch.int32, logits.device)
+    weights = torch.empty_like(ids, dtype=torch.float32)
+    _check("averis_moe_route_groups", lib().averis_moe_route_groups(
+        logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, topk,
+        bias.data_ptr() if bias is not None else None, _choice(SCORES, score, "score"), groups,
+        groups if topk_groups is None else topk_groups, group_top, int(bool(renorm)), scale,
+        ids.data_ptr(), weights.data_ptr(), _stream_on(logits)))
+    return ids, weights
+
+
+def averis_moe_route_groups_grad(logits, ids, dweights, score="sigmoid", renorm=True, scale=1.0,
+                                 out=None):
+    """The logits' gradient (their type) from dweights, for the ids that
+    averis_moe_route_groups returned for the same logits, score, renorm and
+    scale."""
+    ld = _matrix(logits, logits, "logits")
+    tokens, experts = logits.shape
+    _like(ids, logits, torch.int32, "ids")
+    if ids.dim() != 2 or ids.shape[0] != tokens:
+        raise ValueError("ids: expected shape (%d, topk)" % tokens)
+    topk = ids.shape[1]
+    _like(dweights, logits, torch.float32, "dweights", (tokens, topk))
+    out = out if out is not None else _new(tokens, experts, logits.dtype, logits.device)
+    ldd = _matrix(out, logits, "out", (tokens, experts))
+    _check("averis_moe_route_groups_grad", lib().averis_moe_route_groups_grad(
+        logits.data_ptr(), _dtype_code(logits), tokens, experts, ld, topk,
+        _choice(SCORES, score, "score"), int(bool(renorm)), scale, ids.data_ptr(),
+        dweights.data_ptr(), out.data_ptr(), ldd, _stream_on(logits)))
+    return out
+
+
 def averis_moe_sort(ids, experts, ws=None):
     """The slots' stable order by expert; returns (offsets int64 [experts + 1],
     pos int32 [tokens, topk], src int32 [tokens * topk]): offsets as the
@@ -925,6 +987,103 @@ def averis_fp8_gemm_wgrad(xt, dt, out_dtype=torch.bfloat16, offsets=None, rows=N
         ws.data_ptr() if ws is not None else None, ws.numel() if ws is not None else 0,
         _stream_on(c)))
     return c
+
+
+# --------------------------------------------------------------------------
+# around a block's linears
+# --------------------------------------------------------------------------
+
+def _vector(t, ref, what, n):
+    """Type code of t, checked to be a contiguous vector of n elements in float32
+    or bfloat16 on ref's device."""
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.device != ref.device:
+        raise ValueError("%s: expected a contiguous vector of %d elements on %s" % (what, n, ref.device))
+    return _dtype_code(t)
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def averis_rmsnorm(x, weight, eps=1e-6, residual=None, fp8=True, transposed=False, y=False, out=None):
+    """Root-mean-square norm of h = x + residual, times weight (float32 or
+    bfloat16 [cols]); returns (h, rstd, y, q, qt): the sum (written to out, which
+    may be x or residual; x itself without a residual), its rows' factors, and of the
+    output what is asked for, else None: itself, quantized along its columns (fp8) and
+    along its rows (transposed), as averis_fp8_quant(y) gives them."""
+    ldx = _matrix(x, x, "x")
+    rows, cols = x.shape
+    wcode = _vector(weight, x, "weight", cols)
+    dev, h, ldr, ldh = x.device, x, 0, 0
+    if residual is not None:
+        ldr = _matrix(residual, x, "residual", (rows, cols))
+        h = out if out is not None else _new(rows, cols, x.dtype, dev)
+        ldh = _matrix(h, x, "out", (rows, cols))
+    elif out is not None:
+        raise ValueError("out: expected None without a residual")
+    o = _new(rows, cols, x.dtype, dev) if y else None
+    q = FP8.empty(rows, cols, dev) if fp8 else None
+    qt = FP8.empty(cols, rows, dev) if transposed else None
+    rstd = torch.empty_strided((rows,), (1,), dtype=torch.float32, device=dev)
+    _check("averis_rmsnorm", lib().averis_rmsnorm(
+        x.data_ptr(), _dtype_code(x), rows, cols, ldx, _addr(residual), ldr, weight.data_ptr(), wcode,
+        eps, h.data_ptr() if residual is not None else None, ldh, _addr(o), cols, rstd.data_ptr(),
+        q.c() if fp8 else None, qt.c() if transposed else None, _stream_on(x)))
+    return h, rstd, o, q, qt
+
+
+def averis_rmsnorm_grad(dy, h, weight, rstd, dres=None, out=None, ws=None):
+    """The gradients of averis_rmsnorm from dy (y's) and dres (h's, by what else
+    reads it): returns (dh, dweight), dh that of x and of residual alike (into out,
+    which may be dy or dres), dweight float32."""
+    lddy = _matrix(dy, dy, "dy")
+    rows, cols = dy.shape
+    ldh = _matrix(h, dy, "h", (rows, cols))
+    wcode = _vector(weight, dy, "weight", cols)
+    _like(rstd, dy, torch.float32, "rstd", (rows,))
+    ldr = _matrix(dres, dy, "dres", (rows, cols)) if dres is not None else 0
+    out = out if out is not None else _new(rows, cols, dy.dtype, dy.device)
+    ldo = _matrix(out, dy, "out", (rows, cols))
+    dweight = torch.empty_strided((cols,), (1,), dtype=torch.float32, device=dy.device)
+    ws = _ws(ws, OP_RMSNORM_GRAD, (rows, cols), dy.device)
+    _check("averis_rmsnorm_grad", lib().averis_rmsnorm_grad(
+        dy.data_ptr(), _dtype_code(dy), rows, cols, lddy, h.data_ptr(), ldh, weight.data_ptr(), wcode,
+        rstd.data_ptr(), _addr(dres), ldr, out.data_ptr(), ldo, dweight.data_ptr(),
+        _addr(ws), ws.numel() if ws is not None else 0, _stream_on(dy)))
+    return out, dweight
+
+
+def averis_fp8_act_grad(dy, z=None, act="none", plain=True, transposed=True, bias=True, offsets=None,
+                        ws=None):
+    """Back through an activation ("none", "relu", "silu", "gelu") of z and the
+    bias before it: returns (q, qt, dbias) of dz = dy act'(z), None for what is
+    not asked for: quantized along its columns (plain) and along its rows (transposed) as
+    averis_fp8_quant does, and summed over the rows (float32 [cols]; with
+    offsets [nseg, cols], a sum for each segment)."""
+    lddy = _matrix(dy, dy, "dy")
+    rows, cols = dy.shape
+    code = _choice(ACTS, act, "act")
+    ldz = 0
+    if code:
+        if z is None:
+            raise ValueError("z: expected the value before the activation")
+        ldz = _matrix(z, dy, "z", (rows, cols))
+    offs, nseg = _segments(offsets, dy)
+    q = FP8.empty(rows, cols, dy.device) if plain else None
+    qt = None
+    if transposed:
+        tc = rows if offsets is None else int(lib().averis_fp8_seg_cols(rows, nseg))
+        qt = FP8.empty(cols, tc, dy.device)
+    db = None
+    if bias:
+        db = torch.empty((cols,) if offsets is None else (nseg, cols), dtype=torch.float32,
+                         device=dy.device)
+        ws = _ws(ws, OP_FP8_ACT_GRAD, (rows, cols, 0, 0 if offsets is None else nseg), dy.device)
+    _check("averis_fp8_act_grad", lib().averis_fp8_act_grad(
+        dy.data_ptr(), _dtype_code(dy), rows, cols, lddy, z.data_ptr() if code else None, ldz, code,
+        offs, nseg, q.c() if plain else None, qt.c() if transposed else None, _addr(db), _addr(ws),
+        ws.numel() if ws is not None else 0, _stream_on(dy)))
+    return q, qt, db
 
 
 # --------------------------------------------------------------------------

@@ -141,6 +141,12 @@ size_t averis_workspace_bytes(averis_op_t op, int64_t rows, int64_t cols, int64_
                                      nseg == 0 ? kF8All : wgrad ? kF8BlockSegs : kF8RowSegs,
                                      nseg > 0 ? (int)nseg : 1);
   }
+  if (op == AVERIS_OP_RMSNORM_GRAD)
+    return (rows >= 0 && rows <= (int64_t)1 << 30 && cols > 0 && cols <= kMaxNormCols)
+               ? norm_grad_ws_bytes(rows, cols) : 0;
+  if (op == AVERIS_OP_FP8_ACT_GRAD)
+    return (rows >= 0 && rows <= (int64_t)1 << 30 && cols > 0 && cols <= kMaxActCols && nseg >= 0 &&
+            nseg <= kMaxSeg) ? act_grad_ws_bytes(rows, cols, nseg > 0 ? (int)nseg : 1) : 0;
   if (op == AVERIS_OP_GRAD_NORM)
     return (n >= 0 && n <= kMaxGrads) ? grad_norm_ws_bytes((int)n) : 0;
   if (op == AVERIS_OP_WGRAD) {
@@ -166,6 +172,8 @@ size_t averis_workspace_bytes(averis_op_t op, int64_t rows, int64_t cols, int64_
     case AVERIS_OP_GRAD_NORM:
     case AVERIS_OP_FP8_GEMM:
     case AVERIS_OP_FP8_WGRAD:
+    case AVERIS_OP_RMSNORM_GRAD:
+    case AVERIS_OP_FP8_ACT_GRAD:
       break;
   }
   return 0;

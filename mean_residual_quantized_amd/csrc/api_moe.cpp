@@ -11,7 +11,9 @@
 using namespace averis;
 
 static_assert(AVERIS_MAX_EXPERTS == kMaxExperts && AVERIS_MAX_TOPK == kMaxTopk &&
-                  AVERIS_MAX_GRADS == kMaxGrads, "limits");
+                  AVERIS_MAX_GRADS == kMaxGrads && AVERIS_MAX_GROUPS == kMaxGroups &&
+                  AVERIS_SCORE_SOFTMAX == kScoreSoftmax && AVERIS_SCORE_SIGMOID == kScoreSigmoid,
+              "limits and names");
 
 namespace {
 
@@ -74,6 +76,51 @@ averis_status_t averis_moe_route_grad(const void* logits, averis_dtype_t dtype, 
   return hip_status(launch_moe_route_grad(logits, dtype == AVERIS_BF16, tokens, experts, ld, topk,
                                           renorm != 0, expert_ids, dweights, dlogits, ldd,
                                           stream));
+}
+
+averis_status_t averis_moe_route_groups(const void* logits, averis_dtype_t dtype, int64_t tokens,
+                                        int experts, int64_t ld, int topk, const float* bias,
+                                        averis_score_t score, int groups, int topk_groups,
+                                        int group_top, int renorm, float scale,
+                                        int32_t* expert_ids, float* weights, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return AVERIS_E_DTYPE;
+  const averis_status_t s = check_router(tokens, experts, ld, topk);
+  if (s != AVERIS_OK) return s;
+  if (score != AVERIS_SCORE_SOFTMAX && score != AVERIS_SCORE_SIGMOID) return AVERIS_E_ARG;
+  if (groups < 1 || groups > kMaxGroups || experts % groups != 0) return AVERIS_E_ARG;
+  if (topk_groups < 1 || topk_groups > groups) return AVERIS_E_ARG;
+  const int size = experts / groups;
+  if (topk > topk_groups * size || group_top < 1 || group_top > 2) return AVERIS_E_ARG;
+  if (renorm != 0 && renorm != 1) return AVERIS_E_ARG;
+  if (tokens > 0 && (!logits || !expert_ids || !weights)) return AVERIS_E_NULL;
+  if (!aligned(logits, elem_size(dtype)) || !aligned(bias, 4) || !aligned(expert_ids, 4) ||
+      !aligned(weights, 4))
+    return AVERIS_E_ALIGN;
+  const RouteGroups a{tokens, ld, experts, topk, bias, score, groups, topk_groups, group_top,
+                      renorm != 0, scale, expert_ids, weights, size,
+                      (((uint64_t)1 << 32) + (uint64_t)size - 1) / (uint64_t)size, 0};
+  return hip_status(launch_route_groups(logits, dtype == AVERIS_BF16, a, stream));
+}
+
+averis_status_t averis_moe_route_groups_grad(const void* logits, averis_dtype_t dtype,
+                                             int64_t tokens, int experts, int64_t ld, int topk,
+                                             averis_score_t score, int renorm, float scale,
+                                             const int32_t* expert_ids, const float* dweights,
+                                             void* dlogits, int64_t ldd, hipStream_t stream) {
+  if (!dtype_ok(dtype)) return AVERIS_E_DTYPE;
+  const averis_status_t s = check_router(tokens, experts, ld, topk);
+  if (s != AVERIS_OK) return s;
+  if (score != AVERIS_SCORE_SOFTMAX && score != AVERIS_SCORE_SIGMOID) return AVERIS_E_ARG;
+  if (renorm != 0 && renorm != 1) return AVERIS_E_ARG;
+  if (ldd < experts) return AVERIS_E_SHAPE;
+  if (tokens > 0 && (!logits || !expert_ids || !dweights || !dlogits)) return AVERIS_E_NULL;
+  const size_t es = elem_size(dtype);
+  if (!aligned(logits, es) || !aligned(dlogits, es) || !aligned(expert_ids, 4) ||
+      !aligned(dweights, 4))
+    return AVERIS_E_ALIGN;
+  const RouteGroupsGrad a{tokens, ld, ldd, experts, topk, score, renorm != 0, scale, expert_ids,
+                          dweights};
+  return hip_status(launch_route_groups_grad(logits, dtype == AVERIS_BF16, a, dlogits, stream));
 }
 
 averis_status_t averis_moe_sort(const int32_t* expert_ids, int64_t tokens, int topk, int experts,

@@ -3,99 +3,19 @@
 //   k_fp8_rows   runs of 128 along the columns: one read of the input, no LDS
 //   k_fp8_tile   128 x 128 tiles through LDS: the transposed copy (runs along
 //                the rows), with or without the plain copy, from one read; or
-//                both copies of a weight with one scale for the whole tile
+//                both copies of a weight with one scale for the whole tile; of a
+//                matrix, of a norm's output, or of a gradient before an
+//                activation with its column sums
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "fp8_common.hpp"
+#include "activation.hpp"
+#include "fp8_eight.hpp"
 #include "launch.hpp"
 #include "segments.hpp"
 
 namespace averis {
 namespace {
-
-// eight consecutive elements of a row, as loaded
-template <typename T>
-struct Eight;
-template <>
-struct Eight<uint16_t> {
-  u32x4_t w;
-  __device__ __forceinline__ void zero() { w = u32x4_t{0u, 0u, 0u, 0u}; }
-  // elements c .. c + 7 of a row of cols elements, 0 past its end
-  __device__ __forceinline__ void load(const uint16_t* row, int64_t c, int64_t cols) {
-    if (c + 8 <= cols) {
-      w = *reinterpret_cast<const f8_piece_t*>(row + c);
-      return;
-    }
-    zero();
-    if (c >= cols) return;
-    // all loads at once, those past the end of the last element (one by one, each
-    // behind its own branch: 16384 x 3071 53.7 us instead of 47.0)
-    uint16_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = row[c + i < cols ? c + i : cols - 1];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i / 2] |= (c + i < cols ? (uint32_t)e[i] : 0u) << (16 * (i & 1));
-  }
-  // bits of the largest magnitude, as fp32
-  __device__ __forceinline__ uint32_t amax() const {
-    const uint32_t k = 0x7FFF7FFFu;
-    const uint32_t m = pk_max_u16(pk_max_u16(w[0] & k, w[1] & k), pk_max_u16(w[2] & k, w[3] & k));
-    const uint32_t lo = m << 16, hi = m & 0xFFFF0000u;
-    return lo > hi ? lo : hi;
-  }
-  __device__ __forceinline__ u32x2_t codes(uint32_t byte) const {
-    return u32x2_t{f8_codes4_bf16(w[0], w[1], byte), f8_codes4_bf16(w[2], w[3], byte)};
-  }
-};
-template <>
-struct Eight<float> {
-  u32x4_t w[2];
-  __device__ __forceinline__ void zero() { w[0] = w[1] = u32x4_t{0u, 0u, 0u, 0u}; }
-  __device__ __forceinline__ void load(const float* row, int64_t c, int64_t cols) {
-    if (c + 8 <= cols) {
-      w[0] = *reinterpret_cast<const f8_piece_t*>(row + c);
-      w[1] = *reinterpret_cast<const f8_piece_t*>(row + c + 4);
-      return;
-    }
-    zero();
-    if (c >= cols) return;
-    float e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = row[c + i < cols ? c + i : cols - 1];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i / 4][i % 4] = c + i < cols ? __float_as_uint(e[i]) : 0u;
-  }
-  __device__ __forceinline__ uint32_t amax() const {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t a = w[i / 4][i % 4] & 0x7FFFFFFFu;
-      m = a > m ? a : m;
-    }
-    return m;
-  }
-  __device__ __forceinline__ u32x2_t codes(uint32_t byte) const {
-    auto f = [&](int i) { return __uint_as_float(w[i / 4][i % 4]); };
-    return u32x2_t{f8_codes4(f(0), f(1), f(2), f(3), byte), f8_codes4(f(4), f(5), f(6), f(7), byte)};
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ u32x2_t eight_codes(const Eight<T>& v, uint32_t amax, uint32_t& byte) {
-  byte = f8_scale_byte(amax);
-  if (__builtin_expect(f8_not_finite(amax), 0)) {
-    byte = kF8One;
-    return u32x2_t{kF8NanCodes, kF8NanCodes};
-  }
-  return v.codes(byte);
-}
-
-// the codes of eight elements from column c on, those past the row's end 0
-__device__ __forceinline__ u32x2_t without_pad(u32x2_t q, int64_t c, int64_t cols) {
-  const int left = (int)(cols - c < 8 ? cols - c : 8);
-  return u32x2_t{f8_without_pad(q[0], left), f8_without_pad(q[1], left - 4)};
-}
 
 // A wavefront takes 512 columns (four blocks, sixteen lanes each, eight
 // elements a lane) of kRowsPerWave rows: all rows' loads in flight, then per
@@ -136,6 +56,109 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const T* __restrict__ a, int64
   }
 }
 
+// ---------------------------------------------------------------------------
+// What a tile's values come from, eight columns of a row at a time: `load` (all
+// of a thread's loads are in flight before the first is used), then `make`.
+// ---------------------------------------------------------------------------
+template <typename T>
+struct PlainSrc {   // a matrix as it is
+  using Type = T;
+  static constexpr bool kSums = false;
+  const T* a;
+  int64_t ld, bstride;
+  using Raw = Eight<T>;
+  struct Columns {};
+  __device__ __forceinline__ void columns(Columns&, int64_t, int64_t) const {}
+  __device__ __forceinline__ void load(Raw& v, int64_t b, int64_t row, int64_t c, int64_t cols) const {
+    v.load(a + b * bstride + row * ld, c, cols);
+  }
+  __device__ __forceinline__ void make(Eight<T>& v, const Raw& x, Columns&) const { v = x; }
+};
+
+// a norm's output from the sum it is of and each row's factor: the same
+// operations as k_norm's, so the same values
+template <typename T>
+struct NormSrc {
+  using Type = T;
+  static constexpr bool kSums = false;
+  const T* h;
+  int64_t ld;
+  const float* rstd;
+  const void* weight;
+  bool wbf16;
+  struct Raw {
+    Eight<T> h;
+    float rstd;
+    __device__ __forceinline__ void zero() {
+      h.zero();
+      rstd = 0.0f;
+    }
+  };
+  struct Columns {
+    float w[8];
+  };
+  __device__ __forceinline__ void columns(Columns& at, int64_t c, int64_t cols) const {
+    load_vector(weight, wbf16, c, cols, at.w);
+  }
+  __device__ __forceinline__ void load(Raw& v, int64_t, int64_t row, int64_t c, int64_t cols) const {
+    v.h.load(h + row * ld, c, cols);
+    v.rstd = rstd[row];
+  }
+  __device__ __forceinline__ void make(Eight<T>& v, const Raw& x, Columns& at) const {
+    float f[8];
+    x.h.f32(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] * x.rstd * at.w[i];
+    v.set(f);
+  }
+};
+
+// dy act'(z), and its sums over the rows (in fp32, before it is rounded)
+template <typename T>
+struct ActSrc {
+  using Type = T;
+  static constexpr bool kSums = true;
+  const T* dy;
+  const T* z;
+  int64_t lddy, ldz;
+  int act;
+  float* part;   // [chunk][column], or nullptr
+  struct Raw {
+    Eight<T> dy, z;
+    __device__ __forceinline__ void zero() {
+      dy.zero();
+      z.zero();
+    }
+  };
+  struct Columns {
+    float sum[8];
+  };
+  __device__ __forceinline__ void columns(Columns& at, int64_t, int64_t) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at.sum[i] = 0.0f;
+  }
+  __device__ __forceinline__ void load(Raw& v, int64_t, int64_t row, int64_t c, int64_t cols) const {
+    v.dy.load(dy + row * lddy, c, cols);
+    if (act != kActNone) v.z.load(z + row * ldz, c, cols);
+  }
+  __device__ __forceinline__ void make(Eight<T>& v, const Raw& x, Columns& at) const {
+    float f[8], z[8];
+    x.dy.f32(f);
+    x.z.f32(z);
+    if (act == kActRelu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = z[i] <= 0.0f ? 0.0f : f[i];   // (a NaN z lets f by)
+    } else if (act != kActNone) {
+      const ActSigmoid s(act);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= s.slope(z[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) at.sum[i] += f[i];
+    v.set(f);
+  }
+};
+
 // One 128 x 128 tile per workgroup of eight wavefronts.  Thread (r = t / 16,
 // i = t % 16) holds eight columns of rows r, r + 32, ..; a row's run is sixteen
 // lanes, so the plain copy comes from the registers.  The values go to LDS as
@@ -165,16 +188,19 @@ constexpr size_t fp8_tile_lds() {
   return (size_t)128 * 128 * sizeof(T) + (sizeof(T) == 2 ? 0 : 128 * 128) + kTileWaves * 64 * 4;
 }
 
-template <typename T, bool TILE>
-__global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
-    const T* __restrict__ a, int64_t rows, int64_t cols, int64_t lda, int64_t bstride,
-    const int64_t* offs, int nseg, int tx, bool near, Fp8Out out, Fp8Out out_t) {
+template <typename Src, bool TILE>
+__global__ __launch_bounds__(kTileThreads) void k_fp8_tile(Src source, int64_t rows, int64_t cols,
+                                                           const int64_t* offs, int nseg, int tx,
+                                                           bool near, Fp8Out out, Fp8Out out_t) {
+  using T = typename Src::Type;
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   T* raw = reinterpret_cast<T*>(sm);   // [128][128]
   // codes, [128 columns][128 rows]
   unsigned char* ct = sm + (sizeof(T) == 2 ? 0 : 128 * 128 * sizeof(T));
   // maxima: of rows, or a column's (column pair's) part of each wavefront
   uint32_t* red = reinterpret_cast<uint32_t*>(sm + fp8_tile_lds<T>()) - kTileWaves * 64;
+  // sums: a column's part of each wavefront
+  float* sums = reinterpret_cast<float*>(sm + fp8_tile_lds<T>());
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   uint32_t id = blockIdx.x;
   if (near && id < (gridDim.x & ~63u)) id = (id & ~63u) + (id & 7u) * 8u + (id >> 3 & 7u);
@@ -192,15 +218,43 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
     nr = rb - ra;
   }
   const int64_t b = blockIdx.z;
-  a += b * bstride;
   const int i = t & 15, r = t >> 4;
   constexpr int PER = 32 / kTileWaves, STEP = 4 * kTileWaves;   // rows a thread
-  Eight<T> v[PER];
+  typename Src::Raw raws[PER];
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
-    v[p].zero();
-    if (r + STEP * p < nr) v[p].load(a + (r0 + r + STEP * p) * lda, c0 + 8 * i, cols);
+    raws[p].zero();
+    if (r + STEP * p < nr) source.load(raws[p], b, r0 + r + STEP * p, c0 + 8 * i, cols);
   }
+  Eight<T> v[PER];
+  {
+    typename Src::Columns at;
+    source.columns(at, c0 + 8 * i, cols);
+#pragma unroll
+    for (int p = 0; p < PER; ++p) source.make(v[p], raws[p], at);
+    if constexpr (Src::kSums) {
+      // rows of a wavefront, then (below) its sums, in order
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        at.sum[q] += __shfl_xor(at.sum[q], 16, 64);
+        at.sum[q] += __shfl_xor(at.sum[q], 32, 64);
+      }
+      if (lane < 16) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sums[w * 128 + 8 * i + q] = at.sum[q];
+      }
+    }
+  }
+  auto sums_out = [&]() __attribute__((always_inline)) {
+    if constexpr (Src::kSums) {
+      if (t < 128 && c0 + t < cols && source.part) {
+        float s = sums[t];
+#pragma unroll
+        for (int q = 1; q < kTileWaves; ++q) s += sums[q * 128 + t];
+        source.part[(int64_t)chunk * cols + c0 + t] = s;
+      }
+    }
+  };
   uint32_t tile_max = 0;
   if constexpr (TILE) {
 #pragma unroll
@@ -228,7 +282,13 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
       }
     }
   }
-  if (!out_t.codes) return;
+  if (!out_t.codes) {
+    if constexpr (Src::kSums) {
+      __syncthreads();
+      sums_out();
+    }
+    return;
+  }
 #pragma unroll
   for (int p = 0; p < PER; ++p) {
     T* dst = raw + (r + STEP * p) * 128 + 8 * i;
@@ -240,6 +300,7 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
     }
   }
   __syncthreads();
+  sums_out();
   const int64_t orow = b * cols + c0;   // row of the transposed copy
   auto scale_out = [&](int col, uint32_t byte) {
     if (c0 + col < cols) out_t.scales[(orow + col) * out_t.spitch + chunk] = (uint8_t)byte;
@@ -343,20 +404,21 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(
   }
 }
 
-template <typename T, bool TILE>
-hipError_t tile_t(const void* a, int batch, int64_t rows, int64_t cols, int64_t lda,
-                  int64_t bstride, const int64_t* offs, int nseg, const Fp8Out& out,
-                  const Fp8Out& out_t, hipStream_t st) {
-  constexpr size_t lds = fp8_tile_lds<T>();
-  const hipError_t e = lds_attr_once<&k_fp8_tile<T, TILE>>((int)lds);
+// rows that do not start at a 128-byte line: neighbouring tiles share lines
+bool off_lines(const void* a, int64_t row_bytes) {
+  return ((reinterpret_cast<uintptr_t>(a) | (uintptr_t)row_bytes) & 127) != 0;
+}
+
+template <typename Src, bool TILE>
+hipError_t tile_t(const Src& src, bool near, int batch, int64_t rows, int64_t cols,
+                  const int64_t* offs, int nseg, const Fp8Out& out, const Fp8Out& out_t,
+                  hipStream_t st) {
+  constexpr size_t lds = fp8_tile_lds<typename Src::Type>() + (Src::kSums ? kTileWaves * 128 * 4 : 0);
+  const hipError_t e = lds_attr_once<&k_fp8_tile<Src, TILE>>((int)lds);
   if (e != hipSuccess) return e;
   const int64_t tx = (cols + 127) / 128;
-  // rows that do not start at a 128-byte line: neighbouring tiles share lines
-  const bool near = ((reinterpret_cast<uintptr_t>(a) | (uintptr_t)(lda * (int64_t)sizeof(T)) |
-                      (uintptr_t)(batch > 1 ? bstride * (int64_t)sizeof(T) : 0)) & 127) != 0;
   const dim3 g((unsigned)(tx * chunk_upper_bound(rows, offs ? nseg : 1, 128)), 1u, (unsigned)batch);
-  k_fp8_tile<T, TILE><<<g, kTileThreads, lds, st>>>(static_cast<const T*>(a), rows, cols, lda, bstride,
-                                           offs, nseg, (int)tx, near, out, out_t);
+  k_fp8_tile<Src, TILE><<<g, kTileThreads, lds, st>>>(src, rows, cols, offs, nseg, (int)tx, near, out, out_t);
   return hipGetLastError();
 }
 
@@ -389,11 +451,51 @@ hipError_t launch_fp8_tile(const void* a, bool bf16, bool tile, int batch, int64
                            int64_t cols, int64_t lda, int64_t bstride, const int64_t* offs,
                            int nseg, const Fp8Out& out, const Fp8Out& out_t, hipStream_t st) {
   if (rows == 0) return hipSuccess;
-  if (bf16)
-    return tile ? tile_t<uint16_t, true>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st)
-                : tile_t<uint16_t, false>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st);
-  return tile ? tile_t<float, true>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st)
-              : tile_t<float, false>(a, batch, rows, cols, lda, bstride, offs, nseg, out, out_t, st);
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    const PlainSrc<T> src{static_cast<const T*>(a), lda, bstride};
+    const bool near = off_lines(a, lda * (int64_t)sizeof(T)) ||
+                      (batch > 1 && off_lines(nullptr, bstride * (int64_t)sizeof(T)));
+    return tile ? tile_t<PlainSrc<T>, true>(src, near, batch, rows, cols, offs, nseg, out, out_t, st)
+                : tile_t<PlainSrc<T>, false>(src, near, batch, rows, cols, offs, nseg, out, out_t, st);
+  };
+  return bf16 ? run(uint16_t{}) : run(float{});
+}
+
+hipError_t launch_norm_tile(const void* h, bool bf16, int64_t rows, int64_t cols, int64_t ldh,
+                            const void* weight, bool wbf16, const float* rstd, const Fp8Out& out_t,
+                            hipStream_t st) {
+  if (rows == 0) return hipSuccess;
+  const Fp8Out none{nullptr, nullptr, 0, 0};
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    const NormSrc<T> src{static_cast<const T*>(h), ldh, rstd, weight, wbf16};
+    return tile_t<NormSrc<T>, false>(src, off_lines(h, ldh * (int64_t)sizeof(T)), 1, rows, cols,
+                                     nullptr, 1, none, out_t, st);
+  };
+  return bf16 ? run(uint16_t{}) : run(float{});
+}
+
+size_t act_grad_ws_bytes(int64_t rows, int64_t cols, int nseg) {
+  return ((size_t)chunk_upper_bound(rows, nseg, 128) * cols * 4 + 255) & ~(size_t)255;
+}
+
+hipError_t launch_act_grad(const void* dy, bool bf16, int64_t rows, int64_t cols, int64_t lddy,
+                           const void* z, int64_t ldz, int act, const int64_t* offs, int nseg,
+                           const Fp8Out& out, const Fp8Out& out_t, float* dbias, void* ws,
+                           hipStream_t st) {
+  float* part = dbias ? static_cast<float*>(ws) : nullptr;
+  auto run = [&](auto t) {
+    using T = decltype(t);
+    const ActSrc<T> src{static_cast<const T*>(dy), static_cast<const T*>(z), lddy, ldz, act, part};
+    return tile_t<ActSrc<T>, false>(src, off_lines(dy, lddy * (int64_t)sizeof(T)), 1, rows, cols,
+                                    offs, nseg, out, out_t, st);
+  };
+  if (rows > 0) {
+    const hipError_t e = bf16 ? run(uint16_t{}) : run(float{});
+    if (e != hipSuccess) return e;
+  }
+  return dbias ? launch_column_sums(part, rows, 128, cols, offs, nseg, dbias, st) : hipSuccess;
 }
 
 }  // namespace averis

@@ -201,6 +201,33 @@ hipError_t launch_moe_route_grad(const void* logits, bool bf16, int64_t tokens, 
                                  int64_t ld, int topk, bool renorm, const int32_t* ids,
                                  const float* dweights, void* dlogits, int64_t ldd,
                                  hipStream_t st);
+// routing by scores with a bias and groups of experts, and its gradient (moe_groups.hip)
+constexpr int kMaxGroups = 64;
+constexpr int kScoreSoftmax = 0, kScoreSigmoid = 1;
+struct RouteGroups {
+  int64_t tokens, ld;
+  int experts, topk;
+  const float* bias;   // or nullptr
+  int score, groups, topk_groups, group_top;
+  bool renorm;
+  float scale;
+  int32_t* ids;
+  float* weights;
+  int gsize;            // experts / groups
+  uint64_t gsize_inv;   // ceil(2^32 / gsize)
+  int group_lanes;      // set by the launch
+};
+struct RouteGroupsGrad {
+  int64_t tokens, ld, ldd;
+  int experts, topk, score;
+  bool renorm;
+  float scale;
+  const int32_t* ids;
+  const float* dweights;
+};
+hipError_t launch_route_groups(const void* logits, bool bf16, const RouteGroups& a, hipStream_t st);
+hipError_t launch_route_groups_grad(const void* logits, bool bf16, const RouteGroupsGrad& a,
+                                    void* dlogits, hipStream_t st);
 // counts per expert and chunk of slots (0 when one workgroup sorts them all)
 size_t moe_sort_ws_bytes(int64_t slots, int experts);
 hipError_t launch_moe_sort(const int32_t* ids, int64_t slots, int experts, int64_t* offsets,
@@ -255,6 +282,67 @@ hipError_t launch_fp8_rows(const void* a, bool bf16, int64_t rows, int64_t cols,
 hipError_t launch_fp8_tile(const void* a, bool bf16, bool tile, int batch, int64_t rows,
                            int64_t cols, int64_t lda, int64_t bstride, const int64_t* offs,
                            int nseg, const Fp8Out& out, const Fp8Out& out_t, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Root-mean-square norm with the residual's addition (norm.hip)
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxNormCols = 16384;   // a row in one workgroup's registers
+
+struct NormArgs {
+  const void* x;
+  const void* res;   // or nullptr
+  int64_t ldx, ldres;
+  const void* weight;
+  bool wbf16;
+  double eps;
+  void* h;   // x + res, where there is a res
+  int64_t ldh;
+  void* y;   // or nullptr
+  int64_t ldy;
+  float* rstd;
+};
+// out: runs along the columns (may be empty)
+hipError_t launch_norm(const NormArgs& a, bool bf16, int64_t rows, int64_t cols, const Fp8Out& out,
+                       hipStream_t st);
+// the transposed copy of the norm's output from h and rstd (fp8_quant.hip)
+hipError_t launch_norm_tile(const void* h, bool bf16, int64_t rows, int64_t cols, int64_t ldh,
+                            const void* weight, bool wbf16, const float* rstd, const Fp8Out& out_t,
+                            hipStream_t st);
+
+struct NormGradArgs {
+  const void* dy;
+  const void* h;
+  const void* dres;   // or nullptr
+  int64_t lddy, ldh, lddres;
+  const void* weight;
+  bool wbf16;
+  const float* rstd;
+  void* dh;
+  int64_t lddh;
+  float* dweight;   // or nullptr
+};
+size_t norm_grad_ws_bytes(int64_t rows, int64_t cols);
+hipError_t launch_norm_grad(const NormGradArgs& a, bool bf16, int64_t rows, int64_t cols, void* ws,
+                            hipStream_t st);
+
+// out[s][c]: the sum of part[i][c] over the chunks i of segment s, in order, the
+// chunks being of `ch` of the `rows` rows (offs: the rows' segments or nullptr)
+hipError_t launch_column_sums(const float* part, int64_t rows, int64_t ch, int64_t cols,
+                              const int64_t* offs, int nseg, float* out, hipStream_t st);
+
+// ---------------------------------------------------------------------------
+// Activations (activation.hpp) and the way back through one (fp8_quant.hip)
+// ---------------------------------------------------------------------------
+constexpr int64_t kMaxActCols = (int64_t)1 << 27;   // 16 threads each in the sums' grid
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
+
+size_t act_grad_ws_bytes(int64_t rows, int64_t cols, int nseg);
+// dy act'(z) quantized into out and out_t (each may be empty), its sums by
+// segment into dbias (or nullptr; ws: act_grad_ws_bytes)
+hipError_t launch_act_grad(const void* dy, bool bf16, int64_t rows, int64_t cols, int64_t lddy,
+                           const void* z, int64_t ldz, int act, const int64_t* offs, int nseg,
+                           const Fp8Out& out, const Fp8Out& out_t, float* dbias, void* ws,
+                           hipStream_t st);
 
 // What a product contracts: all of k_blocks blocks of 128 (kAll), rows of a
 // and c by segment with a stack of b (kRowSegs), or a range of blocks for each
