@@ -640,6 +640,28 @@ averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
                                 averis_dtype_t cdtype, int64_t ldc, void* ws, size_t ws_bytes,
                                 hipStream_t stream);
 
+/* Activations: z, max(z, 0), z / (1 + e^-z), and the tanh form of gelu,
+ * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum {
+  AVERIS_ACT_NONE = 0,
+  AVERIS_ACT_RELU = 1,
+  AVERIS_ACT_SILU = 2,
+  AVERIS_ACT_GELU = 3
+} averis_act_t;
+
+/* averis_fp8_gemm with an epilogue: z = deq(a) deq(b)^T + 1 bias^T, c = act(z) +
+ * residual, in fp32 and rounded once to c's type.  bias: n values (F32 or BF16;
+ * with segments n for each, nseg x n), or NULL.  residual: m x n of c's type, row
+ * stride ldr, or NULL; it may be c.  z: also written, m x n of c's type, row stride
+ * ldz, for averis_fp8_act_grad, or NULL.  An infinite z with a smooth activation
+ * gives what the formula gives (-inf: NaN).  Everything else, the workspace too,
+ * as for averis_fp8_gemm. */
+averis_status_t averis_fp8_gemm_act(const averis_fp8_t* a, const averis_fp8_t* b, const void* bias,
+                                    averis_dtype_t bias_dtype, averis_act_t act,
+                                    const void* residual, int64_t ldr, const int64_t* seg_offsets,
+                                    int nseg, void* c, averis_dtype_t cdtype, int64_t ldc, void* z,
+                                    int64_t ldz, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* dw = deq(xt) deq(dt)^T over the tokens: xt m x rows and dt n x rows from
  * averis_fp8_quant's out_t, dw m x n (F32 or BF16, row stride lddw).  With
  * seg_offsets (those of the quantization; xt and dt then have
@@ -697,15 +719,6 @@ averis_status_t averis_rmsnorm_grad(const void* dy, averis_dtype_t dtype, int64_
                                     const void* dres, int64_t lddres, void* dh, int64_t lddh,
                                     float* dweight, void* ws, size_t ws_bytes,
                                     hipStream_t stream);
-
-/* Activations: z, max(z, 0), z / (1 + e^-z), and the tanh form of gelu,
- * z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
-typedef enum {
-  AVERIS_ACT_NONE = 0,
-  AVERIS_ACT_RELU = 1,
-  AVERIS_ACT_SILU = 2,
-  AVERIS_ACT_GELU = 3
-} averis_act_t;
 
 /* dz = dy act'(z) (rows x cols; fp32, relu's slope at 0 is 0, the smooth ones'
  * at +-inf 1 and 0): rounded to the type of dy and z and quantized into out and

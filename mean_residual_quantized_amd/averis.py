@@ -45,7 +45,7 @@ EXPORTS = [
     "averis_moe_route", "averis_moe_route_grad", "averis_moe_sort", "averis_moe_dispatch",
     "averis_moe_combine", "averis_moe_combine_grad", "averis_grad_norm", "averis_grad_clip",
     "averis_fp8_seg_cols", "averis_fp8_quant", "averis_fp8_quant_weight", "averis_fp8_gemm",
-    "averis_fp8_gemm_wgrad", "averis_rmsnorm", "averis_rmsnorm_grad", "averis_fp8_act_grad",
+    "averis_fp8_gemm_wgrad", "averis_fp8_gemm_act", "averis_rmsnorm", "averis_rmsnorm_grad", "averis_fp8_act_grad",
     "averis_moe_route_groups", "averis_moe_route_groups_grad",
     "averis_workspace_bytes", "averis_status_str",
     "averis_abi_version", "averis_last_error",
@@ -129,6 +129,7 @@ def lib():
             "averis_fp8_quant_weight": [P, I, I, I64, I64, I64, I64, F8, F8, P],
             "averis_fp8_gemm": [F8, F8, P, I, P, I, I64, P, SZ, P],
             "averis_fp8_gemm_wgrad": [F8, F8, I64, P, I, P, I, I64, P, SZ, P],
+            "averis_fp8_gemm_act": [F8, F8, P, I, I, P, I64, P, I, P, I, I64, P, I64, P, SZ, P],
             "averis_rmsnorm": [P, I, I64, I64, I64, P, I64, P, I, ctypes.c_double, P, I64, P, I64, P,
                                F8, F8, P],
             "averis_rmsnorm_grad": [P, I, I64, I64, I64, P, I64, P, I, P, P, I64, P, I64, P, P, SZ, P],
@@ -1051,6 +1052,38 @@ def averis_rmsnorm_grad(dy, h, weight, rstd, dres=None, out=None, ws=None):
         rstd.data_ptr(), _addr(dres), ldr, out.data_ptr(), ldo, dweight.data_ptr(),
         _addr(ws), ws.numel() if ws is not None else 0, _stream_on(dy)))
     return out, dweight
+
+
+def averis_fp8_gemm_act(a, b, bias=None, act="none", residual=None, save=False,
+                        out_dtype=torch.bfloat16, offsets=None, out=None, ws=None):
+    """c = act(z) + residual, z = deq(a) deq(b)^T + bias; act one of "none",
+    "relu", "silu", "gelu" (its tanh form).  bias: float32 or bfloat16, [n], with
+    offsets (as for averis_fp8_gemm) [nseg, n]; residual: of c's type, may be out.
+    Returns c, or with save (c, z) for averis_fp8_act_grad."""
+    dev = _one_device(a, b)
+    offs, nseg = _segments(offsets, a.codes)
+    m, k, n = a.rows, a.cols, b.rows // nseg
+    c, ldc = out, n
+    if out is None:
+        c = _new(m, n, out_dtype, dev)
+    else:
+        ldc = _matrix(c, c, "out", (m, n))
+        if c.device != dev:
+            raise ValueError("out: expected a tensor on %s" % dev)
+    bcode = 0
+    if bias is not None:
+        shape = (n,) if offsets is None else (nseg, n)
+        if bias.shape != shape or not bias.is_contiguous() or bias.device != dev:
+            raise ValueError("bias: expected a contiguous tensor of shape %s on %s" % (shape, dev))
+        bcode = _dtype_code(bias)
+    ldr = _matrix(residual, c, "residual", (m, n)) if residual is not None else 0
+    z = _new(m, n, c.dtype, dev) if save else None
+    ws = _ws(ws, OP_FP8_GEMM, (m, k, n, 0 if offsets is None else nseg), dev)
+    _check("averis_fp8_gemm_act", lib().averis_fp8_gemm_act(
+        a.c(), b.c(), _addr(bias), bcode, _choice(ACTS, act, "act"), _addr(residual), ldr, offs, nseg,
+        c.data_ptr(), _dtype_code(c), ldc, _addr(z), n, _addr(ws), ws.numel() if ws is not None else 0,
+        _stream_on(c)))
+    return (c, z) if save else c
 
 
 def averis_fp8_act_grad(dy, z=None, act="none", plain=True, transposed=True, bias=True, offsets=None,

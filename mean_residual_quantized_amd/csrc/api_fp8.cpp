@@ -57,10 +57,11 @@ averis_status_t averis_fp8_quant_weight(const void* w, averis_dtype_t dtype, int
                                     batch_stride, nullptr, 1, out_of(out), out_of(out_t), stream));
 }
 
-averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
-                                const int64_t* seg_offsets, int nseg, void* c,
-                                averis_dtype_t cdtype, int64_t ldc, void* ws, size_t ws_bytes,
-                                hipStream_t stream) {
+static averis_status_t gemm_common(const averis_fp8_t* a, const averis_fp8_t* b,
+                                   const int64_t* seg_offsets, int nseg, void* c,
+                                   averis_dtype_t cdtype, int64_t ldc,
+                                   const Fp8Epilogue* epilogue, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
   if (!a || !b) return AVERIS_E_NULL;
   averis_status_t s = check_segs(seg_offsets, nseg);
   if (s != AVERIS_OK) return s;
@@ -73,12 +74,35 @@ averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
   if ((s = check_fp8(a, m, k)) != AVERIS_OK) return s;
   if ((s = check_fp8(b, b->rows, k)) != AVERIS_OK) return s;
   if ((s = check_c(c, cdtype, m, n, ldc)) != AVERIS_OK) return s;
+  if (epilogue) {
+    if (epilogue->res && (s = check_c(epilogue->res, cdtype, m, n, epilogue->ldr)) != AVERIS_OK) return s;
+    if (epilogue->z && (s = check_c(epilogue->z, cdtype, m, n, epilogue->ldz)) != AVERIS_OK) return s;
+  }
   const Fp8Gemm g{operand_of(a), operand_of(b), m, n, (k + 127) / 128,
                   seg_offsets ? kF8RowSegs : kF8All, seg_offsets, nseg, m, c,
-                  cdtype == AVERIS_BF16, ldc};
+                  cdtype == AVERIS_BF16, ldc, epilogue};
   if ((s = check_ws(ws, ws_bytes, fp8_gemm_ws_bytes(m, n, g.k_blocks, g.mode, nseg))) != AVERIS_OK)
     return s;
   return hip_status(launch_fp8_gemm(g, ws, stream));
+}
+
+averis_status_t averis_fp8_gemm(const averis_fp8_t* a, const averis_fp8_t* b,
+                                const int64_t* seg_offsets, int nseg, void* c,
+                                averis_dtype_t cdtype, int64_t ldc, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  return gemm_common(a, b, seg_offsets, nseg, c, cdtype, ldc, nullptr, ws, ws_bytes, stream);
+}
+
+averis_status_t averis_fp8_gemm_act(const averis_fp8_t* a, const averis_fp8_t* b, const void* bias,
+                                    averis_dtype_t bias_dtype, averis_act_t act,
+                                    const void* residual, int64_t ldr, const int64_t* seg_offsets,
+                                    int nseg, void* c, averis_dtype_t cdtype, int64_t ldc, void* z,
+                                    int64_t ldz, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (act < AVERIS_ACT_NONE || act > AVERIS_ACT_GELU) return AVERIS_E_ARG;
+  if (bias && !dtype_ok(bias_dtype)) return AVERIS_E_DTYPE;
+  if (bias && !aligned(bias, elem_size(bias_dtype))) return AVERIS_E_ALIGN;
+  const Fp8Epilogue e{bias, bias && bias_dtype == AVERIS_BF16, act, residual, ldr, z, ldz};
+  return gemm_common(a, b, seg_offsets, nseg, c, cdtype, ldc, &e, ws, ws_bytes, stream);
 }
 
 averis_status_t averis_fp8_gemm_wgrad(const averis_fp8_t* xt, const averis_fp8_t* dt,
@@ -102,7 +126,7 @@ averis_status_t averis_fp8_gemm_wgrad(const averis_fp8_t* xt, const averis_fp8_t
   if ((s = check_c(dw, dwdtype, m, n, lddw)) != AVERIS_OK) return s;
   const Fp8Gemm g{operand_of(xt), operand_of(dt), m, n, (k + 127) / 128,
                   seg_offsets ? kF8BlockSegs : kF8All, seg_offsets, nseg, rows, dw,
-                  dwdtype == AVERIS_BF16, lddw};
+                  dwdtype == AVERIS_BF16, lddw, nullptr};
   if ((s = check_ws(ws, ws_bytes, fp8_gemm_ws_bytes(m, n, g.k_blocks, g.mode, nseg))) != AVERIS_OK)
     return s;
   return hip_status(launch_fp8_gemm(g, ws, stream));

@@ -18,6 +18,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
+#include "activation.hpp"
 #include "fp8_common.hpp"
 #include "launch.hpp"
 #include "segments.hpp"
@@ -80,6 +83,112 @@ struct F8Tile {
 };
 
 // ---------------------------------------------------------------------------
+// Epilogues: four neighbouring columns of a row
+// ---------------------------------------------------------------------------
+struct NoEpilogue {};
+template <bool EPI>
+using EpilogueArg = std::conditional_t<EPI, Fp8Epilogue, NoEpilogue>;
+
+// at element alignment, as f8_piece_t
+typedef u32x2_t f8_half_piece_t __attribute__((aligned(2)));
+template <bool BF16>
+using Four = std::conditional_t<BF16, u32x2_t, u32x4_t>;
+
+// elements at .. at + 3 of p, the first `left` of them (the others 0)
+template <bool BF16>
+__device__ __forceinline__ Four<BF16> four_in(const void* p, int64_t at, int left) {
+  Four<BF16> v = {};
+  if constexpr (BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    if (left >= 4) return *reinterpret_cast<const f8_half_piece_t*>(q);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (x < left) v[x / 2] |= (uint32_t)q[x] << (16 * (x & 1));
+  } else {
+    const uint32_t* q = static_cast<const uint32_t*>(p) + at;
+    if (left >= 4) return *reinterpret_cast<const f8_piece_t*>(q);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (x < left) v[x] = q[x];
+  }
+  return v;
+}
+template <bool BF16>
+__device__ __forceinline__ f32x4_t four_f32(Four<BF16> v) {
+  if constexpr (BF16)
+    return f32x4_t{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u),
+                   __uint_as_float(v[1] << 16), __uint_as_float(v[1] & 0xFFFF0000u)};
+  else
+    return f32x4_t{__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
+                   __uint_as_float(v[3])};
+}
+template <bool BF16>
+__device__ __forceinline__ void four_out(void* p, int64_t at, int left, f32x4_t f) {
+  if constexpr (BF16) {
+    uint16_t* q = static_cast<uint16_t*>(p) + at;
+    const u32x2_t v = {bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])};
+    if (left >= 4) {
+      *reinterpret_cast<f8_half_piece_t*>(q) = v;
+      return;
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (x < left) q[x] = (uint16_t)(v[x / 2] >> (16 * (x & 1)));
+  } else {
+    float* q = static_cast<float*>(p) + at;
+    if (left >= 4) {
+      *reinterpret_cast<f8_piece_t*>(q) = u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]),
+                                                  __float_as_uint(f[2]), __float_as_uint(f[3])};
+      return;
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+      if (x < left) q[x] = f[x];
+  }
+}
+
+__device__ __forceinline__ float activated(float z, int act) {
+  if (act == kActNone) return z;
+  if (act == kActRelu) return z < 0.0f ? 0.0f : z;
+  return ActSigmoid(act).value(z);
+}
+template <int N>
+__device__ __forceinline__ void activate(f32x4_t (&v)[N], int act) {
+  if (act == kActNone) return;
+  if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) v[i][x] = v[i][x] < 0.0f ? 0.0f : v[i][x];   // (a NaN stays)
+    return;
+  }
+  const ActSigmoid s(act);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[i][x] = s.value(v[i][x]);
+}
+
+// the epilogue of one value: row, column of c, column j of the bias
+template <bool OUT_BF16>
+__device__ __forceinline__ void epilogue_one(const Fp8Epilogue& e, void* c, int64_t ldc, int64_t row,
+                                             int64_t col, int64_t j, float s) {
+  auto in = [](const void* p, bool bf16, int64_t at) {
+    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at] << 16)
+                : static_cast<const float*>(p)[at];
+  };
+  auto out = [](void* p, int64_t at, float v) {
+    if constexpr (OUT_BF16) static_cast<uint16_t*>(p)[at] = (uint16_t)bf16x2_rne(v, 0.0f);
+    else static_cast<float*>(p)[at] = v;
+  };
+  if (e.bias) s += in(e.bias, e.bias_bf16, j);
+  if (e.z) out(e.z, row * e.ldz + col, s);
+  s = activated(s, e.act);
+  if (e.res) s += in(e.res, OUT_BF16, row * e.ldr + col);
+  out(c, row * ldc + col, s);
+}
+
+// ---------------------------------------------------------------------------
 // The tiled kernel: 64 F x 64 F outputs a tile, each of four wavefronts 32 F x
 // 32 F of them (F x F accumulators of 32 x 32): F = 4, one workgroup a CU, or 2
 // (128 x 128), two.
@@ -112,10 +221,11 @@ struct F8Tile {
 // slower on large products (half lines a load, a barrier more a block) and no
 // faster where the operands come from memory.
 // ---------------------------------------------------------------------------
-template <int F, bool OUT_BF16, int MODE>
+template <int F, bool OUT_BF16, int MODE, bool EPI>
 __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     Fp8Operand A, Fp8Operand B, int m, int n, int k_blocks, const int64_t* offs, int nseg,
-    int64_t seg_rows, int splits, int tx, int ty, void* c, int64_t ldc, int64_t c_split) {
+    int64_t seg_rows, int splits, int tx, int ty, void* c, int64_t ldc, int64_t c_split,
+    EpilogueArg<EPI> epi) {
   constexpr bool MANY = MODE != kF8BlockSegs;   // several tiles a workgroup
   constexpr int SLOTS = F == 4 ? kF8Cus : 2 * kF8Cus;   // workgroups the card holds
   constexpr int BM = 64 * F, BN = 64 * F, ROWS = BM + BN;
@@ -125,7 +235,9 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   static_assert(SPW * 256 == ROWS, "every wavefront's loads are whole");
   constexpr int NF = 2 * F;
   constexpr int ES = OUT_BF16 ? 2 : 4;
-  constexpr int GROUP = 128 / ES;      // columns of an output pass: 128 bytes
+  // an epilogue takes the sums in fp32, whatever the output's type
+  constexpr bool STAGE_BF16 = OUT_BF16 && !EPI;
+  constexpr int GROUP = STAGE_BF16 ? 64 : 32;   // columns of an output pass: 128 bytes
   constexpr int PASSES = (32 * F + GROUP - 1) / GROUP;   // of a 32-row fragment
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_f8[];
   unsigned char* ring = smem_f8;
@@ -445,7 +557,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     u32x4_t out[4];   // a bf16 pass's values: pieces of two fragments
     auto form = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
-      if constexpr (OUT_BF16) {
+      if constexpr (STAGE_BF16) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           // fragment u / 2, column groups 8 q and 8 q + 8, q = 2 (u mod 2)
@@ -465,7 +577,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t at = wr ^ (32 * u);
-        if constexpr (OUT_BF16) {
+        if constexpr (STAGE_BF16) {
           const u32x4_t v = out[u];
           asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
         } else {
@@ -475,13 +587,70 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
         }
       }
     };
-    const int row0 = wm * 32 * F + (ln >> 3), col0 = wn * 32 * F + (ln & 7) * (16 / ES);
+    const int row0 = wm * 32 * F + (ln >> 3), col0 = wn * 32 * F + (ln & 7) * (STAGE_BF16 ? 8 : 4);
     auto clear = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
 #pragma unroll
       for (int f = 0; f < FPP; ++f) zero(i, p * FPP + f);
     };
-    if (pieces) {
+    if constexpr (EPI) {
+      // A lane has four columns of four rows a pass.  The next pass's residual
+      // is on its way while this one's values are formed.
+      if (HELD == 0 && loads) first_loads(nxt.nk);
+      const int64_t at0 = (int64_t)cur.m0 + row0;
+      auto left = [&](int p) __attribute__((always_inline)) { return cur.cols - col0 - p * GROUP; };
+      f32x4_t bias[PASSES];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        bias[p] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        if (!epi.bias) continue;
+        const int64_t j = (MODE == kF8RowSegs ? (int64_t)cur.seg * n : 0) + cur.n0 + col0 + p * GROUP;
+        bias[p] = epi.bias_bf16 ? four_f32<true>(four_in<true>(epi.bias, j, left(p)))
+                                : four_f32<false>(four_in<false>(epi.bias, j, left(p)));
+      }
+      Four<OUT_BF16> res[2][4];
+      auto load_res = [&](auto pc) __attribute__((always_inline)) {
+        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
+        if (!epi.res) return;
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+          if (row0 + 32 * i + 8 * it < cur.rows)
+            res[P & 1][it] = four_in<OUT_BF16>(
+                epi.res, (at0 + 32 * i + 8 * it) * epi.ldr + cur.n0 + col0 + p * GROUP, left(p));
+      };
+      load_res(F8Step<0>{});
+      each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
+        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
+        to_lds(pc);
+        clear(pc);
+        f32x4_t v[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const f32x4_t*>(src + it * STG_STEP);
+        if constexpr (P + 1 < OUT_PASSES) load_res(F8Step<P + 1>{});
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) v[it] += bias[p];
+        const int64_t col = cur.n0 + col0 + p * GROUP;
+        if (epi.z) {
+#pragma unroll
+          for (int it = 0; it < 4; ++it)
+            if (row0 + 32 * i + 8 * it < cur.rows)
+              four_out<OUT_BF16>(epi.z, (at0 + 32 * i + 8 * it) * epi.ldz + col, left(p), v[it]);
+        }
+        activate(v, epi.act);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          if (row0 + 32 * i + 8 * it >= cur.rows) continue;
+          if (epi.res) v[it] += four_f32<OUT_BF16>(res[P & 1][it]);
+          four_out<OUT_BF16>(c, (at0 + 32 * i + 8 * it) * ldc + col, left(p), v[it]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (HELD > 0) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        if (loads) first_loads(nxt.nk);
+      }
+    } else if (pieces) {
       const uint32_t ldb = (uint32_t)(ldc * ES);
       // below 2^31: a lane past the columns goes to 2^31 and on
       const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
@@ -555,7 +724,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     }
     __builtin_amdgcn_sched_barrier(0);
     if (!more) break;
-    behind = pieces;
+    behind = !EPI && pieces;
     cur = nxt;
   }
 }
@@ -570,11 +739,12 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyWaves = 8;
 
-template <int MF, bool OUT_BF16>
+template <int MF, bool OUT_BF16, bool EPI>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_f8_skinny(Fp8Operand A, Fp8Operand B,
                                                                       int64_t m, int64_t n,
                                                                       int k_blocks, void* c,
-                                                                      int64_t ldc) {
+                                                                      int64_t ldc,
+                                                                      EpilogueArg<EPI> epi) {
   __shared__ float part[kSkinnyWaves][16][16 * MF + 4];   // [..][column][row]
   const int64_t m0 = (int64_t)blockIdx.y * 16 * MF, n0 = (int64_t)blockIdx.x * 16;
   const int lane = threadIdx.x & 63;
@@ -637,6 +807,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_f8_skinny(Fp8Operand
     float s = part[0][col][row];
 #pragma unroll
     for (int q = 1; q < kSkinnyWaves; ++q) s += part[q][col][row];
+    if constexpr (EPI) {
+      epilogue_one<OUT_BF16>(epi, c, ldc, m0 + row, n0 + col, n0 + col, s);
+      continue;
+    }
     const int64_t o = (m0 + row) * ldc + n0 + col;
     if constexpr (OUT_BF16)
       static_cast<uint16_t*>(c)[o] = (uint16_t)bf16x2_rne(s, 0.0f);
@@ -646,9 +820,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_f8_skinny(Fp8Operand
 }
 
 // sums the splits' fp32 partials in order
-template <bool OUT_BF16>
+template <bool OUT_BF16, bool EPI>
 __global__ __launch_bounds__(256) void k_f8_reduce(const float* __restrict__ part, int splits,
-                                                   int64_t m, int64_t n, void* c, int64_t ldc) {
+                                                   int64_t m, int64_t n, void* c, int64_t ldc,
+                                                   EpilogueArg<EPI> epi) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int64_t mn = m * n;
   if (e >= mn) return;
@@ -667,6 +842,26 @@ __global__ __launch_bounds__(256) void k_f8_reduce(const float* __restrict__ par
     }
   }
   const int64_t row = e / n, col = e - row * n;
+  if constexpr (EPI) {
+    if (col + 4 <= n) {   // four of one row
+      f32x4_t v[1] = {f32x4_t{s[0], s[1], s[2], s[3]}};
+      if (epi.bias)
+        v[0] += epi.bias_bf16 ? four_f32<true>(four_in<true>(epi.bias, col, 4))
+                              : four_f32<false>(four_in<false>(epi.bias, col, 4));
+      if (epi.z) four_out<OUT_BF16>(epi.z, row * epi.ldz + col, 4, v[0]);
+      activate(v, epi.act);
+      if (epi.res) v[0] += four_f32<OUT_BF16>(four_in<OUT_BF16>(epi.res, row * epi.ldr + col, 4));
+      four_out<OUT_BF16>(c, row * ldc + col, 4, v[0]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (e + i >= mn) break;
+      const int64_t rr = (e + i) / n, cc = (e + i) - rr * n;
+      epilogue_one<OUT_BF16>(epi, c, ldc, rr, cc, cc, s[i]);
+    }
+    return;
+  }
   if (OUT_BF16 && whole && col + 4 <= n && ldc % 4 == 0 && (n & 3) == 0 &&
       (reinterpret_cast<uintptr_t>(c) & 7) == 0) {
     *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(c) + row * ldc + col) =
@@ -758,12 +953,12 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg)
   return best;
 }
 
-template <int F, bool OB, int MODE>
+template <int F, bool OB, int MODE, bool EPI>
 hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
-                     hipStream_t st) {
+                     const EpilogueArg<EPI>& epi, hipStream_t st) {
   constexpr size_t lds = f8_lds_bytes(F);
   static_assert(lds <= 160 * 1024 / (F == 4 ? 1 : 2), "fits one CU's LDS");
-  const hipError_t e = lds_attr_once<&k_gemm_f8<F, OB, MODE>>((int)lds);
+  const hipError_t e = lds_attr_once<&k_gemm_f8<F, OB, MODE, EPI>>((int)lds);
   if (e != hipSuccess) return e;
   const int64_t ty = MODE == kF8RowSegs ? chunk_upper_bound(g.m, g.nseg, 64 * F)
                                         : (g.m + 64 * F - 1) / (64 * F);
@@ -771,41 +966,62 @@ hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t
   const int64_t tiles = tx * ty * (MODE == kF8BlockSegs ? g.nseg : splits);
   constexpr int slots = F == 4 ? kF8Cus : 2 * kF8Cus;
   const int64_t grid = MODE != kF8BlockSegs && tiles > slots ? slots : tiles;
-  k_gemm_f8<F, OB, MODE><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(
+  k_gemm_f8<F, OB, MODE, EPI><<<dim3((unsigned)grid), kF8Threads, lds, st>>>(
       g.a, g.b, (int)g.m, (int)g.n, (int)g.k_blocks, g.offs, g.nseg, g.rows, splits, (int)tx,
-      (int)ty, c, ldc, c_split);
+      (int)ty, c, ldc, c_split, epi);
   return hipGetLastError();
 }
 
 template <int F, bool OB>
 hipError_t gemm_f8_mode(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
-                        hipStream_t st) {
+                        const Fp8Epilogue* epi, hipStream_t st) {
+  if (epi)   // (of a product by block segments: none)
+    return g.mode == kF8RowSegs
+               ? gemm_f8_t<F, OB, kF8RowSegs, true>(g, splits, c, ldc, c_split, *epi, st)
+               : gemm_f8_t<F, OB, kF8All, true>(g, splits, c, ldc, c_split, *epi, st);
+  const NoEpilogue no;
   switch (g.mode) {
-    case kF8RowSegs: return gemm_f8_t<F, OB, kF8RowSegs>(g, splits, c, ldc, c_split, st);
-    case kF8BlockSegs: return gemm_f8_t<F, OB, kF8BlockSegs>(g, splits, c, ldc, c_split, st);
-    default: return gemm_f8_t<F, OB, kF8All>(g, splits, c, ldc, c_split, st);
+    case kF8RowSegs: return gemm_f8_t<F, OB, kF8RowSegs, false>(g, splits, c, ldc, c_split, no, st);
+    case kF8BlockSegs: return gemm_f8_t<F, OB, kF8BlockSegs, false>(g, splits, c, ldc, c_split, no, st);
+    default: return gemm_f8_t<F, OB, kF8All, false>(g, splits, c, ldc, c_split, no, st);
   }
 }
 
 hipError_t gemm_f8(const Fp8Gemm& g, const Fp8Plan& p, bool bf16, void* c, int64_t ldc,
-                   int64_t c_split, hipStream_t st) {
+                   int64_t c_split, const Fp8Epilogue* epi, hipStream_t st) {
   if (p.f == 2)
-    return bf16 ? gemm_f8_mode<2, true>(g, p.splits, c, ldc, c_split, st)
-                : gemm_f8_mode<2, false>(g, p.splits, c, ldc, c_split, st);
-  return bf16 ? gemm_f8_mode<4, true>(g, p.splits, c, ldc, c_split, st)
-              : gemm_f8_mode<4, false>(g, p.splits, c, ldc, c_split, st);
+    return bf16 ? gemm_f8_mode<2, true>(g, p.splits, c, ldc, c_split, epi, st)
+                : gemm_f8_mode<2, false>(g, p.splits, c, ldc, c_split, epi, st);
+  return bf16 ? gemm_f8_mode<4, true>(g, p.splits, c, ldc, c_split, epi, st)
+              : gemm_f8_mode<4, false>(g, p.splits, c, ldc, c_split, epi, st);
+}
+
+template <int MF, bool EPI>
+hipError_t skinny_t(const Fp8Gemm& g, const EpilogueArg<EPI>& epi, hipStream_t st) {
+  const dim3 grid((unsigned)((g.n + 15) / 16), (unsigned)((g.m + 16 * MF - 1) / (16 * MF)));
+  if (g.c_bf16)
+    k_gemm_f8_skinny<MF, true, EPI><<<grid, 64 * kSkinnyWaves, 0, st>>>(
+        g.a, g.b, g.m, g.n, (int)g.k_blocks, g.c, g.ldc, epi);
+  else
+    k_gemm_f8_skinny<MF, false, EPI><<<grid, 64 * kSkinnyWaves, 0, st>>>(
+        g.a, g.b, g.m, g.n, (int)g.k_blocks, g.c, g.ldc, epi);
+  return hipGetLastError();
+}
+
+template <bool EPI>
+hipError_t reduce_t(const Fp8Gemm& g, const void* part, int splits, const EpilogueArg<EPI>& epi,
+                    hipStream_t st) {
+  const dim3 grid((unsigned)((g.m * g.n + 1023) / 1024));
+  if (g.c_bf16)
+    k_f8_reduce<true, EPI><<<grid, 256, 0, st>>>(static_cast<const float*>(part), splits, g.m, g.n, g.c, g.ldc, epi);
+  else
+    k_f8_reduce<false, EPI><<<grid, 256, 0, st>>>(static_cast<const float*>(part), splits, g.m, g.n, g.c, g.ldc, epi);
+  return hipGetLastError();
 }
 
 template <int MF>
-hipError_t skinny_t(const Fp8Gemm& g, hipStream_t st) {
-  const dim3 grid((unsigned)((g.n + 15) / 16), (unsigned)((g.m + 16 * MF - 1) / (16 * MF)));
-  if (g.c_bf16)
-    k_gemm_f8_skinny<MF, true><<<grid, 64 * kSkinnyWaves, 0, st>>>(g.a, g.b, g.m, g.n,
-                                                                   (int)g.k_blocks, g.c, g.ldc);
-  else
-    k_gemm_f8_skinny<MF, false><<<grid, 64 * kSkinnyWaves, 0, st>>>(g.a, g.b, g.m, g.n,
-                                                                    (int)g.k_blocks, g.c, g.ldc);
-  return hipGetLastError();
+hipError_t skinny(const Fp8Gemm& g, hipStream_t st) {
+  return g.epilogue ? skinny_t<MF, true>(g, *g.epilogue, st) : skinny_t<MF, false>(g, NoEpilogue{}, st);
 }
 
 }  // namespace
@@ -818,20 +1034,16 @@ size_t fp8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, i
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
   const Fp8Plan p = fp8_plan(g.m, g.n, g.k_blocks, g.mode, g.nseg);
-  if (p.skinny == 1) return skinny_t<1>(g, st);
-  if (p.skinny == 2) return skinny_t<2>(g, st);
-  if (p.skinny == 4) return skinny_t<4>(g, st);
+  if (p.skinny == 1) return skinny<1>(g, st);
+  if (p.skinny == 2) return skinny<2>(g, st);
+  if (p.skinny == 4) return skinny<4>(g, st);
   if (p.splits > 1) {
-    const hipError_t e = gemm_f8(g, p, false, ws, g.n, g.m * g.n, st);
+    const hipError_t e = gemm_f8(g, p, false, ws, g.n, g.m * g.n, nullptr, st);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)((g.m * g.n + 1023) / 1024));
-    if (g.c_bf16)
-      k_f8_reduce<true><<<grid, 256, 0, st>>>(static_cast<const float*>(ws), p.splits, g.m, g.n, g.c, g.ldc);
-    else
-      k_f8_reduce<false><<<grid, 256, 0, st>>>(static_cast<const float*>(ws), p.splits, g.m, g.n, g.c, g.ldc);
-    return hipGetLastError();
+    return g.epilogue ? reduce_t<true>(g, ws, p.splits, *g.epilogue, st)
+                      : reduce_t<false>(g, ws, p.splits, NoEpilogue{}, st);
   }
-  return gemm_f8(g, p, g.c_bf16, g.c, g.ldc, g.mode == kF8BlockSegs ? g.m * g.ldc : 0, st);
+  return gemm_f8(g, p, g.c_bf16, g.c, g.ldc, g.mode == kF8BlockSegs ? g.m * g.ldc : 0, g.epilogue, st);
 }
 
 }  // namespace averis

@@ -348,6 +348,18 @@ hipError_t launch_act_grad(const void* dy, bool bf16, int64_t rows, int64_t cols
 // and c by segment with a stack of b (kRowSegs), or a range of blocks for each
 // segment, c a stack (kBlockSegs; rows: the rows the segments divide).
 enum Fp8Mode { kF8All, kF8RowSegs, kF8BlockSegs };
+// What a product does to its sums before they are written: z = sum + bias
+// (n values a segment, or nullptr), kept in z (c's type, or nullptr); c = act(z)
+// + res (c's type, or nullptr).
+struct Fp8Epilogue {
+  const void* bias;
+  bool bias_bf16;
+  int act;
+  const void* res;
+  int64_t ldr;
+  void* z;
+  int64_t ldz;
+};
 struct Fp8Gemm {
   Fp8Operand a, b;
   int64_t m, n, k_blocks;
@@ -358,6 +370,7 @@ struct Fp8Gemm {
   void* c;
   bool c_bf16;
   int64_t ldc;
+  const Fp8Epilogue* epilogue;   // or nullptr
 };
 size_t fp8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg);
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st);
