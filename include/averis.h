@@ -509,7 +509,7 @@ typedef enum { AVERIS_SCORE_SOFTMAX = 0, AVERIS_SCORE_SIGMOID = 1 } averis_score
  *   (1 or 2) largest c_e (of its one open expert, c_e);
  *   of theirs, expert_ids[t][j] are the topk largest c_e in descending order,
  *   weights[t][j] = scale s_e, divided by the sum of the chosen s_e with renorm = 1.
- * The choice is by the exact values of c_e (and, without a bias and with
+ * The choice is by the values of c_e in fp64 (without a bias, and with
  * group_top = 1 or all groups, of l_e, which order alike), equal ones by the
  * lowest index first.  A logit of -inf, or c_e = -inf, is closed: never chosen, and a
  * slot for which none is left gets id -1 and weight 0; a group without an open

@@ -5,7 +5,7 @@
 //   a group's score: the sum of its one or two largest c_e; the best groups stay
 //   the topk largest c_e of theirs are chosen; w = scale s_e (/ the chosen ones' sum)
 //
-// The choice is by the exact c_e (equal ones: the lowest index first).  It is
+// The choice is by c_e in fp64 (equal ones: the lowest index first).  It is
 // made from fp32 scores, their lowest bits given to the expert's place, and
 // where two of those lie closer than their errors allow to tell, and are not of
 // the same logit and bias, the wavefront's tokens are chosen again in fp64.
