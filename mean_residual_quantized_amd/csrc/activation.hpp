@@ -9,32 +9,32 @@
 namespace averis {
 
 // silu(z) = z s(z) and gelu(z) = z s(u), u = 2 sqrt(2 / pi) (z + 0.044715 z^3), with s(u) = 1 / (1 +
-// e^-u): the tanh form of gelu, for (1 + tanh(v)) / 2 = s(2 v).  Both as z s(z (a + b z^2)).  e^-u and
-// the reciprocal are single instructions (an error of 1 ulp each).
-struct ActSigmoid {
-  float a, b;   // of u in units of log 2
-  float a1, b1;   // of du / dz
-  __device__ __forceinline__ explicit ActSigmoid(int act) {
-    const float k = 1.5957691216057308f, c = k * 0.044715f, log2e = 1.4426950408889634f;
-    a1 = act == kActGelu ? k : 1.0f;
-    b1 = act == kActGelu ? 3.0f * c : 0.0f;
-    a = act == kActGelu ? k * log2e : log2e;
-    b = act == kActGelu ? c * log2e : 0.0f;
-  }
-  // |z| past 100 changes nothing, and z^2 might overflow (a NaN z is not seen here: the products below
-  // with z keep it)
-  __device__ __forceinline__ float sigmoid(float z) const {
-    z = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f);
-    const float u = z * __builtin_fmaf(b, z * z, a);
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u));
-  }
-  __device__ __forceinline__ float value(float z) const { return z * sigmoid(z); }
-  // s + z s (1 - s) du/dz, past |z| = 100 its limit, 1 or 0
-  __device__ __forceinline__ float slope(float z) const {
-    z = z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z;
-    const float s = sigmoid(z);
-    return __builtin_fmaf(z * s * (1.0f - s), __builtin_fmaf(b1, z * z, a1), s);
-  }
-};
+// e^-u): the tanh form of gelu, for (1 + tanh(v)) / 2 = s(2 v).  e^-u (2 to the power of -u / log 2) and
+// the reciprocal are single instructions, an error of 1 ulp each.
+constexpr float kActLog2e = 1.4426950408889634f;
+constexpr float kGeluA = 1.5957691216057308f, kGeluB = kGeluA * 0.044715f;   // u = z (A + B z^2)
+
+// s(u) of u / log 2
+__device__ __forceinline__ float act_sigmoid(float u2) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u2));
+}
+__device__ __forceinline__ float act_silu(float z) { return z * act_sigmoid(kActLog2e * z); }
+__device__ __forceinline__ float act_gelu(float z) {
+  return z * act_sigmoid(z * __builtin_fmaf(kGeluB * kActLog2e, z * z, kGeluA * kActLog2e));
+}
+
+// d/dz of z s(u): s + z s (1 - s) du/dz.  Past |z| = 100 it is its limit, 1 or 0, and the products of its
+// terms might overflow: z is held there (a NaN stays one).
+__device__ __forceinline__ float act_held(float z) { return z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z; }
+__device__ __forceinline__ float act_silu_slope(float z) {
+  z = act_held(z);
+  const float s = act_sigmoid(kActLog2e * z);
+  return __builtin_fmaf(z * s, 1.0f - s, s);
+}
+__device__ __forceinline__ float act_gelu_slope(float z) {
+  z = act_held(z);
+  const float q = z * z, s = act_sigmoid(z * __builtin_fmaf(kGeluB * kActLog2e, q, kGeluA * kActLog2e));
+  return __builtin_fmaf(z * s * (1.0f - s), __builtin_fmaf(3.0f * kGeluB, q, kGeluA), s);
+}
 
 }  // namespace averis

@@ -148,10 +148,12 @@ struct ActSrc {
     if (act == kActRelu) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) f[i] = z[i] <= 0.0f ? 0.0f : f[i];   // (a NaN z lets f by)
-    } else if (act != kActNone) {
-      const ActSigmoid s(act);
+    } else if (act == kActSilu) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] *= s.slope(z[i]);
+      for (int i = 0; i < 8; ++i) f[i] *= act_silu_slope(z[i]);
+    } else if (act == kActGelu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= act_gelu_slope(z[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) at.sum[i] += f[i];

@@ -21,7 +21,7 @@
 #include <type_traits>
 
 #include "activation.hpp"
-#include "fp8_common.hpp"
+#include "fp8_eight.hpp"
 #include "launch.hpp"
 #include "segments.hpp"
 
@@ -83,8 +83,10 @@ struct F8Tile {
 };
 
 // ---------------------------------------------------------------------------
-// Epilogues: four neighbouring columns of a row
+// Epilogues
 // ---------------------------------------------------------------------------
+// kinds of them in the tiled kernel: each code of its own, for the instruction cache's sake
+constexpr int kEpiNone = 0, kEpiPlain = 1, kEpiResidual = 2;
 struct NoEpilogue {};
 template <bool EPI>
 using EpilogueArg = std::conditional_t<EPI, Fp8Epilogue, NoEpilogue>;
@@ -113,78 +115,79 @@ __device__ __forceinline__ Four<BF16> four_in(const void* p, int64_t at, int lef
   }
   return v;
 }
+__device__ __forceinline__ float vector_at(const void* p, bool bf16, int64_t i) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16)
+              : static_cast<const float*>(p)[i];
+}
+// z and the residual in whole pieces of 16 bytes below 2^31 bytes a tile
+__host__ __device__ __forceinline__ bool epilogue_whole(const Fp8Epilogue& e, int es) {
+  auto ok = [&](const void* p, int64_t ld) {
+    return !p || (ld * es % 16 == 0 && ld <= (1 << 21) && (reinterpret_cast<uintptr_t>(p) & 15) == 0);
+  };
+  return ok(e.z, e.ldz) && ok(e.res, e.ldr);
+}
 template <bool BF16>
 __device__ __forceinline__ f32x4_t four_f32(Four<BF16> v) {
   if constexpr (BF16)
     return f32x4_t{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xFFFF0000u),
                    __uint_as_float(v[1] << 16), __uint_as_float(v[1] & 0xFFFF0000u)};
   else
-    return f32x4_t{__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
-                   __uint_as_float(v[3])};
+    return __builtin_bit_cast(f32x4_t, v);
 }
+// 16 bytes to elements of a row of which `left` are there
 template <bool BF16>
-__device__ __forceinline__ void four_out(void* p, int64_t at, int left, f32x4_t f) {
-  if constexpr (BF16) {
-    uint16_t* q = static_cast<uint16_t*>(p) + at;
-    const u32x2_t v = {bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])};
-    if (left >= 4) {
-      *reinterpret_cast<f8_half_piece_t*>(q) = v;
-      return;
-    }
+__device__ __forceinline__ void piece_out(char* dst, u32x4_t v, int left) {
+  if (left >= (BF16 ? 8 : 4)) {
+    *reinterpret_cast<f8_piece_t*>(dst) = v;
+    return;
+  }
 #pragma unroll
-    for (int x = 0; x < 3; ++x)
-      if (x < left) q[x] = (uint16_t)(v[x / 2] >> (16 * (x & 1)));
-  } else {
-    float* q = static_cast<float*>(p) + at;
-    if (left >= 4) {
-      *reinterpret_cast<f8_piece_t*>(q) = u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]),
-                                                  __float_as_uint(f[2]), __float_as_uint(f[3])};
-      return;
-    }
-#pragma unroll
-    for (int x = 0; x < 3; ++x)
-      if (x < left) q[x] = f[x];
+  for (int x = 0; x < (BF16 ? 8 : 4); ++x) {
+    if (x >= left) continue;
+    if constexpr (BF16)
+      reinterpret_cast<uint16_t*>(dst)[x] = (uint16_t)(v[x / 2] >> (16 * (x & 1)));
+    else
+      reinterpret_cast<uint32_t*>(dst)[x] = v[x];
   }
 }
 
 __device__ __forceinline__ float activated(float z, int act) {
   if (act == kActNone) return z;
   if (act == kActRelu) return z < 0.0f ? 0.0f : z;
-  return ActSigmoid(act).value(z);
+  return act == kActSilu ? act_silu(z) : act_gelu(z);
+}
+__device__ __forceinline__ void activate(float (&v)[8], int act) {
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f(v[i]);
+  };
+  if (act == kActGelu) each([](float z) { return act_gelu(z); });
+  else if (act == kActSilu) each([](float z) { return act_silu(z); });
+  else if (act == kActRelu) each([](float z) { return z < 0.0f ? 0.0f : z; });
 }
 template <int N>
-__device__ __forceinline__ void activate(f32x4_t (&v)[N], int act) {
-  if (act == kActNone) return;
-  if (act == kActRelu) {
+__device__ __forceinline__ void activate(f32x4_t (&v)[N][4], int act) {
+  auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) v[i][x] = v[i][x] < 0.0f ? 0.0f : v[i][x];   // (a NaN stays)
-    return;
-  }
-  const ActSigmoid s(act);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) v[i][x] = s.value(v[i][x]);
+    for (int i = 0; i < 16 * N; ++i) v[i / 16][i / 4 % 4][i % 4] = f(v[i / 16][i / 4 % 4][i % 4]);
+  };
+  if (act == kActGelu) each([](float z) { return act_gelu(z); });
+  else if (act == kActSilu) each([](float z) { return act_silu(z); });
+  else if (act == kActRelu) each([](float z) { return z < 0.0f ? 0.0f : z; });   // (a NaN stays)
 }
 
 // the epilogue of one value: row, column of c, column j of the bias
 template <bool OUT_BF16>
 __device__ __forceinline__ void epilogue_one(const Fp8Epilogue& e, void* c, int64_t ldc, int64_t row,
                                              int64_t col, int64_t j, float s) {
-  auto in = [](const void* p, bool bf16, int64_t at) {
-    return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at] << 16)
-                : static_cast<const float*>(p)[at];
-  };
   auto out = [](void* p, int64_t at, float v) {
     if constexpr (OUT_BF16) static_cast<uint16_t*>(p)[at] = (uint16_t)bf16x2_rne(v, 0.0f);
     else static_cast<float*>(p)[at] = v;
   };
-  if (e.bias) s += in(e.bias, e.bias_bf16, j);
+  if (e.bias) s += vector_at(e.bias, e.bias_bf16, j);
   if (e.z) out(e.z, row * e.ldz + col, s);
   s = activated(s, e.act);
-  if (e.res) s += in(e.res, OUT_BF16, row * e.ldr + col);
+  if (e.res) s += vector_at(e.res, OUT_BF16, row * e.ldr + col);
   out(c, row * ldc + col, s);
 }
 
@@ -221,11 +224,12 @@ __device__ __forceinline__ void epilogue_one(const Fp8Epilogue& e, void* c, int6
 // slower on large products (half lines a load, a barrier more a block) and no
 // faster where the operands come from memory.
 // ---------------------------------------------------------------------------
-template <int F, bool OUT_BF16, int MODE, bool EPI>
+template <int F, bool OUT_BF16, int MODE, int EPI>
 __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     Fp8Operand A, Fp8Operand B, int m, int n, int k_blocks, const int64_t* offs, int nseg,
     int64_t seg_rows, int splits, int tx, int ty, void* c, int64_t ldc, int64_t c_split,
-    EpilogueArg<EPI> epi) {
+    EpilogueArg<EPI != kEpiNone> epi) {
+  constexpr bool RES = EPI == kEpiResidual;
   constexpr bool MANY = MODE != kF8BlockSegs;   // several tiles a workgroup
   constexpr int SLOTS = F == 4 ? kF8Cus : 2 * kF8Cus;   // workgroups the card holds
   constexpr int BM = 64 * F, BN = 64 * F, ROWS = BM + BN;
@@ -235,9 +239,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
   static_assert(SPW * 256 == ROWS, "every wavefront's loads are whole");
   constexpr int NF = 2 * F;
   constexpr int ES = OUT_BF16 ? 2 : 4;
-  // an epilogue takes the sums in fp32, whatever the output's type
-  constexpr bool STAGE_BF16 = OUT_BF16 && !EPI;
-  constexpr int GROUP = STAGE_BF16 ? 64 : 32;   // columns of an output pass: 128 bytes
+  constexpr int GROUP = 128 / ES;      // columns of an output pass: 128 bytes
   constexpr int PASSES = (32 * F + GROUP - 1) / GROUP;   // of a 32-row fragment
   extern __shared__ __attribute__((aligned(16))) unsigned char smem_f8[];
   unsigned char* ring = smem_f8;
@@ -473,7 +475,11 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
                 "stage 1's last load is the last pass's");
   bool behind = false;   // the first loads went out with a whole tile's output
   auto wait_loads = [&](auto firstc) __attribute__((always_inline)) {
-    if (behind) f8_wait_vm<(decltype(firstc)::value != 0 ? AFTER0 : 4)>();
+    // (the small tile's epilogue has four stores a pass at least behind them and four
+    // behind the HELD of stage 1, the large one's stage 1 itself behind stage 0)
+    if (behind)
+      f8_wait_vm<(decltype(firstc)::value != 0 ? (!EPI ? AFTER0 : F == 4 ? CPW : 4 * OUT_PASSES)
+                  : EPI && F == 4              ? 0 : 4)>();
     else f8_wait_vm<0>();
   };
   // stage s in slot s & 1; on entry its first fragments and scale words are
@@ -557,7 +563,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     u32x4_t out[4];   // a bf16 pass's values: pieces of two fragments
     auto form = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
-      if constexpr (STAGE_BF16) {
+      if constexpr (OUT_BF16) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           // fragment u / 2, column groups 8 q and 8 q + 8, q = 2 (u mod 2)
@@ -577,7 +583,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint32_t at = wr ^ (32 * u);
-        if constexpr (STAGE_BF16) {
+        if constexpr (OUT_BF16) {
           const u32x4_t v = out[u];
           asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
         } else {
@@ -587,69 +593,237 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
         }
       }
     };
-    const int row0 = wm * 32 * F + (ln >> 3), col0 = wn * 32 * F + (ln & 7) * (STAGE_BF16 ? 8 : 4);
+    const int row0 = wm * 32 * F + (ln >> 3), col0 = wn * 32 * F + (ln & 7) * (16 / ES);
     auto clear = [&](auto pc) __attribute__((always_inline)) {
       constexpr int i = decltype(pc)::value / PASSES, p = decltype(pc)::value % PASSES;
 #pragma unroll
       for (int f = 0; f < FPP; ++f) zero(i, p * FPP + f);
     };
-    if constexpr (EPI) {
-      // A lane has four columns of four rows a pass.  The next pass's residual
-      // is on its way while this one's values are formed.
-      if (HELD == 0 && loads) first_loads(nxt.nk);
-      const int64_t at0 = (int64_t)cur.m0 + row0;
-      auto left = [&](int p) __attribute__((always_inline)) { return cur.cols - col0 - p * GROUP; };
-      f32x4_t bias[PASSES];
+    bool behind_next = false;
+    const int64_t shift = (MODE == kF8RowSegs ? (int64_t)cur.seg * n : 0) + cur.n0;   // of the bias
+    if constexpr (EPI != kEpiNone && F == 4) {
+      // The large tile's epilogue, of whole pieces only: 32 rows of the wavefront's at a
+      // time to LDS in fp32 (in the blocks of the second slot that its own loads fill;
+      // piece p of row r at p ^ (p / 8 mod 2) ^ (r mod 8): neither the writes, of one piece
+      // of neighbouring rows, nor the reads, of a row's even or odd pieces, meet a bank
+      // twice), and from there in steps of four rows, a lane eight columns, four steps'
+      // residual read ahead.  The steps are a loop: with every pass unrolled, as the small
+      // tile has them, the code outgrows the instruction cache and the accumulators leave
+      // their registers (16384 x 1024 x 4096, gelu and z kept, 158 us; this 111, the small
+      // tile 123, the product alone 76).
+      using T = std::conditional_t<OUT_BF16, uint16_t, float>;
+      if (loads) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        bias[p] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        if (!epi.bias) continue;
-        const int64_t j = (MODE == kF8RowSegs ? (int64_t)cur.seg * n : 0) + cur.n0 + col0 + p * GROUP;
-        bias[p] = epi.bias_bf16 ? four_f32<true>(four_in<true>(epi.bias, j, left(p)))
-                                : four_f32<false>(four_in<false>(epi.bias, j, left(p)));
+        for (int k = 0; k < FIRST0; ++k) first_load(k, nxt.nk);
       }
-      Four<OUT_BF16> res[2][4];
+      const uint32_t to = (uint32_t)(uintptr_t)(lds_void*)(smem_f8 + SLOT + wave * 1024 + (ln & 31) / 2 * 4096 +
+                                                           (ln & 1) * 512) + 16 * ((ln & 7) ^ (ln >> 5));
+      const int k = ln & 15, rl = ln >> 4, col = wn * 128 + 8 * k;
+      // row 4 it + rl, pieces 2 k and 2 k + 1
+      const unsigned char* from = smem_f8 + SLOT + wave * 1024 + rl / 2 * 4096 + rl % 2 * 512 + 128 * (k >> 2);
+      const int sw = (k >> 2 & 1) ^ rl;   // (r mod 8 = rl + 4 (it mod 2))
+      const bool in = col < cur.cols;
+      float bias[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) bias[x] = 0.0f;
+      if (epi.bias && in) load_vector(epi.bias, epi.bias_bf16, shift + col, shift + col + 8, bias);
+      const int64_t row0e = (int64_t)cur.m0 + wm * 128 + rl;
+      const int rows_left = cur.rows - wm * 128 - rl;   // row r of the lane's is there: r < it
+      const T* res = static_cast<const T*>(epi.res) + row0e * epi.ldr + cur.n0 + col;
+      T* zp = static_cast<T*>(epi.z) + row0e * epi.ldz + cur.n0 + col;
+      T* cp = static_cast<T*>(c) + row0e * ldc + cur.n0 + col;
+      Eight<T> ahead[4];   // the next four steps' residual
+      auto load_res = [&](int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (in && r + 4 * u < rows_left) ahead[u].load(res + (int64_t)(r + 4 * u) * epi.ldr, 0, 8);
+      };
+      if constexpr (RES) load_res(0);
+      each_step<F>([&](auto ic) __attribute__((always_inline)) {
+        constexpr int i = decltype(ic)::value;
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t& y = acc[i][j];
+            const f32x4_t v = {y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]};
+            asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(to ^ (32 * q) ^ (16 * (j & 1))), "a"(v), "i"(128 * j)
+                         : "memory");
+          }
+#pragma unroll
+        for (int j = 0; j < F; ++j) zero(i, j);
+        auto step = [&](int it, const Eight<T>& add) __attribute__((always_inline)) {
+          const unsigned char* p = from + it * 8192;
+          const int x = sw ^ (4 * (it & 1));
+          const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(p + 16 * ((2 * k & 6) ^ x));
+          const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(p + 16 * ((2 * k & 6 | 1) ^ x));
+          const int64_t r = 32 * i + 4 * it;
+          if (!in || r >= rows_left) return;
+          float f[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            f[y] = lo[y] + bias[y];
+            f[4 + y] = hi[y] + bias[4 + y];
+          }
+          Eight<T> o;
+          if (epi.z) {
+            o.set(f);
+            o.store(zp + r * epi.ldz, 0, 8);
+          }
+          activate(f, epi.act);
+          if constexpr (RES) {
+            float g[8];
+            add.f32(g);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) f[y] += g[y];
+          }
+          o.set(f);
+          o.store(cp + r * ldc, 0, 8);
+        };
+        if constexpr (RES) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            Eight<T> add[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add[u] = ahead[u];
+            load_res(32 * i + 16 * h + 16);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) step(4 * h + u, add[u]);
+          }
+        } else {
+#pragma unroll 1
+          for (int it = 0; it < 8; ++it) step(it, ahead[0]);
+        }
+      });
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the last values are out of their place
+      if (loads) {
+#pragma unroll
+        for (int k = FIRST0; k < FIRST; ++k) first_load(k, nxt.nk);
+      }
+      behind_next = loads;
+    } else if constexpr (EPI != kEpiNone) {
+      // The small tile's: the same passes as below, each formed from the accumulators' own
+      // layout: bias, then (where it is kept) z through LDS and out, then the activation
+      // and the residual, whose loads are a pass ahead, and c through LDS.  A pass's values
+      // are formed while those of the pass before come back.  The next tile's first loads
+      // go out ahead of all: no wait for them is one for the stores.
+      if (loads) {
+#pragma unroll
+        for (int k = 0; k < FIRST - HELD; ++k) first_load(k, nxt.nk);
+      }
+      const bool whole = pieces && epilogue_whole(epi, ES);
+      // fragment j's columns 8 u + 4 h .. + 3, h = lane / 32, of row lane mod 32
+      const int colf = wn * 32 * F + 4 * (ln >> 5), rowf = wm * 32 * F + (ln & 31);
+      f32x4_t bias[F][4];
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          bias[j][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          const int col = colf + 32 * j + 8 * u;
+          if (epi.bias)
+            bias[j][u] = epi.bias_bf16 ? four_f32<true>(four_in<true>(epi.bias, shift + col, cur.cols - col))
+                                       : four_f32<false>(four_in<false>(epi.bias, shift + col, cur.cols - col));
+        }
+      Four<OUT_BF16> ahead[2][FPP][4];
       auto load_res = [&](auto pc) __attribute__((always_inline)) {
         constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
-        if (!epi.res) return;
+        if (rowf + 32 * i >= cur.rows) return;
+        const int64_t at = (int64_t)(cur.m0 + rowf + 32 * i) * epi.ldr + cur.n0;
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-          if (row0 + 32 * i + 8 * it < cur.rows)
-            res[P & 1][it] = four_in<OUT_BF16>(
-                epi.res, (at0 + 32 * i + 8 * it) * epi.ldr + cur.n0 + col0 + p * GROUP, left(p));
+        for (int f = 0; f < FPP; ++f)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int col = colf + 32 * (p * FPP + f) + 8 * u;
+            ahead[P & 1][f][u] = four_in<OUT_BF16>(epi.res, at + col, cur.cols - col);
+          }
       };
-      load_res(F8Step<0>{});
-      each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
-        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
-        to_lds(pc);
-        clear(pc);
-        f32x4_t v[4];
+      // a pass's values, as pieces 2 u + h of its rows' 128 bytes
+      auto pack = [&](const f32x4_t (&y)[FPP][4]) __attribute__((always_inline)) {
 #pragma unroll
-        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const f32x4_t*>(src + it * STG_STEP);
-        if constexpr (P + 1 < OUT_PASSES) load_res(F8Step<P + 1>{});
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (OUT_BF16) {
+            const f32x4_t &l = y[u / 2][2 * (u & 1)], &h = y[u / 2][2 * (u & 1) + 1];
+            const auto a = __builtin_amdgcn_permlane32_swap(bf16x2_rne(l[0], l[1]), bf16x2_rne(h[0], h[1]), false, false);
+            const auto b = __builtin_amdgcn_permlane32_swap(bf16x2_rne(l[2], l[3]), bf16x2_rne(h[2], h[3]), false, false);
+            out[u] = u32x4_t{a[0], b[0], a[1], b[1]};
+          } else {
+            out[u] = __builtin_bit_cast(u32x4_t, y[0][u]);
+          }
+        }
+      };
+      u32x4_t vz[4], vc[4];
+      auto through_lds = [&](u32x4_t (&v)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const u32x4_t x = out[u];
+          asm volatile("ds_write_b128 %0, %1" ::"v"(wr ^ (32 * u)), "v"(x) : "memory");
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) v[it] = *reinterpret_cast<const u32x4_t*>(src + it * STG_STEP);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) v[it] += bias[p];
-        const int64_t col = cur.n0 + col0 + p * GROUP;
-        if (epi.z) {
+      };
+      char* zb = static_cast<char*>(epi.z) + (cur.m0 * epi.ldz + cur.n0) * ES;
+      auto store = [&](char* base, int64_t ld, auto pc, const u32x4_t (&v)[4]) __attribute__((always_inline)) {
+        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
+        if (whole) {
+          const uint32_t ldb = (uint32_t)(ld * ES);
+          const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+              const_cast<uint8_t*>(scalar_base(reinterpret_cast<const uint8_t*>(base))), 0,
+              (int)((uint32_t)(cur.rows - 1) * ldb + (uint32_t)(cur.cols * ES)), 0x00027000);
+          const uint32_t at = ((uint32_t)(row0 + 32 * i) * ldb + (uint32_t)(col0 * ES) + 128 * p) |
+                              (col0 + p * GROUP < cur.cols ? 0u : 0x80000000u);
 #pragma unroll
           for (int it = 0; it < 4; ++it)
-            if (row0 + 32 * i + 8 * it < cur.rows)
-              four_out<OUT_BF16>(epi.z, (at0 + 32 * i + 8 * it) * epi.ldz + col, left(p), v[it]);
-        }
-        activate(v, epi.act);
+            __builtin_amdgcn_raw_buffer_store_b128(v[it], rsrc, (int)(at + (uint32_t)(8 * it) * ldb), 0, OUT_BF16 ? 2 : 0);
+        } else {
+          const int left = cur.cols - col0 - p * GROUP;
+          char* dst = base + ((int64_t)(row0 + 32 * i) * ld + col0 + p * GROUP) * ES;
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          if (row0 + 32 * i + 8 * it >= cur.rows) continue;
-          if (epi.res) v[it] += four_f32<OUT_BF16>(res[P & 1][it]);
-          four_out<OUT_BF16>(c, (at0 + 32 * i + 8 * it) * ldc + col, left(p), v[it]);
+          for (int it = 0; it < 4; ++it, dst += 8 * ld * ES)
+            if (row0 + 32 * i + 8 * it < cur.rows) piece_out<OUT_BF16>(dst, v[it], left);
         }
+      };
+      if constexpr (RES) load_res(F8Step<0>{});
+      each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
+        constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
+        f32x4_t y[FPP][4];
+#pragma unroll
+        for (int f = 0; f < FPP; ++f)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const f32x16_t& a = acc[i][p * FPP + f];
+            y[f][u] = f32x4_t{a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]} + bias[p * FPP + f][u];
+          }
+        clear(pc);
+        if (epi.z) {
+          pack(y);
+          through_lds(vz);
+        }
+        if constexpr (RES && P + 1 < OUT_PASSES) load_res(F8Step<P + 1>{});
+        activate(y, epi.act);
+        if constexpr (RES) {
+#pragma unroll
+          for (int f = 0; f < FPP; ++f)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) y[f][u] += four_f32<OUT_BF16>(ahead[P & 1][f][u]);
+        }
+        pack(y);
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (P > 0) store(cb, ldc, F8Step<P - 1>{}, vc);
+        if (epi.z) store(zb, epi.ldz, pc, vz);
+        through_lds(vc);
       });
       if constexpr (HELD > 0) {
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-        if (loads) first_loads(nxt.nk);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the last values are out of their place
+        if (loads) {
+#pragma unroll
+          for (int k = FIRST - HELD; k < FIRST; ++k) first_load(k, nxt.nk);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      store(cb, ldc, F8Step<OUT_PASSES - 1>{}, vc);
+      behind_next = loads && whole;
     } else if (pieces) {
       const uint32_t ldb = (uint32_t)(ldc * ES);
       // below 2^31: a lane past the columns goes to 2^31 and on
@@ -724,7 +898,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     }
     __builtin_amdgcn_sched_barrier(0);
     if (!more) break;
-    behind = !EPI && pieces;
+    behind = EPI ? behind_next : pieces;
     cur = nxt;
   }
 }
@@ -843,17 +1017,6 @@ __global__ __launch_bounds__(256) void k_f8_reduce(const float* __restrict__ par
   }
   const int64_t row = e / n, col = e - row * n;
   if constexpr (EPI) {
-    if (col + 4 <= n) {   // four of one row
-      f32x4_t v[1] = {f32x4_t{s[0], s[1], s[2], s[3]}};
-      if (epi.bias)
-        v[0] += epi.bias_bf16 ? four_f32<true>(four_in<true>(epi.bias, col, 4))
-                              : four_f32<false>(four_in<false>(epi.bias, col, 4));
-      if (epi.z) four_out<OUT_BF16>(epi.z, row * epi.ldz + col, 4, v[0]);
-      activate(v, epi.act);
-      if (epi.res) v[0] += four_f32<OUT_BF16>(four_in<OUT_BF16>(epi.res, row * epi.ldr + col, 4));
-      four_out<OUT_BF16>(c, row * ldc + col, 4, v[0]);
-      return;
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (e + i >= mn) break;
@@ -953,9 +1116,9 @@ Fp8Plan fp8_plan(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, int nseg)
   return best;
 }
 
-template <int F, bool OB, int MODE, bool EPI>
+template <int F, bool OB, int MODE, int EPI>
 hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
-                     const EpilogueArg<EPI>& epi, hipStream_t st) {
+                     const EpilogueArg<EPI != kEpiNone>& epi, hipStream_t st) {
   constexpr size_t lds = f8_lds_bytes(F);
   static_assert(lds <= 160 * 1024 / (F == 4 ? 1 : 2), "fits one CU's LDS");
   const hipError_t e = lds_attr_once<&k_gemm_f8<F, OB, MODE, EPI>>((int)lds);
@@ -975,15 +1138,17 @@ hipError_t gemm_f8_t(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t
 template <int F, bool OB>
 hipError_t gemm_f8_mode(const Fp8Gemm& g, int splits, void* c, int64_t ldc, int64_t c_split,
                         const Fp8Epilogue* epi, hipStream_t st) {
-  if (epi)   // (of a product by block segments: none)
-    return g.mode == kF8RowSegs
-               ? gemm_f8_t<F, OB, kF8RowSegs, true>(g, splits, c, ldc, c_split, *epi, st)
-               : gemm_f8_t<F, OB, kF8All, true>(g, splits, c, ldc, c_split, *epi, st);
+  if (epi && g.mode == kF8RowSegs)   // (of a product by block segments: none)
+    return epi->res ? gemm_f8_t<F, OB, kF8RowSegs, kEpiResidual>(g, splits, c, ldc, c_split, *epi, st)
+                    : gemm_f8_t<F, OB, kF8RowSegs, kEpiPlain>(g, splits, c, ldc, c_split, *epi, st);
+  if (epi)
+    return epi->res ? gemm_f8_t<F, OB, kF8All, kEpiResidual>(g, splits, c, ldc, c_split, *epi, st)
+                    : gemm_f8_t<F, OB, kF8All, kEpiPlain>(g, splits, c, ldc, c_split, *epi, st);
   const NoEpilogue no;
   switch (g.mode) {
-    case kF8RowSegs: return gemm_f8_t<F, OB, kF8RowSegs, false>(g, splits, c, ldc, c_split, no, st);
-    case kF8BlockSegs: return gemm_f8_t<F, OB, kF8BlockSegs, false>(g, splits, c, ldc, c_split, no, st);
-    default: return gemm_f8_t<F, OB, kF8All, false>(g, splits, c, ldc, c_split, no, st);
+    case kF8RowSegs: return gemm_f8_t<F, OB, kF8RowSegs, kEpiNone>(g, splits, c, ldc, c_split, no, st);
+    case kF8BlockSegs: return gemm_f8_t<F, OB, kF8BlockSegs, kEpiNone>(g, splits, c, ldc, c_split, no, st);
+    default: return gemm_f8_t<F, OB, kF8All, kEpiNone>(g, splits, c, ldc, c_split, no, st);
   }
 }
 
@@ -1033,10 +1198,16 @@ size_t fp8_gemm_ws_bytes(int64_t m, int64_t n, int64_t k_blocks, Fp8Mode mode, i
 
 hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
-  const Fp8Plan p = fp8_plan(g.m, g.n, g.k_blocks, g.mode, g.nseg);
+  Fp8Plan p = fp8_plan(g.m, g.n, g.k_blocks, g.mode, g.nseg);
   if (p.skinny == 1) return skinny<1>(g, st);
   if (p.skinny == 2) return skinny<2>(g, st);
   if (p.skinny == 4) return skinny<4>(g, st);
+  if (g.epilogue && p.f == 4 && p.splits == 1) {
+    const int es = g.c_bf16 ? 2 : 4;
+    if (!(g.n * es % 16 == 0 && g.ldc * es % 16 == 0 && g.ldc <= (1 << 21) &&
+          (reinterpret_cast<uintptr_t>(g.c) & 15) == 0 && epilogue_whole(*g.epilogue, es)))
+      p.f = 2;
+  }
   if (p.splits > 1) {
     const hipError_t e = gemm_f8(g, p, false, ws, g.n, g.m * g.n, nullptr, st);
     if (e != hipSuccess) return e;
