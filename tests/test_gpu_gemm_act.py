@@ -84,7 +84,11 @@ def test_epilogue(m, n, k):
                 assert torch.equal(av.averis_fp8_gemm_act(a, b, bias=bv, act=use, residual=rs, out=rs), c)
 
 
-@pytest.mark.parametrize("m,n,k", LARGE)
+# columns in whole 16-byte pieces, which the large tile's epilogue is for
+WHOLE = [(3001, 3008, 3790), (12001, 2216, 800), (9000, 5008, 260), (16384, 1032, 2048), (1001, 3008, 16300)]
+
+
+@pytest.mark.parametrize("m,n,k", LARGE + WHOLE)
 def test_large_products_are_exact(m, n, k):
     """Both tile sizes, several tiles a workgroup and split sums, of small integers."""
     rng = np.random.default_rng([m, n, k, 2])
@@ -102,9 +106,23 @@ def test_large_products_are_exact(m, n, k):
         assert torch.equal(av.averis_fp8_gemm_act(a, b, bias=bias, act="relu", residual=res, out=out), c)
         out.fill_(9.0)
         assert (buf == 9.0).all()
+        # rows that start at whole pieces and end before the next one does; in place; without each part
+        wide, rw = (torch.full((m + 1, n + 16), v, dtype=dt, device="cuda") for v in (9.0, 4.0))
+        rw[:m, 8:8 + n] = res
+        part = wide[:m, 8:8 + n]
+        assert torch.equal(av.averis_fp8_gemm_act(a, b, bias=bias, act="relu", residual=rw[:m, 8:8 + n], out=part), c)
+        part.fill_(9.0)
+        assert (wide == 9.0).all()
+        own = rw[:m, 8:8 + n]
+        assert torch.equal(av.averis_fp8_gemm_act(a, b, bias=bias, act="relu", residual=own, out=own), c)
+        assert (rw[:m, :8] == 4.0).all() and (rw[:m, 8 + n:] == 4.0).all() and (rw[m:] == 4.0).all()
+        assert torch.equal(av.averis_fp8_gemm_act(a, b, bias=bias, out_dtype=dt), z.to(dt))
+        assert torch.equal(av.averis_fp8_gemm_act(a, b, out_dtype=dt), av.averis_fp8_gemm(a, b, dt))
+        smooth(av.averis_fp8_gemm_act(a, b, bias=bias, act="gelu", residual=res, out_dtype=dt), z.float(), "gelu", res)
+        smooth(av.averis_fp8_gemm_act(a, b, bias=bias, act="silu", out_dtype=dt), z.float(), "silu", None)
 
 
-@pytest.mark.parametrize("k,n", [(200, 96), (640, 300), (2100, 1031)])
+@pytest.mark.parametrize("k,n", [(200, 96), (640, 300), (2100, 1031), (2100, 2104)])
 @pytest.mark.parametrize("offs", [[0, 5], [0, 0, 3, 3, 70, 90], [0, 256, 256, 900, 1500, 1500], [0, 300, 310, 1400],
                                   [0, 1, 1, 2500, 2756, 8000, 9000]])
 def test_segments_are_exact(offs, k, n):
