@@ -97,8 +97,7 @@ averis_status_t averis_moe_route_groups(const void* logits, averis_dtype_t dtype
       !aligned(weights, 4))
     return AVERIS_E_ALIGN;
   const RouteGroups a{tokens, ld, experts, topk, bias, score, groups, topk_groups, group_top,
-                      renorm != 0, scale, expert_ids, weights, size,
-                      (((uint64_t)1 << 32) + (uint64_t)size - 1) / (uint64_t)size, 0};
+                      renorm != 0, scale, expert_ids, weights, size, 0, 0};
   return hip_status(launch_route_groups(logits, dtype == AVERIS_BF16, a, stream));
 }
 

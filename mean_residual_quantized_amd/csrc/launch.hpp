@@ -213,9 +213,10 @@ struct RouteGroups {
   float scale;
   int32_t* ids;
   float* weights;
-  int gsize;            // experts / groups
-  uint64_t gsize_inv;   // ceil(2^32 / gsize)
-  int group_lanes;      // set by the launch
+  int gsize;   // experts / groups
+  // set by the launch: lanes a group, ceil(2^32 / them)
+  int group_lanes;
+  uint64_t lanes_inv;
 };
 struct RouteGroupsGrad {
   int64_t tokens, ld, ldd;

@@ -12,6 +12,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "launch.hpp"
 #include "moe_lanes.hpp"
@@ -21,12 +23,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The lane's V logits: experts g V .. g V + V - 1 of the token's G lanes.  Lanes
-// and places then order as the experts do, and a group of experts is a run of
-// lanes wherever its size is a multiple of V.
+// Logits first .. first + V - 1 of a row, of which `many` are there (the others closed)
 template <typename T, int V>
-__device__ __forceinline__ void load_run(const T* row, int first, int experts, float* l) {
-  if (first + V <= experts) {
+__device__ __forceinline__ void load_run(const T* row, int first, int many, float* l) {
+  if (many >= V) {
 #pragma unroll
     for (int v = 0; v < V; v += Elem<T>::kPer)
       Elem<T>::unpack(*reinterpret_cast<const piece_t*>(row + first + v), l + v);
@@ -34,15 +34,26 @@ __device__ __forceinline__ void load_run(const T* row, int first, int experts, f
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    l[v] = first + v < experts ? Elem<T>::f32(row[first + v]) : kMasked;
+    l[v] = v < many ? Elem<T>::f32(row[first + v]) : kMasked;
 }
 
-// Sum over G neighbouring lanes in fp64, and the largest
-template <int G>
-__device__ __forceinline__ double group_sum64(double v) {
-#pragma unroll
-  for (int d = 1; d < G; d <<= 1) v += __shfl_xor(v, d, 64);
-  return v;
+// the other lane's value, 64 bits of it
+template <int D, typename K>
+__device__ __forceinline__ K partner_of(K v) {
+  if constexpr (sizeof(K) == 4) {
+    return __builtin_bit_cast(K, partner<D>(__builtin_bit_cast(uint32_t, v)));
+  } else {
+    const u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+    return __builtin_bit_cast(K, u32x2_t{partner<D>(w[0]), partner<D>(w[1])});
+  }
+}
+// f(D) for each step of a butterfly over G lanes
+template <int G, int D = 1, typename F>
+__device__ __forceinline__ void butterfly(F f) {
+  if constexpr (D < G) {
+    f(std::integral_constant<int, D>{});
+    butterfly<G, 2 * D>(f);
+  }
 }
 
 // The two largest of two ordered pairs
@@ -72,15 +83,19 @@ __device__ __forceinline__ void sort_down(uint32_t* s) {
           }
 }
 
-// what a lane of a token's G may keep in LDS, for it and for its neighbours
+// What a token's lanes keep in LDS for one another: the two (three) largest of
+// each lane, then each group's score (G lanes hold at most G groups), and the chosen.
 template <int G, int V>
-struct RouteShare {
+struct alignas(16) RouteShare {
   static constexpr int kTokens = 256 / G;
-  static constexpr int kGroups = G * V < kMaxGroups ? G * V : kMaxGroups;
+  static constexpr int kGroups = G < 4 ? 4 : G;
   static constexpr int kSlots = G * V < kMaxTopk ? G * V : kMaxTopk;
-  double group[kTokens][kGroups];    // scores (fp32 ones in their place)
-  uint32_t key[kTokens][kSlots];     // chosen
-  int32_t id[kTokens][kSlots];
+  double pair[kTokens][G][2];          // (the fp32 keys in their place)
+  double score[kTokens][kGroups];
+  float size[kTokens][kGroups];        // |first| + |second|
+  uint32_t edge[kTokens][4];           // score and size of the last group that stays, of the first that does not
+  uint32_t key[kTokens][kSlots + 1];   // (the next one behind them)
+  int32_t id[kTokens][kSlots + 1];
 };
 
 // one wavefront's LDS accesses are in order
@@ -90,132 +105,118 @@ __device__ __forceinline__ void lds_order() {
   asm volatile("" ::: "memory");
 }
 
-// Scores of the lane's logits in fp64: 0 where an expert is closed (softmax;
-// sigmoid gives that itself).
-template <int G, int V>
-__device__ __forceinline__ void scores64(const float* l, int score, double* s) {
-  if (score == kScoreSigmoid) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = 1.0 / (1.0 + exp(-(double)l[v]));
-    return;
-  }
-  float top = l[0];
-#pragma unroll
-  for (int v = 1; v < V; ++v) top = __builtin_fmaxf(top, l[v]);
-  top = group_fmax<G>(top);
-  if (top == kMasked) top = 0.0f;
-  double total = 0.0;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    s[v] = exp((double)l[v] - (double)top);
-    total += s[v];
-  }
-  total = group_sum64<G>(total);
-#pragma unroll
-  for (int v = 0; v < V; ++v) s[v] = total == 0.0 ? 0.0 : s[v] / total;
+// the lane's experts: a run of `many` from `first` on, within its group
+struct RouteLane {
+  int group, first, many;
+};
+template <int V>
+__device__ __forceinline__ RouteLane route_lane(const RouteGroups& a, int g) {
+  RouteLane r;
+  r.group = (int)(((uint64_t)(uint32_t)g * a.lanes_inv) >> 32);   // g / group_lanes
+  const int place = (g - r.group * a.group_lanes) * V, left = a.gsize - place;
+  r.first = r.group * a.gsize + place;
+  r.many = r.group >= a.groups ? 0 : left < V ? left : V;
+  return r;
 }
 
-// orders as c does: NaN above +inf, -0 as +0; closed (-inf) below all
-__device__ __forceinline__ double rank64(double c) { return c != c ? __builtin_inf() : c; }
-
-// The choice in fp64, for every token of the wavefront.  Its ids go to sh.id.
-// NaN scores count as +inf here and by NaN's own mark above it.
-template <int G, int V>
-__device__ __forceinline__ void choose64(const float* l, const RouteGroups& a, int g, int tok,
-                                      RouteShare<G, V>& sh) {
-  double c[V];
+// The choice in fp64, for every token of the wavefront; its ids go to sh.id.
+template <typename T, int G, int V>
+__device__ __forceinline__ void choose64(const T* row, const RouteGroups& a, int g, int tok,
+                                         RouteShare<G, V>& sh) {
+  const RouteLane at0 = route_lane<V>(a, g);
   const bool limited = a.topk_groups < a.groups;
   const bool by_logit = !a.bias && !(limited && a.group_top == 2);
-  bool nan[V];
-  if (by_logit) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = l[v];
-  } else {
-    scores64<G, V>(l, a.score, c);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = g * V + v;
-      if (a.bias) c[v] += e < a.experts ? (double)a.bias[e] : 0.0;
-      if (l[v] == kMasked) c[v] = (double)kMasked;
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    nan[v] = c[v] != c[v];
-    c[v] = rank64(c[v]);
-  }
   const double closed = -__builtin_inf();
-  if (limited) {
-    for (int j = 0; j < a.groups; ++j) {
-      double t1 = closed, t2 = closed;
-      bool n = false;
+  double c[V];
+  uint32_t nan = 0;   // bit v: c[v] is NaN (and +inf in its place)
+  {
+    float l[V];
+    load_run<T, V>(row, at0.first, at0.many, l);
+    double top = 0.0, inv = 1.0;
+    if (!by_logit && a.score == kScoreSoftmax) {
+      float m = l[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) m = __builtin_fmaxf(m, l[v]);
+      m = group_fmax<G>(m);
+      top = m == kMasked ? 0.0 : (double)m;
+      double total = 0.0;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int e = g * V + v;
-        const bool in = e >= j * a.gsize && e < (j + 1) * a.gsize;
-        merge2(t1, t2, in ? c[v] : closed, closed);
-        n |= in && nan[v];
+        c[v] = exp((double)l[v] - top);
+        total += c[v];
       }
-#pragma unroll
-      for (int d = 1; d < G; d <<= 1) merge2(t1, t2, __shfl_xor(t1, d, 64), __shfl_xor(t2, d, 64));
-      const uint64_t any = __ballot(n) >> ((threadIdx.x & 63) & ~(G - 1));
-      double s = t1;
-      if (t1 != closed && a.group_top == 2 && t2 != closed) s = t1 + t2;
-      // a group with a NaN is above every other
-      if (G == 64 ? any != 0 : (any & ((1ull << (G & 63)) - 1)) != 0) s = __builtin_nan("");
-      if (g == 0) sh.group[tok][j] = s;
+      butterfly<G>([&](auto d) { total += partner_of<decltype(d)::value>(total); });
+      inv = total;
     }
-    lds_order();
-    // (by the lane: the groups of its experts)
-    int last = -1;
-    bool stays = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = g * V + v < a.experts ? g * V + v : a.experts - 1, mine = e / a.gsize;
-      if (mine != last) {
-        const double s = sh.group[tok][mine];
-        int rank = 0;
-        for (int j = 0; j < a.groups; ++j) {
-          const double o = sh.group[tok][j];
-          const bool above = s != s ? o != o && j < mine : o != o || o > s || (o == s && j < mine);
-          rank += above ? 1 : 0;
-        }
-        stays = rank < a.topk_groups && !(s == closed);
-        last = mine;
-      }
-      if (!stays) {
-        c[v] = closed;
-        nan[v] = false;
+      if (by_logit) c[v] = l[v];
+      else if (a.score == kScoreSigmoid) c[v] = 1.0 / (1.0 + exp(-(double)l[v]));
+      else c[v] = inv == 0.0 ? 0.0 : c[v] / inv;
+      if (a.bias && v < at0.many) c[v] += (double)a.bias[at0.first + v];
+      if (l[v] == kMasked) c[v] = closed;
+      if (c[v] != c[v]) {
+        nan |= 1u << v;
+        c[v] = __builtin_inf();
       }
     }
   }
+  if (limited) {
+    double t1 = closed, t2 = closed;
+#pragma unroll
+    for (int v = 0; v < V; ++v) merge2(t1, t2, c[v], closed);
+    sh.pair[tok][g][0] = nan ? __builtin_nan("") : t1;
+    sh.pair[tok][g][1] = t2;
+    lds_order();
+    if (g < a.groups) {
+      double s1 = closed, s2 = closed;
+      bool any = false;   // a group with a NaN is above every other
+      for (int i = 0; i < a.group_lanes; ++i) {
+        const double u = sh.pair[tok][g * a.group_lanes + i][0];
+        any |= u != u;
+        merge2(s1, s2, u, sh.pair[tok][g * a.group_lanes + i][1]);
+      }
+      if (a.group_top == 2 && s2 != closed) s1 += s2;
+      sh.score[tok][g] = any ? __builtin_nan("") : s1;
+    }
+    lds_order();
+    const int mine = at0.group < a.groups ? at0.group : 0;
+    const double s = sh.score[tok][mine];
+    int rank = 0;
+    for (int j = 0; j < a.groups; ++j) {
+      const double o = sh.score[tok][j];
+      rank += s != s ? (o != o && j < mine) : (o != o || o > s || (o == s && j < mine));
+    }
+    if (rank >= a.topk_groups || s == closed) {
+      nan = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = closed;
+    }
+  }
+  constexpr int kNone = 0x7FFFFFFF;
   for (int r = 0; r < a.topk; ++r) {
     double best = closed;
-    int at = 0x7FFFFFFF;
-    bool n = false;
+    int at = kNone, n = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool up = c[v] != closed && ((nan[v] && !n) || (nan[v] == n && c[v] > best) || at == 0x7FFFFFFF);
+      const int m = (nan >> v) & 1;
+      const bool up = c[v] != closed && (at == kNone || m > n || (m == n && c[v] > best));
       best = up ? c[v] : best;
-      at = up ? g * V + v : at;
-      n = up ? nan[v] : n;
+      at = up ? at0.first + v : at;
+      n = up ? m : n;
     }
-#pragma unroll
-    for (int d = 1; d < G; d <<= 1) {
-      const double ob = __shfl_xor(best, d, 64);
-      const int oa = __shfl_xor(at, d, 64);
-      const bool on = __shfl_xor((int)n, d, 64) != 0;
-      const bool up = oa != 0x7FFFFFFF &&
-                      (at == 0x7FFFFFFF || (on && !n) ||
-                       (on == n && (ob > best || (ob == best && oa < at))));
+    butterfly<G>([&](auto d) {
+      const double ob = partner_of<decltype(d)::value>(best);
+      const int oa = partner_of<decltype(d)::value>(at), on = partner_of<decltype(d)::value>(n);
+      const bool up = oa != kNone && (at == kNone || on > n || (on == n && (ob > best || (ob == best && oa < at))));
       best = up ? ob : best;
       at = up ? oa : at;
       n = up ? on : n;
-    }
+    });
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (g * V + v == at) c[v] = closed;
-    if (g == 0) sh.id[tok][r] = at == 0x7FFFFFFF ? -1 : at;
+      if (at0.first + v == at) c[v] = closed;
+    if (g == 0) sh.id[tok][r] = at == kNone ? -1 : at;
   }
   lds_order();
 }
@@ -227,196 +228,292 @@ __device__ __forceinline__ float sigmoid_over(float x, float most) {
   return expf(x - __builtin_fminf(most, 0.0f)) / (1.0f + expf(x));
 }
 
-// G lanes share a token, V of its experts each.  Each lane sorts its keys
-// once; a round then compares the lanes' first keys alone, and the lane that
-// has the largest moves on to its next.
+// G lanes share a token, V experts each of one group's (lanes and places order as
+// the experts do).  Each lane sorts its keys once; a round then compares the
+// lanes' first keys alone, and the lane that has the largest moves on to its
+// next.  Bound by vector instructions, most of them the scores' and keys' (about
+// ten and two slow ones an expert) and the rounds' (about 30).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logits, RouteGroups a) {
   __shared__ RouteShare<G, V> sh;
-  constexpr uint32_t kPlace = V - 1;   // the key's bits for the place: V - 1 - v
-  constexpr int KO = (kMaxTopk < G * V ? kMaxTopk : G * V) > G ? (kMaxTopk < G * V ? kMaxTopk : G * V) / G : 1;
+  constexpr uint32_t kPlace = V - 1;        // the key's bits for the place: V - 1 - v
+  constexpr uint32_t kOpen = 0x00800000u;   // keys of open experts are at least this
+  constexpr int KM = kMaxTopk < G * V ? kMaxTopk : G * V, KO = KM > G ? KM / G : 1;
   const int lane = threadIdx.x & 63, g = threadIdx.x % G, tok = threadIdx.x / G;
-  const int base = lane & ~(G - 1);
   const int64_t t = (int64_t)blockIdx.x * (256 / G) + tok;
   const bool live = t < a.tokens;   // the others repeat the last token, unstored
   const T* row = logits + (live ? t : a.tokens - 1) * a.ld;
-  float l[V];
-  load_run<T, V>(row, g * V, a.experts, l);
+  const RouteLane at0 = route_lane<V>(a, g);
   const bool limited = a.topk_groups < a.groups;
   // Without a bias the logits order as the scores do (but sums of two do not).
   const bool by_logit = !a.bias && !(limited && a.group_top == 2);
 
-  float top = 0.0f, total = 1.0f;   // softmax
-  if (a.score == kScoreSoftmax && !(by_logit && a.renorm)) {
-    top = l[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) top = __builtin_fmaxf(top, l[v]);
-    top = group_fmax<G>(top);
-    if (top == kMasked) top = 0.0f;
-    float part = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) part += __builtin_amdgcn_exp2f((l[v] - top) * kLog2e);
-    total = group_sum<G>(part);
-    if (total == 0.0f) total = 1.0f;
-  }
   uint32_t s[V];
+  float top = 0.0f, total = 1.0f;   // softmax
   {
+    float l[V], bias[V];
+    load_run<T, V>(row, at0.first, at0.many, l);
+    if (a.bias) load_run<float, V>(a.bias, at0.first, at0.many, bias);
+    if (a.score == kScoreSoftmax && !(by_logit && a.renorm)) {
+      top = l[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) top = __builtin_fmaxf(top, l[v]);
+      top = group_fmax<G>(top);
+      if (top == kMasked) top = 0.0f;
+      float part = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) part += __builtin_amdgcn_exp2f((l[v] - top) * kLog2e);
+      total = group_sum<G>(part);
+      if (total == 0.0f) total = 1.0f;
+    }
     const float inv = 1.0f / total;
+    float c[V];
+    if (by_logit) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = l[v] + 0.0f;   // (-0 as 0)
+    } else if (a.score == kScoreSigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l[v]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = __builtin_amdgcn_exp2f((l[v] - top) * kLog2e) * inv;
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] += bias[v];
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float c = l[v];
-      if (!by_logit) {
-        c = a.score == kScoreSigmoid
-                ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l[v]))
-                : __builtin_amdgcn_exp2f((l[v] - top) * kLog2e) * inv;
-        if (a.bias) c += g * V + v < a.experts ? a.bias[g * V + v] : 0.0f;
-      }
-      uint32_t k = f32_ordered(c + 0.0f);
-      if (c != c) k = 0xFFFFFFFFu;
-      k = (k & ~kPlace) | (kPlace - v);
-      s[v] = l[v] == kMasked || c == kMasked ? 0u : k;
+      c[v] = l[v] == kMasked ? kMasked : c[v];   // (its key is below kOpen)
+      uint32_t k = __float_as_uint(c[v]);
+      k ^= (uint32_t)((int32_t)k >> 31) | 0x80000000u;
+      k = c[v] != c[v] ? 0xFFFFFFFFu : k;
+      s[v] = (k & ~kPlace) | (kPlace - v);
     }
   }
-  // a key's value, and whether one lies so near below another that their order is open
-  auto value = [](uint32_t k) __attribute__((always_inline)) { return f32_from_ordered(k & ~kPlace); };
+  // A key's value, and whether one lies so near below another that their order is open.
   // Errors: a score's is at most 2^-20 (exp2 and the reciprocal 1 ulp each, the exponent |l| 2^-24, the
-  // sum of a softmax 2^-20), without a bias 2^-16 of it; a key's cut bits 2^-19 of the value.
+  // sum of a softmax 2^-20), without a bias 2^-16 of it; a key's cut bits 2^-18 of the value.
+  auto value = [](uint32_t k, uint32_t cut) __attribute__((always_inline)) { return f32_from_ordered(k & ~cut); };
   const float rel = a.bias ? 0x1p-17f : 0x1p-15f, abs_ = a.bias ? 0x1p-18f : 0.0f;
   auto near = [&](uint32_t hi, uint32_t lo) __attribute__((always_inline)) {
-    if (hi == 0u || lo == 0u) return false;
+    if (hi < kOpen || lo < kOpen) return false;
     if (by_logit) return sizeof(T) == 4 && (hi & ~kPlace) == (lo & ~kPlace);
-    const float x = value(hi), y = value(lo);
+    const float x = value(hi, kPlace), y = value(lo, kPlace);
     return x - y <= rel * __builtin_fabsf(x) + abs_;
   };
-  bool open = false;   // the order is open
-  if (!limited) {
-    sort_down<V>(s);
-  } else {
-    const int p = a.group_lanes;   // lanes to a group; 0: groups end inside a lane's run
-    // a group's score from its two largest keys, as an ordered key: 0 closed
-    auto score_key = [&](uint32_t k1, uint32_t k2) __attribute__((always_inline)) {
-      if (k1 == 0u) return 0u;
-      float x = value(k1);
-      if (a.group_top == 2 && k2 != 0u) x += value(k2);
-      return x != x ? 0xFFFFFFFFu : f32_ordered(x + 0.0f);
-    };
-    uint32_t lo = 0xFFFFFFFFu, hi = 0u;   // the last group that stays, the first that does not
-    float mag = 0.0f;
-    auto magnitude = [&](uint32_t k1, uint32_t k2) __attribute__((always_inline)) {
-      const float x = k1 ? __builtin_fabsf(value(k1)) + (k2 ? __builtin_fabsf(value(k2)) : 0.0f) : 0.0f;
-      mag = __builtin_fmaxf(mag, x);
-    };
-    if (p > 0) {
-      sort_down<V>(s);
-      uint32_t k1 = s[0], k2 = s[1];
-      if (p > 1) merge2(k1, k2, partner<1>(k1), partner<1>(k2));
-      if (p > 2) merge2(k1, k2, partner<2>(k1), partner<2>(k2));
-      if (p > 4) merge2(k1, k2, partner<4>(k1), partner<4>(k2));
-      if (p > 8) merge2(k1, k2, partner<8>(k1), partner<8>(k2));
-      if (p > 16) merge2(k1, k2, partner<16>(k1), partner<16>(k2));
-      const uint32_t mine = score_key(k1, k2);
-      magnitude(k1, k2);
-      const int at = g / p;
-      int rank = 0;
-      for (int j = 0; j < a.groups; ++j) {
-        const uint32_t o = (uint32_t)__shfl((int)mine, base + j * p, 64);
-        rank += o > mine || (o == mine && j < at) ? 1 : 0;
-      }
-      // (lanes past the last expert have closed groups)
-      const bool stays = rank < a.topk_groups && mine != 0u;
-      if (stays) lo = mine;
-      else hi = mine;
+  sort_down<V>(s);
+  auto bias_of = [&](int e) { return a.bias ? a.bias[e] : 0.0f; };
+  // of the same logit and bias: the lowest index has come first
+  auto same = [&](int d, int e) {
+    return Elem<T>::f32(row[d]) == Elem<T>::f32(row[e]) && bias_of(d) == bias_of(e);
+  };
+  auto exact = [&](int e) {   // (a softmax's sum is choose64's)
+    if (e < 0) return -__builtin_inf();
+    const double l = (double)Elem<T>::f32(row[e]);
+    return by_logit ? l : 1.0 / (1.0 + exp(-l)) + (double)bias_of(e);
+  };
+  bool open = false, all = false;   // the order is open; nothing but choose64 settles it
+  if (limited) {
+    // a group's score as a key whose lowest six bits give equal ones an order; closed: 0
+    constexpr uint32_t kCut = 63;
+    uint32_t* pairs = reinterpret_cast<uint32_t*>(sh.pair[tok]);
+    uint32_t* scores = reinterpret_cast<uint32_t*>(sh.score[tok]);
+    *reinterpret_cast<u32x4_t*>(pairs + 4 * g) = u32x4_t{s[0], s[1], s[2], 0u};
+    if (g < 4) sh.edge[tok][g] = 0u;
+    if constexpr (G < 4) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = stays ? s[v] : 0u;
-    } else {
-      uint32_t* score = reinterpret_cast<uint32_t*>(sh.group[tok]);
-      for (int j = 0; j < a.groups; ++j) {
-        uint32_t k1 = 0u, k2 = 0u;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int e = g * V + v;
-          merge2(k1, k2, e >= j * a.gsize && e < (j + 1) * a.gsize ? s[v] : 0u, 0u);
+      for (int i = G; i < 4; ++i) sh.edge[tok][i] = 0u;
+    }
+    lds_order();
+    const int padded = (a.groups + 3) & ~3;
+    for (int j = g; j < padded; j += G) {
+      uint32_t k1 = 0u, k2 = 0u, score = 0u;
+      if (j < a.groups) {
+        for (int i = 0; i < a.group_lanes; ++i) {
+          const u32x2_t o = *reinterpret_cast<const u32x2_t*>(pairs + 4 * (j * a.group_lanes + i));
+          merge2(k1, k2, o[0], o[1]);
         }
+      }
+      if (k1 >= kOpen) {
+        float x = value(k1, kPlace), size = __builtin_fabsf(x);
+        if (a.group_top == 2 && k2 >= kOpen) {
+          const float y = value(k2, kPlace);
+          x += y;
+          size += __builtin_fabsf(y);
+        }
+        sh.size[tok][j] = size;
+        score = ((x != x ? 0xFFFFFFFFu : f32_ordered(x + 0.0f)) & ~kCut) | (kCut - j);
+      }
+      scores[j] = score;
+    }
+    lds_order();
+    const int group = at0.group < a.groups ? at0.group : 0;
+    const uint32_t mine = scores[group];
+    int rank = 0;
+    for (int j = 0; j < padded; j += 4) {
+      const u32x4_t o = *reinterpret_cast<const u32x4_t*>(scores + j);
 #pragma unroll
-        for (int d = 1; d < G; d <<= 1)
-          merge2(k1, k2, (uint32_t)__shfl_xor((int)k1, d, 64), (uint32_t)__shfl_xor((int)k2, d, 64));
-        magnitude(k1, k2);
-        if (g == 0) score[j] = score_key(k1, k2);
+      for (int i = 0; i < 4; ++i) rank += o[i] > mine ? 1 : 0;
+    }
+    bool stays = rank < a.topk_groups && mine != 0u;
+    if (at0.many > 0 && at0.first == at0.group * a.gsize && mine != 0u &&
+        (rank == a.topk_groups - 1 || rank == a.topk_groups)) {
+      const int i = rank == a.topk_groups ? 2 : 0;
+      sh.edge[tok][i] = mine;
+      sh.edge[tok][i + 1] = __float_as_uint(sh.size[tok][group]);
+    }
+    lds_order();
+    const uint32_t hi = sh.edge[tok][0], lo = sh.edge[tok][2];
+    if (hi != 0u && lo != 0u) {
+      if (by_logit) {
+        open = sizeof(T) == 4 && (hi & ~kCut) == (lo & ~kCut);
+      } else {
+        const float x = value(hi, kCut), y = value(lo, kCut);
+        const float size = __builtin_fmaxf(__uint_as_float(sh.edge[tok][1]), __uint_as_float(sh.edge[tok][3]));
+        open = x - y <= 2.0f * (rel * size + abs_) + 0x1p-16f * __builtin_fabsf(x);
+      }
+    }
+    if (__builtin_expect(__ballot(open) != 0, 0)) {
+      // the groups' exact scores, of the two that lead each by a margin to its third
+      all = open && !by_logit && a.score == kScoreSoftmax;
+      if (g < a.groups) {
+        uint32_t k1 = 0u, k2 = 0u, k3 = 0u;
+        int e1 = -1, e2 = -1, e3 = -1;
+        for (int i = 0; i < a.group_lanes; ++i) {
+          const u32x4_t o = *reinterpret_cast<const u32x4_t*>(pairs + 4 * (g * a.group_lanes + i));
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const uint32_t k = o[q];
+            if (k < kOpen) continue;
+            const int e = g * a.gsize + i * V + (int)(kPlace - (k & kPlace));
+            if (k > k1) {
+              k3 = k2, e3 = e2;
+              k2 = k1, e2 = e1;
+              k1 = k, e1 = e;
+            } else if (k > k2) {
+              k3 = k2, e3 = e2;
+              k2 = k, e2 = e;
+            } else if (k > k3) {
+              k3 = k, e3 = e;
+            }
+          }
+        }
+        double x = exact(e1);
+        const double y = exact(e2);
+        if (a.group_top == 2) {
+          if (e2 >= 0) x += y;
+          all |= open && near(k2, k3) && !same(e2, e3);
+        } else {
+          x = y > x ? y : x;
+          all |= open && near(k1, k3) && !same(e1, e3);
+        }
+        all |= open && x != x;
+        sh.score[tok][g] = x;
       }
       lds_order();
-      int last = -1;
-      bool stays = false;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = g * V + v < a.experts ? g * V + v : a.experts - 1;
-        const int at = (int)(((uint64_t)(uint32_t)e * a.gsize_inv) >> 32);   // e / gsize
-        if (at != last) {
-          const uint32_t mine = score[at];
-          int rank = 0;
-          for (int j = 0; j < a.groups; ++j) {
-            const uint32_t o = score[j];
-            rank += o > mine || (o == mine && j < at) ? 1 : 0;
-          }
-          stays = rank < a.topk_groups && mine != 0u;
-          if (stays) lo = lo < mine ? lo : mine;
-          else hi = hi > mine ? hi : mine;
-          last = at;
+      if (open) {
+        const double x = sh.score[tok][group];
+        rank = 0;
+        for (int j = 0; j < a.groups; ++j) {
+          const double o = sh.score[tok][j];
+          rank += o > x || (o == x && j < group) ? 1 : 0;
         }
-        s[v] = stays ? s[v] : 0u;
+        stays = rank < a.topk_groups && x != -__builtin_inf();
       }
-      sort_down<V>(s);
+      open = false;
     }
-    lo = group_min<G>(lo);
-    hi = group_max<G>(hi);
-    mag = group_fmax<G>(mag);
-    if (lo != 0xFFFFFFFFu && hi != 0u) {
-      if (by_logit) {
-        open = sizeof(T) == 4 && lo == hi;   // (fp32: the cut bits decide)
-      } else {
-        const float x = f32_from_ordered(lo), y = f32_from_ordered(hi);
-        open = x - y <= 2.0f * (rel * mag + abs_);
-      }
-    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = stays ? s[v] : 0u;
   }
 
-  for (int r = 0; r < a.topk; ++r) {
+  // the largest key left goes to slot r
+  auto take = [&](int r) __attribute__((always_inline)) {
     const uint32_t head = s[0] & ~kPlace;
     const uint32_t best = group_max<G>(head);
-    uint64_t has = __ballot(head == best) >> base;
-    if constexpr (G < 64) has &= (1ull << (G & 63)) - 1;
+    const uint64_t has = __ballot(head == best);
     // equal keys: the lowest expert is the lowest lane's
-    if (g == __builtin_ctzll(has)) {
+    int first;
+    if constexpr (G == 64) {
+      first = __builtin_ctzll(has);
+    } else {
+      const uint32_t half = (uint32_t)(lane & 32 ? has >> 32 : has);
+      first = __builtin_ctz(G == 32 ? half : (half >> (lane & 31 & ~(G - 1))) & ((1u << (G & 31)) - 1u));
+    }
+    if (g == first) {
       sh.key[tok][r] = s[0];
-      sh.id[tok][r] = best == 0u ? -1 : g * V + (int)(kPlace - (s[0] & kPlace));
+      sh.id[tok][r] = s[0] < kOpen ? -1 : at0.first + (int)(kPlace - (s[0] & kPlace));
 #pragma unroll
       for (int v = 0; v + 1 < V; ++v) s[v] = s[v + 1];
       s[V - 1] = 0u;
     }
-  }
+  };
+  for (int r = 0; r < a.topk; ++r) take(r);
   lds_order();
 
-  // Is the order of the chosen open, or the last one's to what was left?  Two
-  // of the same logit and bias are not: the lowest index has come first.
-  auto bias_of = [&](int e) { return a.bias ? a.bias[e] : 0.0f; };
-  auto same = [&](int d, int e) {
-    return Elem<T>::f32(row[d]) == Elem<T>::f32(row[e]) && bias_of(d) == bias_of(e);
-  };
+  // Is the order of the chosen open, or the last one's to what was left?
 #pragma unroll
   for (int o = 0; o < KO; ++o) {
     const int j = o * G + g;
     if (j + 1 < a.topk && near(sh.key[tok][j], sh.key[tok][j + 1]))
       open |= !same(sh.id[tok][j], sh.id[tok][j + 1]);
   }
-  {
-    const uint32_t last = sh.key[tok][a.topk - 1];
-    if (near(last, s[0])) {
+  const uint32_t last = sh.key[tok][a.topk - 1];
+  if (near(last, s[0])) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (near(last, s[v]))
-          open |= !same(sh.id[tok][a.topk - 1], g * V + (int)(kPlace - (s[v] & kPlace)));
-    }
+    for (int v = 0; v < V; ++v)
+      if (near(last, s[v]))
+        open |= !same(sh.id[tok][a.topk - 1], at0.first + (int)(kPlace - (s[v] & kPlace)));
   }
-  if (__builtin_expect(__ballot(open) != 0, 0)) choose64<G, V>(l, a, g, tok, sh);
+  // (a lane's own finding is its token's)
+  open = group_max<G>(open ? 1u : 0u) != 0u;
+  if (__builtin_expect(__ballot(open || all) != 0, 0)) {
+    // Mostly two neighbours: the chosen and the next one are ranked by their exact
+    // values.  Where that does not settle it (more behind the next one, a softmax's
+    // sum, NaN), all of it again.
+    take(a.topk);
+    lds_order();
+    all |= open && ((!by_logit && a.score == kScoreSoftmax) || near(last, s[0]));
+    auto above = [](double c, int e, double d, int f) { return c > d || (c == d && (uint32_t)e < (uint32_t)f); };
+    const int next = sh.id[tok][a.topk];
+    const double cn = exact(next);
+    double c[KO];
+    int e[KO], rank[KO], below = 0;   // of the slots, that are above the next one
+    all |= open && cn != cn;
+#pragma unroll
+    for (int o = 0; o < KO; ++o) {
+      const int j = o * G + g;
+      e[o] = j < a.topk ? sh.id[tok][j] : -1;
+      c[o] = exact(e[o]);
+      all |= open && c[o] != c[o];
+      rank[o] = above(cn, next, c[o], e[o]) ? 1 : 0;
+    }
+#pragma unroll
+    for (int o = 0; o < KO; ++o) {
+#pragma unroll 1
+      for (int i = 0; i < G; ++i) {
+        const int src = (lane & ~(G - 1)) + i;
+        const double d = __shfl(c[o], src, 64);
+        const int f = __shfl(e[o], src, 64);
+        below += above(d, f, cn, next) ? 1 : 0;
+#pragma unroll
+        for (int q = 0; q < KO; ++q) rank[q] += above(d, f, c[q], e[q]) ? 1 : 0;
+      }
+    }
+    lds_order();
+    if (open) {   // (the wavefront's other tokens are as they were)
+#pragma unroll
+      for (int o = 0; o < KO; ++o)
+        if (o * G + g < a.topk) sh.id[tok][o * G + g] = -1;
+      lds_order();
+#pragma unroll
+      for (int o = 0; o < KO; ++o)
+        if (e[o] >= 0 && rank[o] < a.topk) sh.id[tok][rank[o]] = e[o];
+      if (g == 0 && next >= 0 && below < a.topk) sh.id[tok][below] = next;
+    }
+    lds_order();
+    if (__ballot(all) != 0) choose64<T, G, V>(row, a, g, tok, sh);
+  }
 
   // the weights
   float x[KO];
@@ -525,7 +622,7 @@ __global__ __launch_bounds__(256) void k_route_groups_grad(const T* logits, Rout
       if (id[o] >= 0) img[tok][id[o]] = d[o];
     lds_order();
     float l[V];
-    load_run<T, V>(row, g * V, a.experts, l);
+    load_run<T, V>(row, g * V, a.experts - g * V, l);
     float top = l[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) top = __builtin_fmaxf(top, l[v]);
@@ -580,22 +677,55 @@ __global__ __launch_bounds__(256) void k_route_groups_grad(const T* logits, Rout
     CALL(64, 16);                 \
   }
 
+template <typename T, int G, int V>
+void groups_gv(const T* l, const RouteGroups& a, hipStream_t st) {
+  in_launches(a.tokens, 256 / G, [&](int64_t t, int64_t n) {
+    RouteGroups b = a;
+    b.tokens = n;
+    b.ids += t * a.topk;
+    b.weights += t * a.topk;
+    k_route_groups<T, G, V><<<dim3((unsigned)((n + 256 / G - 1) / (256 / G))), 256, 0, st>>>(l + t * a.ld, b);
+  });
+}
+
+// Lanes a token and experts a lane.  A group takes whole lanes; with 32 experts a lane any division fits
+// 64 lanes.
 template <typename T>
-void groups_t(const T* l, const RouteGroups& a, hipStream_t st) {
-  const int experts = a.experts;
-#define AVERIS_ROUTE(G, V)                                                                       \
-  in_launches(a.tokens, 256 / G, [&](int64_t t, int64_t n) {                                     \
-    RouteGroups b = a;                                                                           \
-    b.tokens = n;                                                                                \
-    b.ids += t * a.topk;                                                                         \
-    b.weights += t * a.topk;                                                                     \
-    const int p = a.gsize / V;                                                                   \
-    b.group_lanes = a.gsize % V == 0 && (p & (p - 1)) == 0 ? p : 0;                              \
-    k_route_groups<T, G, V><<<dim3((unsigned)((n + 256 / G - 1) / (256 / G))), 256, 0, st>>>(    \
-        l + t * a.ld, b);                                                                        \
-  })
-  AVERIS_GROUP_SHAPES(AVERIS_ROUTE)
-#undef AVERIS_ROUTE
+void groups_t(const T* l, RouteGroups a, hipStream_t st) {
+  if (a.topk_groups == a.groups) {   // no group matters
+    a.groups = a.topk_groups = 1;
+    a.gsize = a.experts;
+  }
+  auto lanes = [&](int v) {
+    int need = a.groups * ((a.gsize + v - 1) / v), g = 1;
+    while (g < need) g *= 2;
+    return g;
+  };
+  auto shape = [&](int v) {
+    a.group_lanes = (a.gsize + v - 1) / v;
+    a.lanes_inv = (((uint64_t)1 << 32) + (uint64_t)a.group_lanes - 1) / (uint64_t)a.group_lanes;
+  };
+  const int g8 = lanes(8), g16 = lanes(16);
+  if (g8 <= 4) {
+    shape(8);
+    if (g8 == 1) groups_gv<T, 1, 8>(l, a, st);
+    else if (g8 == 2) groups_gv<T, 2, 8>(l, a, st);
+    else groups_gv<T, 4, 8>(l, a, st);
+  } else if (g8 <= 16 && g16 == g8) {   // sixteen a lane need as many: eight
+    shape(8);
+    if (g8 == 8) groups_gv<T, 8, 8>(l, a, st);
+    else groups_gv<T, 16, 8>(l, a, st);
+  } else if (g16 <= 64) {
+    shape(16);
+    if (g16 <= 4) groups_gv<T, 4, 16>(l, a, st);
+    else if (g16 == 8) groups_gv<T, 8, 16>(l, a, st);
+    else if (g16 == 16) groups_gv<T, 16, 16>(l, a, st);
+    else if (g16 == 32) groups_gv<T, 32, 16>(l, a, st);
+    else groups_gv<T, 64, 16>(l, a, st);
+  } else {
+    shape(32);
+    groups_gv<T, 64, 32>(l, a, st);
+  }
 }
 
 template <typename T>
