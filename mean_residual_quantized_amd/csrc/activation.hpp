@@ -24,17 +24,15 @@ __device__ __forceinline__ float act_gelu(float z) {
 }
 
 // d/dz of z s(u): s + z s (1 - s) du/dz.  Past |z| = 100 it is its limit, 1 or 0, and the products of its
-// terms might overflow: z is held there (a NaN stays one).
-__device__ __forceinline__ float act_held(float z) { return z > 100.0f ? 100.0f : z < -100.0f ? -100.0f : z; }
+// terms might overflow: z is held there (where it is NaN, s is).
 __device__ __forceinline__ float act_silu_slope(float z) {
-  z = act_held(z);
-  const float s = act_sigmoid(kActLog2e * z);
-  return __builtin_fmaf(z * s, 1.0f - s, s);
+  const float s = act_sigmoid(kActLog2e * z), h = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f);
+  return __builtin_fmaf(h * s, 1.0f - s, s);
 }
 __device__ __forceinline__ float act_gelu_slope(float z) {
-  z = act_held(z);
-  const float q = z * z, s = act_sigmoid(z * __builtin_fmaf(kGeluB * kActLog2e, q, kGeluA * kActLog2e));
-  return __builtin_fmaf(z * s * (1.0f - s), __builtin_fmaf(3.0f * kGeluB, q, kGeluA), s);
+  const float h = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f), q = h * h;
+  const float s = act_sigmoid(z * __builtin_fmaf(kGeluB * kActLog2e, q, kGeluA * kActLog2e));
+  return __builtin_fmaf(h * s * (1.0f - s), __builtin_fmaf(3.0f * kGeluB, q, kGeluA), s);
 }
 
 }  // namespace averis

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const T* __restrict__ a, int64
 template <typename T>
 struct PlainSrc {   // a matrix as it is
   using Type = T;
-  static constexpr bool kSums = false;
+  static constexpr bool kSums = false, kLastFirst = false;
   const T* a;
   int64_t ld, bstride;
   using Raw = Eight<T>;
@@ -80,7 +80,7 @@ struct PlainSrc {   // a matrix as it is
 template <typename T>
 struct NormSrc {
   using Type = T;
-  static constexpr bool kSums = false;
+  static constexpr bool kSums = false, kLastFirst = true;
   const T* h;
   int64_t ld;
   const float* rstd;
@@ -117,7 +117,7 @@ struct NormSrc {
 template <typename T>
 struct ActSrc {
   using Type = T;
-  static constexpr bool kSums = true;
+  static constexpr bool kSums = true, kLastFirst = false;
   const T* dy;
   const T* z;
   int64_t lddy, ldz;
@@ -204,7 +204,8 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(Src source, int64_t r
   // sums: a column's part of each wavefront
   float* sums = reinterpret_cast<float*>(sm + fp8_tile_lds<T>());
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  uint32_t id = blockIdx.x;
+  // (a source that was written just now: its last rows first, while the last-level cache has them)
+  uint32_t id = Src::kLastFirst ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
   if (near && id < (gridDim.x & ~63u)) id = (id & ~63u) + (id & 7u) * 8u + (id >> 3 & 7u);
   const int chunk = (int)(id / (uint32_t)tx), block = (int)(id % (uint32_t)tx);
   const int64_t c0 = (int64_t)block * 128;

@@ -29,6 +29,43 @@ __device__ __forceinline__ F wave_sum(F v) {
   return v;
 }
 
+// EIGHTS: rows of whole pieces (cols a multiple of 8), whose loads and stores
+// need no code for a row's last elements (with it the gradient of 16384 x 1001
+// takes 45 us, of 16384 x 1024 30)
+template <bool EIGHTS, typename T>
+__device__ __forceinline__ void load8(Eight<T>& v, const T* row, int64_t c, int64_t cols) {
+  if constexpr (EIGHTS) {
+    v.zero();
+    if (c < cols) v.load(row + c, 0, 8);
+  } else {
+    v.load(row, c, cols);
+  }
+}
+template <bool EIGHTS, typename T>
+__device__ __forceinline__ void store8(const Eight<T>& v, T* row, int64_t c, int64_t cols) {
+  if constexpr (EIGHTS) {
+    if (c < cols) v.store(row + c, 0, 8);
+  } else {
+    v.store(row, c, cols);
+  }
+}
+template <bool EIGHTS>
+__device__ __forceinline__ void weight8(const void* w, bool bf16, int64_t c, int64_t cols, float* f) {
+  if constexpr (EIGHTS) {
+    if (bf16) {
+      Eight<uint16_t> v;
+      load8<true>(v, static_cast<const uint16_t*>(w), c, cols);
+      v.f32(f);
+    } else {
+      Eight<float> v;
+      load8<true>(v, static_cast<const float*>(w), c, cols);
+      v.f32(f);
+    }
+  } else {
+    load_vector(w, bf16, c, cols, f);
+  }
+}
+
 // columns of the lane's piece i: 512 to a wavefront and step, so that sixteen
 // lanes hold a block of 128
 template <int W>
@@ -37,7 +74,7 @@ __device__ __forceinline__ int64_t piece_at(int lane, int g, int i) {
 }
 
 // W wavefronts hold a row, I pieces of eight elements a lane.
-template <typename T, int W, int I>
+template <typename T, int W, int I, bool EIGHTS>
 __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64_t row0, int64_t rows,
                                                                int64_t cols, double inv_cols, Fp8Out out) {
   constexpr int PER = W > 4 ? 1 : 4 / W;   // rows a workgroup
@@ -51,12 +88,12 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   Eight<T> h[I];
 #pragma unroll
-  for (int i = 0; i < I; ++i) h[i].load(x, piece_at<W>(lane, g, i), cols);
+  for (int i = 0; i < I; ++i) load8<EIGHTS>(h[i], x, piece_at<W>(lane, g, i), cols);
   if (a.res) {
     const T* res = static_cast<const T*>(a.res) + row * a.ldres;
     Eight<T> v[I];
 #pragma unroll
-    for (int i = 0; i < I; ++i) v[i].load(res, piece_at<W>(lane, g, i), cols);
+    for (int i = 0; i < I; ++i) load8<EIGHTS>(v[i], res, piece_at<W>(lane, g, i), cols);
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       float f[8], e[8];
@@ -69,7 +106,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64
     if (live) {
 #pragma unroll
       for (int i = 0; i < I; ++i)
-        h[i].store(static_cast<T*>(a.h) + row * a.ldh, piece_at<W>(lane, g, i), cols);
+        store8<EIGHTS>(h[i], static_cast<T*>(a.h) + row * a.ldh, piece_at<W>(lane, g, i), cols);
     }
   }
   double sum = 0.0;
@@ -97,12 +134,12 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64
     if (c - 8 * lane >= cols) break;
     float v[8], wt[8];
     h[i].f32(v);
-    load_vector(a.weight, a.wbf16, c, cols, wt);
+    weight8<EIGHTS>(a.weight, a.wbf16, c, cols, wt);
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = v[q] * f * wt[q];
     Eight<T> y;
     y.set(v);
-    if (a.y) y.store(static_cast<T*>(a.y) + row * a.ldy, c, cols);
+    if (a.y) store8<EIGHTS>(y, static_cast<T*>(a.y) + row * a.ldy, c, cols);
     if (out.codes) {
       uint32_t byte;
       u32x2_t q = eight_codes(y, row16_max(y.amax()), byte);
@@ -118,7 +155,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64
 
 // Workgroup b takes rows b PER + .., each gridDim.x PER further on, and adds up
 // the weight's gradient of them in registers: part[b][cols].
-template <typename T, int W, int I>
+template <typename T, int W, int I, bool EIGHTS>
 __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs a, int64_t rows,
                                                                     int64_t cols, float inv_cols,
                                                                     float* __restrict__ part) {
@@ -131,7 +168,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs
   float wt[I][8], dw[I][8];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    load_vector(a.weight, a.wbf16, piece_at<W>(lane, g, i), cols, wt[i]);
+    weight8<EIGHTS>(a.weight, a.wbf16, piece_at<W>(lane, g, i), cols, wt[i]);
 #pragma unroll
     for (int q = 0; q < 8; ++q) dw[i][q] = 0.0f;
   }
@@ -143,13 +180,13 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs
     Eight<T> dy[I], h[I], res[I];
 #pragma unroll
     for (int i = 0; i < I; ++i) {
-      dy[i].load(static_cast<const T*>(a.dy) + at * a.lddy, piece_at<W>(lane, g, i), cols);
-      h[i].load(static_cast<const T*>(a.h) + at * a.ldh, piece_at<W>(lane, g, i), cols);
+      load8<EIGHTS>(dy[i], static_cast<const T*>(a.dy) + at * a.lddy, piece_at<W>(lane, g, i), cols);
+      load8<EIGHTS>(h[i], static_cast<const T*>(a.h) + at * a.ldh, piece_at<W>(lane, g, i), cols);
     }
     if (a.dres) {
 #pragma unroll
       for (int i = 0; i < I; ++i)
-        res[i].load(static_cast<const T*>(a.dres) + at * a.lddres, piece_at<W>(lane, g, i), cols);
+        load8<EIGHTS>(res[i], static_cast<const T*>(a.dres) + at * a.lddres, piece_at<W>(lane, g, i), cols);
     }
     const float f = a.rstd[at];
     float c = 0.0f;
@@ -189,7 +226,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs
       }
       Eight<T> o;
       o.set(d);
-      o.store(static_cast<T*>(a.dh) + at * a.lddh, piece_at<W>(lane, g, i), cols);
+      store8<EIGHTS>(o, static_cast<T*>(a.dh) + at * a.lddh, piece_at<W>(lane, g, i), cols);
     }
   }
   if (!part) return;
@@ -254,23 +291,45 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __r
   }
 }
 
-// f(W, I) for a row of `cols`
+// f(W, I) for a row of `cols`.  Two pieces a lane (us, bf16: 32768 x 2048 one / two / four pieces 86.6 /
+// 82.6 / 84.9, 8192 x 8192 92.6 / 85.0 / 87.7, 16384 x 1024 22.0 / 19.7).
 template <typename F>
 auto norm_shape(int64_t cols, F f) {
   using std::integral_constant;
   if (cols <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
   if (cols <= 1024) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (cols <= 2048) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-  if (cols <= 4096) return f(integral_constant<int, 2>{}, integral_constant<int, 4>{});
-  if (cols <= 8192) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  if (cols <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+  if (cols <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  if (cols <= 8192) return f(integral_constant<int, 8>{}, integral_constant<int, 2>{});
   return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
 }
+// The gradient: one piece, for its registers (one / two / four: 32768 x 2048 107.2 / 109.3 / 107.2, 16384 x
+// 4096 105 / 113 / 109, 8192 x 8192 108 / 112 / 123, 2999 x 1000 fp32 15.9 / 17.2).
+template <typename F>
+auto grad_shape(int64_t cols, F f) {
+  using std::integral_constant;
+  if (cols <= 512) return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  if (cols <= 1024) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  if (cols <= 2048) return f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  if (cols <= 4096) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (cols <= 8192) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+}
 
-// workgroups of the gradient: four of four wavefronts a CU
+// f(a value of the type, whether rows are of whole pieces)
+template <typename F>
+void of_kind(bool bf16, int64_t cols, F f) {
+  if (bf16 && cols % 8 == 0) f(uint16_t{}, std::true_type{});
+  else if (bf16) f(uint16_t{}, std::false_type{});
+  else if (cols % 8 == 0) f(float{}, std::true_type{});
+  else f(float{}, std::false_type{});
+}
+
+// workgroups of the gradient: four of four wavefronts a CU, or two larger ones
 constexpr int64_t kNormGradBlocks = 1024;
 
 int64_t norm_grad_blocks(int64_t rows, int64_t cols) {
-  return norm_shape(cols, [&](auto wc, auto) {
+  return grad_shape(cols, [&](auto wc, auto) {
     constexpr int W = decltype(wc)::value, PER = W > 4 ? 1 : 4 / W;
     const int64_t most = W > 4 ? kNormGradBlocks / 2 : kNormGradBlocks, need = (rows + PER - 1) / PER;
     return need < most ? need : most;
@@ -289,10 +348,9 @@ hipError_t launch_norm(const NormArgs& a, bool bf16, int64_t rows, int64_t cols,
     for (int64_t r = 0; r < rows; r += kMost * PER) {
       const int64_t n = (rows - r + PER - 1) / PER;
       const dim3 grid((unsigned)(n < kMost ? n : kMost)), block(W > 4 ? 64 * W : 256);
-      if (bf16)
-        k_norm<uint16_t, W, I><<<grid, block, 0, st>>>(a, r, rows, cols, inv, out);
-      else
-        k_norm<float, W, I><<<grid, block, 0, st>>>(a, r, rows, cols, inv, out);
+      of_kind(bf16, cols, [&](auto t, auto ec) {
+        k_norm<decltype(t), W, I, decltype(ec)::value><<<grid, block, 0, st>>>(a, r, rows, cols, inv, out);
+      });
     }
     return 0;
   });
@@ -308,15 +366,14 @@ hipError_t launch_norm_grad(const NormGradArgs& a, bool bf16, int64_t rows, int6
   const int64_t blocks = norm_grad_blocks(rows, cols);
   float* part = a.dweight ? static_cast<float*>(ws) : nullptr;
   if (rows > 0) {
-    norm_shape(cols, [&](auto wc, auto ic) {
+    grad_shape(cols, [&](auto wc, auto ic) {
       constexpr int W = decltype(wc)::value, I = decltype(ic)::value, PER = W > 4 ? 1 : 4 / W;
       const dim3 grid((unsigned)blocks), block(W > 4 ? 64 * W : 256);
       const size_t lds = part && PER > 1 ? (size_t)PER * cols * 4 : 0;   // at most 32 KB
       const float inv = (float)(1.0 / (double)cols);
-      if (bf16)
-        k_norm_grad<uint16_t, W, I><<<grid, block, lds, st>>>(a, rows, cols, inv, part);
-      else
-        k_norm_grad<float, W, I><<<grid, block, lds, st>>>(a, rows, cols, inv, part);
+      of_kind(bf16, cols, [&](auto t, auto ec) {
+        k_norm_grad<decltype(t), W, I, decltype(ec)::value><<<grid, block, lds, st>>>(a, rows, cols, inv, part);
+      });
       return 0;
     });
     const hipError_t e = hipGetLastError();
