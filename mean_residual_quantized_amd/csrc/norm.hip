@@ -264,12 +264,15 @@ constexpr int kSumWaves = 16;
 __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __restrict__ part,
                                                                 int64_t rows, int64_t ch, int64_t cols,
                                                                 const int64_t* offs, int nseg,
+                                                                int64_t chunks,
                                                                 float* __restrict__ out) {
   __shared__ float sh[kSumWaves][64];
   const SegRange s = describe_segment(offs, nseg, rows, ch, blockIdx.y);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane, n = s.c1 - s.c0;
-  const int64_t i0 = s.c0 + n * w / kSumWaves, i1 = s.c0 + n * (w + 1) / kSumWaves;
+  // within the array whatever the offsets hold (decreasing ones may claim rows twice)
+  const int64_t c0 = s.c0 < chunks ? s.c0 : chunks, c1 = s.c1 < chunks ? s.c1 : chunks;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane, n = c1 - c0;
+  const int64_t i0 = c0 + n * w / kSumWaves, i1 = c0 + n * (w + 1) / kSumWaves;
   float v = 0.0f;
   if (c < cols) {
     int64_t i = i0;
@@ -385,7 +388,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, bool bf16, int64_t rows, int6
 hipError_t launch_column_sums(const float* part, int64_t rows, int64_t ch, int64_t cols,
                               const int64_t* offs, int nseg, float* out, hipStream_t st) {
   k_column_sums<<<dim3((unsigned)((cols + 63) / 64), (unsigned)nseg), 64 * kSumWaves, 0, st>>>(
-      part, rows, ch, cols, offs, nseg, out);
+      part, rows, ch, cols, offs, nseg, chunk_upper_bound(rows, offs ? nseg : 1, ch), out);
   return hipGetLastError();
 }
 

@@ -136,6 +136,24 @@ def test_segments(offs, act, dtype):
         assert torch.equal(db[s], pb)
 
 
+def test_malformed_offsets_address_nothing_outside():
+    """Decreasing and outlying offsets, which the kernels clamp, claim rows more than once: more runs than any
+    division of the rows has.  What the calls before and after wrote stays."""
+    rows, cols = 300, 200
+    dy = torch.randn(rows, cols, device="cuda")
+    ref = av.averis_fp8_act_grad(dy)
+    for offs in ([0, 300, 0, 300, 0, 300], [-5, 400, 7, 1 << 40, -(1 << 40), 300, 2, 290, 1, 300], [300, 0, 300, 0]):
+        o = torch.tensor(offs, dtype=torch.int64, device="cuda")
+        need = av.workspace_bytes(av.OP_FP8_ACT_GRAD, rows, cols, 0, len(offs) - 1)
+        buf = torch.full((need + 512,), 77, dtype=torch.uint8, device="cuda")
+        _, _, db = av.averis_fp8_act_grad(dy, offsets=o, ws=buf[:need])
+        assert db.shape == (len(offs) - 1, cols)
+        assert (buf[need:] == 77).all()
+    again = av.averis_fp8_act_grad(dy)
+    assert torch.equal(again[0].codes, ref[0].codes) and torch.equal(again[1].codes, ref[1].codes)
+    assert torch.equal(again[2], ref[2])
+
+
 def test_special_values():
     inf, nan = float("inf"), float("nan")
     z = torch.tensor([[inf, -inf, nan, 1e30, -1e30, 0.0, -0.0, 200.0, -200.0]], device="cuda")
