@@ -653,7 +653,8 @@ typedef enum {
  * residual, in fp32 and rounded once to c's type.  bias: n values (F32 or BF16;
  * with segments n for each, nseg x n), or NULL.  residual: m x n of c's type, row
  * stride ldr, or NULL; it may be c.  z: also written, m x n of c's type, row stride
- * ldz, for averis_fp8_act_grad, or NULL.  An infinite z with a smooth activation
+ * ldz, for averis_fp8_act_grad, or NULL; it overlaps neither c nor residual.  An
+ * infinite z with a smooth activation
  * gives what the formula gives (-inf: NaN).  Everything else, the workspace too,
  * as for averis_fp8_gemm. */
 averis_status_t averis_fp8_gemm_act(const averis_fp8_t* a, const averis_fp8_t* b, const void* bias,

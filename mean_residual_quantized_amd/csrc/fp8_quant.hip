@@ -76,7 +76,8 @@ struct PlainSrc {   // a matrix as it is
 };
 
 // a norm's output from the sum it is of and each row's factor: the same
-// operations as k_norm's, so the same values
+// operations as k_norm's, so the same values.  Last rows first: after k_norm
+// 32768 x 2048 45 -> 38 us.
 template <typename T>
 struct NormSrc {
   using Type = T;
@@ -113,7 +114,9 @@ struct NormSrc {
   }
 };
 
-// dy act'(z), and its sums over the rows (in fp32, before it is rounded)
+// dy act'(z), and its sums over the rows (in fp32, before it is rounded).  Both
+// copies: 16384 x 4096 gelu bf16 88 us (403 MB, 4.6 TB/s; its vector instructions
+// alone about 50), 32768 x 768 in 64 segments 39 us.
 template <typename T>
 struct ActSrc {
   using Type = T;

@@ -232,7 +232,10 @@ __device__ __forceinline__ float sigmoid_over(float x, float most) {
 // the experts do).  Each lane sorts its keys once; a round then compares the
 // lanes' first keys alone, and the lane that has the largest moves on to its
 // next.  Bound by vector instructions, most of them the scores' and keys' (about
-// ten and two slow ones an expert) and the rounds' (about 30).
+// ten and two slow ones an expert), the sort's (eight an expert) and the rounds'
+// (about 40): 65521 tokens of 256 experts in 8 groups, top 8, fp32 33 us (67 MB,
+// 2.0 TB/s; 69 with eight experts a lane and every near choice made again whole),
+// 10007 of 160 in 8 groups bf16 8.3 us, 16 of 64 4.8 us (latency).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logits, RouteGroups a) {
   __shared__ RouteShare<G, V> sh;
@@ -558,7 +561,8 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
 //   sigmoid:  dl_j = (D_j - m) w_j (1 - s_j), renormalised; D_j s_j (1 - s_j) else
 //   softmax:  dl_j = (D_j - m) w_j over the chosen, renormalised; over all experts else
 // The chosen few are scattered into the token's zeros in LDS, and whole rows
-// written.
+// written.  Bound by memory: 65521 tokens of 256 experts fp32 18 us (67 MB written
+// and 36 read, a line for each chosen logit).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route_groups_grad(const T* logits, RouteGroupsGrad a,
                                                            T* dlogits) {
@@ -688,8 +692,10 @@ void groups_gv(const T* l, const RouteGroups& a, hipStream_t st) {
   });
 }
 
-// Lanes a token and experts a lane.  A group takes whole lanes; with 32 experts a lane any division fits
-// 64 lanes.
+// Lanes a token and experts a lane: sixteen, for a wavefront's rounds serve all its tokens (65521 x 256,
+// without the second looks: eight experts on each of 32 lanes 48 us, sixteen on each of 16 29 us), eight
+// where sixteen would need as many lanes.  A group takes whole lanes; with 32 experts a lane any division
+// fits 64 lanes.
 template <typename T>
 void groups_t(const T* l, RouteGroups a, hipStream_t st) {
   if (a.topk_groups == a.groups) {   // no group matters

@@ -73,7 +73,11 @@ __device__ __forceinline__ int64_t piece_at(int lane, int g, int i) {
   return 512 * (int64_t)(g + W * i) + 8 * lane;
 }
 
-// W wavefronts hold a row, I pieces of eight elements a lane.
+// W wavefronts hold a row, I pieces of eight elements a lane: the row is read
+// once, into registers.  Bound by memory: 32768 x 2048 bf16 with a residual and
+// codes 79 us (470 MB, 5.9 TB/s; a copy reaches 5.3), 2999 x 1000 fp32 9 us
+// (latency), 16 x 2048 4.2 us.  The transposed copy is k_fp8_tile's, from h and f:
+// 38 us more (201 MB): its runs go across 128 rows, more than a workgroup holds.
 template <typename T, int W, int I, bool EIGHTS>
 __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64_t row0, int64_t rows,
                                                                int64_t cols, double inv_cols, Fp8Out out) {
@@ -154,7 +158,8 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm(NormArgs a, int64
 }
 
 // Workgroup b takes rows b PER + .., each gridDim.x PER further on, and adds up
-// the weight's gradient of them in registers: part[b][cols].
+// the weight's gradient of them in registers: part[b][cols].  Bound by memory:
+// 32768 x 2048 bf16 107 us (537 MB and 8 MB of partial sums, 5.1 TB/s).
 template <typename T, int W, int I, bool EIGHTS>
 __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs a, int64_t rows,
                                                                     int64_t cols, float inv_cols,
@@ -258,7 +263,8 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs
 }
 
 // 64 columns and one segment a workgroup, its chunks divided in order among 16
-// wavefronts, whose sums are added in order
+// wavefronts, whose sums are added in order.  Bound by latency: 1024 x 2048
+// 5.9 us, 320 chunks of 768 in 64 segments 4.6 us.
 constexpr int kSumWaves = 16;
 
 __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __restrict__ part,
