@@ -654,9 +654,8 @@ typedef enum {
  * with segments n for each, nseg x n), or NULL.  residual: m x n of c's type, row
  * stride ldr, or NULL; it may be c.  z: also written, m x n of c's type, row stride
  * ldz, for averis_fp8_act_grad, or NULL; it overlaps neither c nor residual.  An
- * infinite z with a smooth activation
- * gives what the formula gives (-inf: NaN).  Everything else, the workspace too,
- * as for averis_fp8_gemm. */
+ * infinite z with a smooth activation gives what the formula gives (-inf: NaN).
+ * Everything else, the workspace too, as for averis_fp8_gemm. */
 averis_status_t averis_fp8_gemm_act(const averis_fp8_t* a, const averis_fp8_t* b, const void* bias,
                                     averis_dtype_t bias_dtype, averis_act_t act,
                                     const void* residual, int64_t ldr, const int64_t* seg_offsets,
