@@ -1202,9 +1202,10 @@ hipError_t launch_fp8_gemm(const Fp8Gemm& g, void* ws, hipStream_t st) {
   if (p.skinny == 1) return skinny<1>(g, st);
   if (p.skinny == 2) return skinny<2>(g, st);
   if (p.skinny == 4) return skinny<4>(g, st);
+  // the large tile's epilogue takes eight columns a lane, in pieces of 16 bytes; any other form the small one's
   if (g.epilogue && p.f == 4 && p.splits == 1) {
     const int es = g.c_bf16 ? 2 : 4;
-    if (!(g.n * es % 16 == 0 && g.ldc * es % 16 == 0 && g.ldc <= (1 << 21) &&
+    if (!(g.n % 8 == 0 && g.ldc * es % 16 == 0 && g.ldc <= (1 << 21) &&
           (reinterpret_cast<uintptr_t>(g.c) & 15) == 0 && epilogue_whole(*g.epilogue, es)))
       p.f = 2;
   }

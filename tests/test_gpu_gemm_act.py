@@ -195,3 +195,23 @@ def test_offsets_past_32_bits():
                                out=res)
     ref = (x[some].double() @ y.double().t() + bias.double()).clamp(min=0.0) + 5.0
     assert torch.equal(c[some].double(), ref)
+
+
+@pytest.mark.parametrize("offs", [None, [0, 900, 900, 2000, 4096]])
+def test_columns_in_half_a_lane(offs):
+    """fp32 rows of whole 16-byte pieces, four columns past a multiple of eight: nothing is read or written
+    past a row's end, whichever tile is taken."""
+    m, n, k = 4096, 4092, 640
+    nseg = 1 if offs is None else len(offs) - 1
+    rng = np.random.default_rng(n)
+    a, b = operands(rng, m, nseg * n, k)
+    o = None if offs is None else torch.tensor(offs, dtype=torch.int64, device="cuda")
+    bias = torch.randn(n if offs is None else (nseg, n), device="cuda")
+    res = torch.randn(m, n, device="cuda")
+    z = av.averis_fp8_gemm(a, b, F32, offsets=o)
+    z = z + bias if offs is None else torch.cat([z[p:q] + bias[s] for s, (p, q) in enumerate(zip(offs, offs[1:]))])
+    buf = torch.full((m + 1, n), 9.0, device="cuda")
+    c, kept = av.averis_fp8_gemm_act(a, b, bias=bias, act="relu", residual=res, save=True, offsets=o, out=buf[:m])
+    assert torch.equal(kept, z) and torch.equal(c, z.clamp(min=0.0) + res)
+    assert (buf[m:] == 9.0).all()
+    assert torch.equal(av.averis_fp8_gemm_act(a, b, bias=bias, offsets=o, out_dtype=F32), z)
