@@ -602,16 +602,19 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
     bool behind_next = false;
     const int64_t shift = (MODE == kF8RowSegs ? (int64_t)cur.seg * n : 0) + cur.n0;   // of the bias
     if constexpr (EPI != kEpiNone && F == 4) {
-      // The large tile's epilogue, of whole pieces only: 32 rows of the wavefront's at a
-      // time to LDS in fp32 (in the blocks of the second slot that its own loads fill;
+      // The large tile's epilogue, of whole eights of columns: 32 rows of the wavefront's at
+      // a time to LDS in fp32 (in the blocks of the second slot that its own loads fill;
       // piece p of row r at p ^ (p / 8 mod 2) ^ (r mod 8): neither the writes, of one piece
       // of neighbouring rows, nor the reads, of a row's even or odd pieces, meet a bank
-      // twice), and from there in steps of four rows, a lane eight columns, four steps'
-      // residual read ahead.  The steps are a loop: with every pass unrolled, as the small
-      // tile has them, the code outgrows the instruction cache and the accumulators leave
-      // their registers (16384 x 1024 x 4096, gelu and z kept, 158 us; this 111, the small
-      // tile 123, the product alone 76).
-      using T = std::conditional_t<OUT_BF16, uint16_t, float>;
+      // twice), and from there in steps of four rows, a lane eight columns.  A SIMD has this
+      // one wavefront, so nothing else runs under a wait of its own: four steps are formed
+      // together, while the next four's values come back from LDS and their residual from
+      // memory, with no branch between.  The steps are a loop: with every pass unrolled, as
+      // the small tile has them, the code outgrows the instruction cache and the accumulators
+      // leave their registers.  16384 x 1024 x 4096: bias 76 us (the product alone 76; 92 with
+      // one step at a time), gelu 86, z kept as well 95 (112; 268 MB written, 51 us at a
+      // copy's rate), residual 90 (127; the small tile 114); 16384 x 4096 x 1024 with a
+      // residual 59 (alone 54), 64 experts (32768 rows, 2048 -> 768) silu with z 70 (57).
       if (loads) {
 #pragma unroll
         for (int k = 0; k < FIRST0; ++k) first_load(k, nxt.nk);
@@ -619,24 +622,53 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
       const uint32_t to = (uint32_t)(uintptr_t)(lds_void*)(smem_f8 + SLOT + wave * 1024 + (ln & 31) / 2 * 4096 +
                                                            (ln & 1) * 512) + 16 * ((ln & 7) ^ (ln >> 5));
       const int k = ln & 15, rl = ln >> 4, col = wn * 128 + 8 * k;
-      // row 4 it + rl, pieces 2 k and 2 k + 1
+      // row 4 it + rl, pieces 2 k and 2 k + 1 (the odd steps' at ^ 64: r mod 8 = rl + 4 (it mod 2))
       const unsigned char* from = smem_f8 + SLOT + wave * 1024 + rl / 2 * 4096 + rl % 2 * 512 + 128 * (k >> 2);
-      const int sw = (k >> 2 & 1) ^ rl;   // (r mod 8 = rl + 4 (it mod 2))
+      const int sw = (k >> 2 & 1) ^ rl, lo0 = 16 * ((2 * k & 6) ^ sw), hi0 = 16 * ((2 * k & 6 | 1) ^ sw);
       const bool in = col < cur.cols;
       float bias[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) bias[x] = 0.0f;
       if (epi.bias && in) load_vector(epi.bias, epi.bias_bf16, shift + col, shift + col + 8, bias);
-      const int64_t row0e = (int64_t)cur.m0 + wm * 128 + rl;
-      const int rows_left = cur.rows - wm * 128 - rl;   // row r of the lane's is there: r < it
-      const T* res = static_cast<const T*>(epi.res) + row0e * epi.ldr + cur.n0 + col;
-      T* zp = static_cast<T*>(epi.z) + row0e * epi.ldz + cur.n0 + col;
-      T* cp = static_cast<T*>(c) + row0e * ldc + cur.n0 + col;
-      Eight<T> ahead[4];   // the next four steps' residual
-      auto load_res = [&](int r) __attribute__((always_inline)) {
+      // through descriptors of the tile's bytes: what lies past its rows and columns is
+      // neither read nor written, with no branch for it
+      auto tile_of = [&](const void* p, int64_t ld) __attribute__((always_inline)) {
+        const uint8_t* base = static_cast<const uint8_t*>(p) + ((int64_t)cur.m0 * ld + cur.n0) * ES;
+        return __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(scalar_base(base)), 0,
+            (int)((uint32_t)(cur.rows - 1) * (uint32_t)(ld * ES) + (uint32_t)(cur.cols * ES)), 0x00027000);
+      };
+      auto place = [&](int64_t ld) __attribute__((always_inline)) {
+        return ((uint32_t)(wm * 128 + rl) * (uint32_t)(ld * ES) + (uint32_t)(col * ES)) | (in ? 0u : 0x80000000u);
+      };
+      const __amdgpu_buffer_rsrc_t c_tile = tile_of(c, ldc), z_tile = tile_of(epi.z, epi.ldz);
+      const __amdgpu_buffer_rsrc_t r_tile = tile_of(RES ? epi.res : c, RES ? epi.ldr : ldc);
+      const uint32_t c_at = place(ldc), z_at = place(epi.ldz), r_at = RES ? place(epi.ldr) : 0;
+      const uint32_t c_step = 4 * (uint32_t)(ldc * ES), z_step = 4 * (uint32_t)(epi.ldz * ES);
+      const uint32_t r_step = RES ? 4 * (uint32_t)(epi.ldr * ES) : 0;
+      // (c streams, as the product's alone does; z, with it, is 5 us faster if it does not)
+      auto store8 = [&](auto streamc, const float (&f)[8], __amdgpu_buffer_rsrc_t tile,
+                        uint32_t at) __attribute__((always_inline)) {
+        if constexpr (OUT_BF16) {
+          const u32x4_t v = {bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
+                             bf16x2_rne(f[6], f[7])};
+          __builtin_amdgcn_raw_buffer_store_b128(v, tile, (int)at, 0, decltype(streamc)::value ? 2 : 0);
+        } else {
+          const f32x4_t lo = {f[0], f[1], f[2], f[3]}, hi = {f[4], f[5], f[6], f[7]};
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, lo), tile, (int)at, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, hi), tile, (int)(at + 16), 0, 0);
+        }
+      };
+      constexpr int U = 4;   // steps that are formed together
+      constexpr int RV = OUT_BF16 ? 1 : 2;
+      u32x4_t ahead[U][RV];   // the next steps' residual
+      auto load_res = [&](int it) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (in && r + 4 * u < rows_left) ahead[u].load(res + (int64_t)(r + 4 * u) * epi.ldr, 0, 8);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int x = 0; x < RV; ++x)
+            ahead[u][x] = __builtin_amdgcn_raw_buffer_load_b128(
+                r_tile, (int)(r_at + (uint32_t)(it + u) * r_step + 16 * x), 0, 0);
       };
       if constexpr (RES) load_res(0);
       each_step<F>([&](auto ic) __attribute__((always_inline)) {
@@ -650,50 +682,65 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
             asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(to ^ (32 * q) ^ (16 * (j & 1))), "a"(v), "i"(128 * j)
                          : "memory");
           }
+        f32x4_t next[U][2];
+        auto read = [&](int it) __attribute__((always_inline)) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int flip = 64 * ((it + u) & 1);
+            const unsigned char* p = from + (it + u) * 8192;
+            next[u][0] = *reinterpret_cast<const f32x4_t*>(p + (lo0 ^ flip));
+            next[u][1] = *reinterpret_cast<const f32x4_t*>(p + (hi0 ^ flip));
+          }
+        };
+        read(0);
 #pragma unroll
         for (int j = 0; j < F; ++j) zero(i, j);
-        auto step = [&](int it, const Eight<T>& add) __attribute__((always_inline)) {
-          const unsigned char* p = from + it * 8192;
-          const int x = sw ^ (4 * (it & 1));
-          const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(p + 16 * ((2 * k & 6) ^ x));
-          const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(p + 16 * ((2 * k & 6 | 1) ^ x));
-          const int64_t r = 32 * i + 4 * it;
-          if (!in || r >= rows_left) return;
-          float f[8];
+        auto steps = [&](auto act) __attribute__((always_inline)) {
+#pragma unroll 1
+          for (int it = 0; it < 8; it += U) {
+            float f[U][8];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            f[y] = lo[y] + bias[y];
-            f[4 + y] = hi[y] + bias[4 + y];
-          }
-          Eight<T> o;
-          if (epi.z) {
-            o.set(f);
-            o.store(zp + r * epi.ldz, 0, 8);
-          }
-          activate(f, epi.act);
-          if constexpr (RES) {
-            float g[8];
-            add.f32(g);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int y = 0; y < 8; ++y) f[y] += g[y];
+              for (int y = 0; y < 8; ++y) f[u][y] = next[u][y / 4][y % 4] + bias[y];
+            u32x4_t add[U][RV];
+            if constexpr (RES) {
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int x = 0; x < RV; ++x) add[u][x] = ahead[u][x];
+              if (i + 1 < F || it + U < 8) load_res(8 * i + it + U);
+            }
+            read((it + U) & 7);   // (behind the last ones the first again, unused)
+            __builtin_amdgcn_sched_barrier(0);
+            const uint32_t row = (uint32_t)(8 * i + it);
+            if (epi.z) {
+#pragma unroll
+              for (int u = 0; u < U; ++u) store8(step0, f[u], z_tile, z_at + (row + u) * z_step);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int y = 0; y < 8; ++y) f[u][y] = act(f[u][y]);
+            if constexpr (RES) {
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                  if constexpr (OUT_BF16)
+                    f[u][y] += __uint_as_float(y & 1 ? add[u][0][y / 2] & 0xFFFF0000u : add[u][0][y / 2] << 16);
+                  else
+                    f[u][y] += __uint_as_float(add[u][y / 4][y % 4]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) store8(step1, f[u], c_tile, c_at + (row + u) * c_step);
           }
-          o.set(f);
-          o.store(cp + r * ldc, 0, 8);
         };
-        if constexpr (RES) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            Eight<T> add[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) add[u] = ahead[u];
-            load_res(32 * i + 16 * h + 16);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) step(4 * h + u, add[u]);
-          }
-        } else {
-#pragma unroll 1
-          for (int it = 0; it < 8; ++it) step(it, ahead[0]);
-        }
+        if (epi.act == kActGelu) steps([](float z) { return act_gelu(z); });
+        else if (epi.act == kActSilu) steps([](float z) { return act_silu(z); });
+        else if (epi.act == kActRelu) steps([](float z) { return z < 0.0f ? 0.0f : z; });
+        else steps([](float z) { return z; });
       });
       __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the last values are out of their place
       if (loads) {
