@@ -697,8 +697,8 @@ averis_status_t averis_fp8_gemm_wgrad(const averis_fp8_t* xt, const averis_fp8_t
  * else h is written (it may be x or residual; y overlaps none of the three).  weight:
  * cols elements, F32 or BF16.  rstd: rows floats.  cols <= AVERIS_MAX_NORM_COLS,
  * rows <= 2^30; with out_t fewer than 2^23 tiles of 128 x 128.  eps >= 0; a row
- * whose mean square + eps is 0 gives NaN, as one with a value that is not
- * finite does. */
+ * whose mean square + eps is 0 gives NaN, as one with a NaN does; one with an
+ * infinity has rstd 0, NaN there and 0 elsewhere. */
 averis_status_t averis_rmsnorm(const void* x, averis_dtype_t dtype, int64_t rows, int64_t cols,
                                int64_t ldx, const void* residual, int64_t ldres,
                                const void* weight, averis_dtype_t wdtype, double eps, void* h,
