@@ -168,8 +168,9 @@ struct ActSrc {
 // i = t % 16) holds eight columns of rows r, r + 32, ..; a row's run is sixteen
 // lanes, so the plain copy comes from the registers.  The values go to LDS as
 // loaded; for the transposed copy a thread takes a column's (bf16: a column
-// pair's) run of rows from there, and the codes go back through LDS (bf16: in
-// the place of the values, 36 KB in all, four workgroups a CU) so that eight
+// pair's) run of rows from there, and the codes go back through LDS (in the
+// place of the values: bf16 34 KB in all, four workgroups a CU; fp32 66 KB, two,
+// 16384 x 2048 37.5 us, 44.6 with a place of their own and one) so that eight
 // lanes store a 128-byte row of the transposed copy.  Bound by memory: each
 // value is read once and each code written once.  Neighbouring workgroups take
 // neighbouring tiles of the same rows.  Workgroup w runs on die w mod 8; where
@@ -190,7 +191,7 @@ constexpr int kTileWaves = 8, kTileThreads = 64 * kTileWaves;
 
 template <typename T>
 constexpr size_t fp8_tile_lds() {
-  return (size_t)128 * 128 * sizeof(T) + (sizeof(T) == 2 ? 0 : 128 * 128) + kTileWaves * 64 * 4;
+  return (size_t)128 * 128 * sizeof(T) + kTileWaves * 64 * 4;
 }
 
 template <typename Src, bool TILE>
@@ -200,8 +201,8 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(Src source, int64_t r
   using T = typename Src::Type;
   extern __shared__ __attribute__((aligned(16))) unsigned char sm[];
   T* raw = reinterpret_cast<T*>(sm);   // [128][128]
-  // codes, [128 columns][128 rows]
-  unsigned char* ct = sm + (sizeof(T) == 2 ? 0 : 128 * 128 * sizeof(T));
+  // codes, [128 columns][128 rows], in the values' place
+  unsigned char* ct = sm;
   // maxima: of rows, or a column's (column pair's) part of each wavefront
   uint32_t* red = reinterpret_cast<uint32_t*>(sm + fp8_tile_lds<T>()) - kTileWaves * 64;
   // sums: a column's part of each wavefront
@@ -371,10 +372,15 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(Src source, int64_t r
     constexpr int PARTS = kTileWaves / 2, PR = 128 / PARTS;
     const int col = t & 127, part = t >> 7;
     const float* src = reinterpret_cast<const float*>(raw) + PR * part * 128 + col;
+    float x[PR];
+#pragma unroll
+    for (int q = 0; q < PR; ++q) x[q] = src[q * 128];
     uint32_t m = tile_max;
+    if constexpr (TILE) __syncthreads();   // the codes take the values' place
     if constexpr (!TILE) {
+#pragma unroll
       for (int q = 0; q < PR; ++q) {
-        const uint32_t z = __float_as_uint(src[q * 128]) & 0x7FFFFFFFu;
+        const uint32_t z = __float_as_uint(x[q]) & 0x7FFFFFFFu;
         m = z > m ? z : m;
       }
       red[part * 128 + col] = m;
@@ -388,8 +394,8 @@ __global__ __launch_bounds__(kTileThreads) void k_fp8_tile(Src source, int64_t r
       u32x4_t y;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float* z = src + (16 * h + 4 * q) * 128;
-        y[q] = f8_not_finite(m) ? kF8NanCodes : f8_codes4(z[0], z[128], z[256], z[384], byte);
+        const float* z = x + 16 * h + 4 * q;
+        y[q] = f8_not_finite(m) ? kF8NanCodes : f8_codes4(z[0], z[1], z[2], z[3], byte);
       }
       if (nr < 128) {
 #pragma unroll
