@@ -262,10 +262,13 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs
   }
 }
 
-// 64 columns and one segment a workgroup, its chunks divided in order among 16
-// wavefronts, whose sums are added in order.  Bound by latency: 1024 x 2048
-// 5.9 us, 320 chunks of 768 in 64 segments 4.6 us.
-constexpr int kSumWaves = 16;
+// 64 columns and kSumSegs segments a workgroup of 16 wavefronts.  A segment's chunks are
+// divided in order into sixteen parts, and the parts' sums added in order: by all
+// wavefronts, one such segment after the other, or by one of them where no part has
+// more than one chunk.  Bound by latency: 1024 x 2048 5.8 us, chunks of 768 columns in 64
+// segments 4.8, in 512 7.0 (a segment a workgroup, each looking for its own from the
+// first on, 5.1 and 47; sixteen 5.7 and 5.9).
+constexpr int kSumWaves = 16, kSumSegs = 8;
 
 __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __restrict__ part,
                                                                 int64_t rows, int64_t ch, int64_t cols,
@@ -273,30 +276,73 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __r
                                                                 int64_t chunks,
                                                                 float* __restrict__ out) {
   __shared__ float sh[kSumWaves][64];
-  const SegRange s = describe_segment(offs, nseg, rows, ch, blockIdx.y);
+  __shared__ int64_t before[kSumWaves], first[kSumSegs + 1];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  // within the array whatever the offsets hold (decreasing ones may claim rows twice)
-  const int64_t c0 = s.c0 < chunks ? s.c0 : chunks, c1 = s.c1 < chunks ? s.c1 : chunks;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane, n = c1 - c0;
-  const int64_t i0 = c0 + n * w / kSumWaves, i1 = c0 + n * (w + 1) / kSumWaves;
-  float v = 0.0f;
-  if (c < cols) {
-    int64_t i = i0;
-    for (; i + 8 <= i1; i += 8) {
-      float e[8];
+  const int seg0 = blockIdx.y * kSumSegs, segs = nseg - seg0 < kSumSegs ? nseg - seg0 : kSumSegs;
+  auto count = [&](int s) {
+    int64_t a = 0, e = rows;
+    if (offs) seg_bounds(offs, s, rows, a, e);
+    return (e - a + ch - 1) / ch;
+  };
+  // the chunks of the segments before, then of the workgroup's own
+  int64_t n = 0;
+  for (int s = threadIdx.x; s < seg0; s += 64 * kSumWaves) n += count(s);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) e[q] = part[(i + q) * cols + c];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v += e[q];
-    }
-    for (; i < i1; ++i) v += part[i * cols + c];
-  }
-  sh[w][lane] = v;
+  for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d, 64);
+  if (lane == 0) before[w] = n;
+  const int64_t own = w == 0 && lane < segs ? count(seg0 + lane) : 0;
   __syncthreads();
-  if (w == 0 && c < cols) {
+  if (w == 0) {
+    int64_t at = own;
 #pragma unroll
-    for (int q = 1; q < kSumWaves; ++q) v += sh[q][lane];
-    out[(int64_t)blockIdx.y * cols + c] = v;
+    for (int d = 1; d < kSumSegs; d <<= 1) {
+      const int64_t o = __shfl_up(at, d, 64);
+      if (lane >= d) at += o;
+    }
+    int64_t all = 0;
+    for (int q = 0; q < kSumWaves; ++q) all += before[q];
+    // within the array whatever the offsets hold (decreasing ones may claim rows twice)
+    at += all;
+    if (lane < kSumSegs) first[lane + 1] = at < chunks ? at : chunks;
+    if (lane == 0) first[0] = all < chunks ? all : chunks;
+  }
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  if (w < segs) {
+    const int64_t c0 = first[w], m = first[w + 1] - c0;
+    if (m <= kSumWaves && c < cols) {
+      float e[kSumWaves], v = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kSumWaves; ++q) e[q] = q < m ? part[(c0 + q) * cols + c] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < kSumWaves; ++q) v += e[q];
+      out[(int64_t)(seg0 + w) * cols + c] = v;
+    }
+  }
+  for (int s = 0; s < segs; ++s) {
+    const int64_t c0 = first[s], m = first[s + 1] - c0;
+    if (m <= kSumWaves) continue;
+    const int64_t i0 = c0 + m * w / kSumWaves, i1 = c0 + m * (w + 1) / kSumWaves;
+    float v = 0.0f;
+    if (c < cols) {
+      int64_t i = i0;
+      for (; i + 8 <= i1; i += 8) {
+        float e[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) e[q] = part[(i + q) * cols + c];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v += e[q];
+      }
+      for (; i < i1; ++i) v += part[i * cols + c];
+    }
+    sh[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && c < cols) {
+#pragma unroll
+      for (int q = 1; q < kSumWaves; ++q) v += sh[q][lane];
+      out[(int64_t)(seg0 + s) * cols + c] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -393,7 +439,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, bool bf16, int64_t rows, int6
 
 hipError_t launch_column_sums(const float* part, int64_t rows, int64_t ch, int64_t cols,
                               const int64_t* offs, int nseg, float* out, hipStream_t st) {
-  k_column_sums<<<dim3((unsigned)((cols + 63) / 64), (unsigned)nseg), 64 * kSumWaves, 0, st>>>(
+  k_column_sums<<<dim3((unsigned)((cols + 63) / 64), (unsigned)((nseg + kSumSegs - 1) / kSumSegs)), 64 * kSumWaves, 0, st>>>(
       part, rows, ch, cols, offs, nseg, chunk_upper_bound(rows, offs ? nseg : 1, ch), out);
   return hipGetLastError();
 }

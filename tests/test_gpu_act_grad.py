@@ -196,3 +196,33 @@ def test_offsets_past_32_bits():
     assert torch.equal(qt.codes[:, a:], pt.codes)
     ref = sum(dy[i:i + 20000].double().sum(0) for i in range(0, rows, 20000))
     assert torch.equal(db.double(), ref)                     # integers below 2^24: exact
+
+
+@pytest.mark.parametrize("nseg", [9, 300, 4096])
+def test_bias_gradient_of_many_segments(nseg):
+    """Segments of none, few and many runs of 128, more than one workgroup's; their sums are those of calls on
+    their own, bit for bit."""
+    rng = np.random.default_rng(nseg)
+    rows, cols = 9000, 70
+    cuts = np.sort(rng.integers(0, 3000, nseg - 1))
+    offs = [0] + cuts.tolist() + [rows]   # the last one of over 46 runs
+    dy = torch.randn(rows, cols, device="cuda")
+    z = torch.randn(rows, cols, device="cuda")
+    o = torch.tensor(offs, dtype=torch.int64, device="cuda")
+    _, _, db = av.averis_fp8_act_grad(dy, z=z, act="silu", plain=False, transposed=False, offsets=o)
+    filled = [s for s in range(nseg) if offs[s] < offs[s + 1]]
+    for s in sorted(set(rng.choice(filled, min(len(filled), 20)).tolist() + [filled[-1]])):
+        a, b = offs[s:s + 2]
+        assert torch.equal(db[s], av.averis_fp8_act_grad(dy[a:b], z=z[a:b], act="silu", plain=False, transposed=False)[2])
+    empty = [s for s in range(nseg) if offs[s] == offs[s + 1]]
+    assert (db[empty] == 0).all()
+    s64 = torch.sigmoid(z.double())
+    d64 = dy.double() * s64 * (1 + z.double() * (1 - s64))
+    ref = torch.zeros(nseg, cols, dtype=torch.float64, device="cuda")
+    which = torch.from_numpy(np.searchsorted(np.array(offs[1:]), np.arange(rows), side="right")).cuda()
+    ref.index_add_(0, which, d64)
+    mag = torch.zeros_like(ref).index_add_(0, which, d64.abs())
+    # a sum of n fp32 terms, each off by its slope's 2^-17 and its own rounding
+    n = torch.tensor(np.diff(np.array(offs)), device="cuda").double()[:, None]
+    lim = (n + 1) * U * mag + 2.0 ** -17 * torch.zeros_like(ref).index_add_(0, which, dy.double().abs())
+    assert ((db.double() - ref).abs() <= lim + 1e-30).all()
