@@ -834,6 +834,15 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
       if constexpr (RES) load_res(F8Step<0>{});
       each_step<OUT_PASSES>([&](auto pc) __attribute__((always_inline)) {
         constexpr int P = decltype(pc)::value, i = P / PASSES, p = P % PASSES;
+        // none of these rows in a part of a tile: nothing to form (16 rows among 64 experts, 2048 ->
+        // 768, 18.3 -> 16.9 us)
+        if (wm * 32 * F + 32 * i >= cur.rows) {
+          clear(pc);
+          if constexpr (P > 0 && p == 0) {
+            if (wm * 32 * F + 32 * (i - 1) < cur.rows) store(cb, ldc, F8Step<P - 1>{}, vc);
+          }
+          return;
+        }
         f32x4_t y[FPP][4];
 #pragma unroll
         for (int f = 0; f < FPP; ++f)
@@ -869,8 +878,9 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      store(cb, ldc, F8Step<OUT_PASSES - 1>{}, vc);
-      behind_next = loads && whole;
+      const bool all = wm * 32 * F + 32 * (F - 1) < cur.rows;
+      if (all) store(cb, ldc, F8Step<OUT_PASSES - 1>{}, vc);
+      behind_next = loads && whole && all;   // (every pass's stores are out)
     } else if (pieces) {
       const uint32_t ldb = (uint32_t)(ldc * ES);
       // below 2^31: a lane past the columns goes to 2^31 and on
