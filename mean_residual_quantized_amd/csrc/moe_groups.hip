@@ -542,17 +542,13 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
     x[o] = id[o] >= 0 ? x[o] : 0.0f;
     part += x[o];
   }
-  float inv = a.scale;
-  if (a.renorm) {
-    const float sum = group_sum<G>(part);
-    inv = sum == 0.0f ? 0.0f : a.scale / sum;
-  }
+  const float sum = a.renorm ? group_sum<G>(part) : 1.0f;
 #pragma unroll
   for (int o = 0; o < KO; ++o) {
     const int j = o * G + g;
     if (live && j < a.topk) {
       a.ids[t * a.topk + j] = id[o];
-      a.weights[t * a.topk + j] = id[o] < 0 ? 0.0f : x[o] * inv;
+      a.weights[t * a.topk + j] = id[o] < 0 || sum == 0.0f ? 0.0f : x[o] / sum * a.scale;
     }
   }
 }
@@ -606,17 +602,21 @@ __global__ __launch_bounds__(256) void k_route_groups_grad(const T* logits, Rout
       x[o] = id[o] >= 0 ? x[o] : 0.0f;
       d[o] = id[o] >= 0 ? d[o] : 0.0f;
       part += x[o];
-      dot = __builtin_fmaf(x[o], d[o], dot);
     }
-    float inv = 1.0f, mean = 0.0f;
+    float mean = 0.0f;
     if (a.renorm) {
+      // divided, not multiplied by 1 / sum: one expert alone has the weight 1, and no gradient
       const float sum = group_sum<G>(part);
-      inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      mean = group_sum<G>(dot) * inv;
+#pragma unroll
+      for (int o = 0; o < KO; ++o) {
+        x[o] = sum == 0.0f ? 0.0f : x[o] / sum;
+        dot = __builtin_fmaf(x[o], d[o], dot);
+      }
+      mean = group_sum<G>(dot);
     }
 #pragma unroll
     for (int o = 0; o < KO; ++o)
-      if (id[o] >= 0) img[tok][id[o]] = (d[o] - mean) * (x[o] * inv) * rest[o];
+      if (id[o] >= 0) img[tok][id[o]] = (d[o] - mean) * x[o] * rest[o];
     lds_order();
   }
   float f[V];

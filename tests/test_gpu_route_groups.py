@@ -227,3 +227,18 @@ def test_more_tokens_than_one_launch_takes():
     for i, e in enumerate(rid[:, 0]):
         want[i, e] = s[i, e] * (1 - s[i, e]) * float(rw[i, 0])
     assert ((d[-300:].double().cpu() - want).abs() <= 2.0 ** -8 * want + 1e-38).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_expert_alone(dtype, score):
+    """Renormalised, the weight of a token's only expert is the scale, and its logit has no gradient: exactly."""
+    for t, e, k in ((1000, 40, 1), (777, 256, 1), (500, 12, 4)):
+        l = (6 * torch.randn(t, e, device="cuda")).to(dtype)
+        if k > 1:   # one open expert
+            l.masked_fill_(torch.arange(e, device="cuda") != torch.randint(0, e, (t, 1), device="cuda"), float("-inf"))
+        bias = torch.randn(e, device="cuda")
+        ids, w = av.averis_moe_route_groups(l, k, bias=bias, score=score, scale=2.5)
+        assert (w[:, 0] == 2.5).all() and (ids[:, 0] >= 0).all() and (ids[:, 1:] == -1).all() and (w[:, 1:] == 0).all()
+        d = av.averis_moe_route_groups_grad(l, ids, torch.randn(t, k, device="cuda"), score=score, scale=2.5)
+        assert (d == 0).all()
