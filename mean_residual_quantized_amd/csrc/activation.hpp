@@ -23,16 +23,17 @@ __device__ __forceinline__ float act_gelu(float z) {
   return z * act_sigmoid(z * __builtin_fmaf(kGeluB * kActLog2e, z * z, kGeluA * kActLog2e));
 }
 
-// d/dz of z s(u): s + z s (1 - s) du/dz.  Past |z| = 100 it is its limit, 1 or 0, and the products of its
-// terms might overflow: z is held there (where it is NaN, s is).
+// d/dz of z s(u): s + s (1 - s) z du/dz, in this order (gelu of 16384 x 4096 normal z in bf16: every code
+// as fp64 gives it; with z s first 790 are a step off).  Past |z| = 100 it is its limit, 1 or 0, and the
+// products of its terms might overflow: z is held there (where it is NaN, s is).
 __device__ __forceinline__ float act_silu_slope(float z) {
   const float s = act_sigmoid(kActLog2e * z), h = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f);
-  return __builtin_fmaf(h * s, 1.0f - s, s);
+  return __builtin_fmaf(s * (1.0f - s), h, s);
 }
 __device__ __forceinline__ float act_gelu_slope(float z) {
   const float h = __builtin_amdgcn_fmed3f(z, -100.0f, 100.0f), q = h * h;
   const float s = act_sigmoid(z * __builtin_fmaf(kGeluB * kActLog2e, q, kGeluA * kActLog2e));
-  return __builtin_fmaf(h * s * (1.0f - s), __builtin_fmaf(3.0f * kGeluB, q, kGeluA), s);
+  return __builtin_fmaf(s * (1.0f - s), h * __builtin_fmaf(3.0f * kGeluB, q, kGeluA), s);
 }
 
 }  // namespace averis
