@@ -612,7 +612,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
       // memory, with no branch between.  The steps are a loop: with every pass unrolled, as
       // the small tile has them, the code outgrows the instruction cache and the accumulators
       // leave their registers.  16384 x 1024 x 4096: bias 76 us (the product alone 76; 92 with
-      // one step at a time), gelu 86, z kept as well 95 (112; 268 MB written, 51 us at a
+      // one step at a time), gelu 86, z kept as well 101 (112; 268 MB written, 51 us at a
       // copy's rate), residual 90 (127; the small tile 114); 16384 x 4096 x 1024 with a
       // residual 59 (alone 54), 64 experts (32768 rows, 2048 -> 768) silu with z 70 (57).
       if (loads) {
@@ -646,13 +646,14 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
       const uint32_t c_at = place(ldc), z_at = place(epi.ldz), r_at = RES ? place(epi.ldr) : 0;
       const uint32_t c_step = 4 * (uint32_t)(ldc * ES), z_step = 4 * (uint32_t)(epi.ldz * ES);
       const uint32_t r_step = RES ? 4 * (uint32_t)(epi.ldr * ES) : 0;
-      // (c streams, as the product's alone does; z, with it, is 5 us faster if it does not)
-      auto store8 = [&](auto streamc, const float (&f)[8], __amdgpu_buffer_rsrc_t tile,
+      // (bf16 streams, as the product's alone does: gelu with z 103 us, 115 if neither does, where a
+      // step's activations are in memory; a program that writes the same z again has it in the last-level cache)
+      auto store8 = [&](const float (&f)[8], __amdgpu_buffer_rsrc_t tile,
                         uint32_t at) __attribute__((always_inline)) {
         if constexpr (OUT_BF16) {
           const u32x4_t v = {bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]),
                              bf16x2_rne(f[6], f[7])};
-          __builtin_amdgcn_raw_buffer_store_b128(v, tile, (int)at, 0, decltype(streamc)::value ? 2 : 0);
+          __builtin_amdgcn_raw_buffer_store_b128(v, tile, (int)at, 0, 2);
         } else {
           const f32x4_t lo = {f[0], f[1], f[2], f[3]}, hi = {f[4], f[5], f[6], f[7]};
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, lo), tile, (int)at, 0, 0);
@@ -716,7 +717,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
             const uint32_t row = (uint32_t)(8 * i + it);
             if (epi.z) {
 #pragma unroll
-              for (int u = 0; u < U; ++u) store8(step0, f[u], z_tile, z_at + (row + u) * z_step);
+              for (int u = 0; u < U; ++u) store8(f[u], z_tile, z_at + (row + u) * z_step);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -734,7 +735,7 @@ __global__ __launch_bounds__(kF8Threads, F == 4 ? 1 : 2) void k_gemm_f8(
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) store8(step1, f[u], c_tile, c_at + (row + u) * c_step);
+            for (int u = 0; u < U; ++u) store8(f[u], c_tile, c_at + (row + u) * c_step);
           }
         };
         if (epi.act == kActGelu) steps([](float z) { return act_gelu(z); });

@@ -75,7 +75,7 @@ __device__ __forceinline__ int64_t piece_at(int lane, int g, int i) {
 
 // W wavefronts hold a row, I pieces of eight elements a lane: the row is read
 // once, into registers.  Bound by memory: 32768 x 2048 bf16 with a residual and
-// codes 79 us (470 MB, 5.9 TB/s; a copy reaches 5.3), 2999 x 1000 fp32 9 us
+// codes 79 us (470 MB, 5.9 TB/s; a copy reaches 5.3), 2999 x 1000 fp32 8 us
 // (latency), 16 x 2048 4.2 us.  The transposed copy is k_fp8_tile's, from h and f:
 // 38 us more (201 MB): its runs go across 128 rows, more than a workgroup holds.
 template <typename T, int W, int I, bool EIGHTS>
