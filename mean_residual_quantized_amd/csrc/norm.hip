@@ -265,7 +265,7 @@ __global__ __launch_bounds__(W > 4 ? 64 * W : 256) void k_norm_grad(NormGradArgs
 // 64 columns and kSumSegs segments a workgroup of 16 wavefronts.  A segment's chunks are
 // divided in order into sixteen parts, and the parts' sums added in order: by all
 // wavefronts, one such segment after the other, or by one of them where no part has
-// more than one chunk.  Bound by latency: 1024 x 2048 5.8 us, chunks of 768 columns in 64
+// more than one chunk.  Bound by latency: 1024 x 2048 6.5 us, chunks of 768 columns in 64
 // segments 4.8, in 512 7.0 (a segment a workgroup, each looking for its own from the
 // first on, 5.1 and 47; sixteen 5.7 and 5.9).
 constexpr int kSumWaves = 16, kSumSegs = 8;
@@ -280,10 +280,38 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __r
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int seg0 = blockIdx.y * kSumSegs, segs = nseg - seg0 < kSumSegs ? nseg - seg0 : kSumSegs;
   auto count = [&](int s) {
-    int64_t a = 0, e = rows;
-    if (offs) seg_bounds(offs, s, rows, a, e);
+    int64_t a, e;
+    seg_bounds(offs, s, rows, a, e);
     return (e - a + ch - 1) / ch;
   };
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  // by all wavefronts
+  auto together = [&](int seg, int64_t c0, int64_t m) __attribute__((always_inline)) {
+    const int64_t i0 = c0 + m * w / kSumWaves, i1 = c0 + m * (w + 1) / kSumWaves;
+    float v = 0.0f;
+    if (c < cols) {
+      int64_t i = i0;
+      for (; i + 8 <= i1; i += 8) {
+        float e[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) e[q] = part[(i + q) * cols + c];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v += e[q];
+      }
+      for (; i < i1; ++i) v += part[i * cols + c];
+    }
+    sh[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && c < cols) {
+#pragma unroll
+      for (int q = 1; q < kSumWaves; ++q) v += sh[q][lane];
+      out[(int64_t)seg * cols + c] = v;
+    }
+  };
+  if (!offs) {
+    together(0, 0, (rows + ch - 1) / ch);
+    return;
+  }
   // the chunks of the segments before, then of the workgroup's own
   int64_t n = 0;
   for (int s = threadIdx.x; s < seg0; s += 64 * kSumWaves) n += count(s);
@@ -307,7 +335,6 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __r
     if (lane == 0) first[0] = all < chunks ? all : chunks;
   }
   __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   if (w < segs) {
     const int64_t c0 = first[w], m = first[w + 1] - c0;
     if (m <= kSumWaves && c < cols) {
@@ -322,26 +349,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void k_column_sums(const float* __r
   for (int s = 0; s < segs; ++s) {
     const int64_t c0 = first[s], m = first[s + 1] - c0;
     if (m <= kSumWaves) continue;
-    const int64_t i0 = c0 + m * w / kSumWaves, i1 = c0 + m * (w + 1) / kSumWaves;
-    float v = 0.0f;
-    if (c < cols) {
-      int64_t i = i0;
-      for (; i + 8 <= i1; i += 8) {
-        float e[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) e[q] = part[(i + q) * cols + c];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v += e[q];
-      }
-      for (; i < i1; ++i) v += part[i * cols + c];
-    }
-    sh[w][lane] = v;
-    __syncthreads();
-    if (w == 0 && c < cols) {
-#pragma unroll
-      for (int q = 1; q < kSumWaves; ++q) v += sh[q][lane];
-      out[(int64_t)(seg0 + s) * cols + c] = v;
-    }
+    together(seg0 + s, c0, m);
     __syncthreads();
   }
 }
