@@ -83,8 +83,8 @@ __device__ __forceinline__ void sort_down(uint32_t* s) {
           }
 }
 
-// What a token's lanes keep in LDS for one another: the two (three) largest of
-// each lane, then each group's score (G lanes hold at most G groups), and the chosen.
+// What a token's lanes keep in LDS for one another: the two largest of each lane,
+// then each group's score (G lanes hold at most G groups), and the chosen.
 template <int G, int V>
 struct alignas(16) RouteShare {
   static constexpr int kTokens = 256 / G;
@@ -322,7 +322,7 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
     constexpr uint32_t kCut = 63;
     uint32_t* pairs = reinterpret_cast<uint32_t*>(sh.pair[tok]);
     uint32_t* scores = reinterpret_cast<uint32_t*>(sh.score[tok]);
-    *reinterpret_cast<u32x4_t*>(pairs + 4 * g) = u32x4_t{s[0], s[1], s[2], 0u};
+    *reinterpret_cast<u32x2_t*>(pairs + 4 * g) = u32x2_t{s[0], s[1]};
     if (g < 4) sh.edge[tok][g] = 0u;
     if constexpr (G < 4) {
 #pragma unroll
@@ -378,27 +378,24 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
       }
     }
     if (__builtin_expect(__ballot(open) != 0, 0)) {
-      // the groups' exact scores, of the two that lead each by a margin to its third
+      // the groups' exact scores, of the two largest keys each
       all = open && !by_logit && a.score == kScoreSoftmax;
+      uint32_t ref = 0u;   // the key of the last that counts
+      int e1 = -1, e2 = -1;
       if (g < a.groups) {
-        uint32_t k1 = 0u, k2 = 0u, k3 = 0u;
-        int e1 = -1, e2 = -1, e3 = -1;
+        uint32_t k1 = 0u, k2 = 0u;
         for (int i = 0; i < a.group_lanes; ++i) {
-          const u32x4_t o = *reinterpret_cast<const u32x4_t*>(pairs + 4 * (g * a.group_lanes + i));
+          const u32x2_t o = *reinterpret_cast<const u32x2_t*>(pairs + 4 * (g * a.group_lanes + i));
 #pragma unroll
-          for (int q = 0; q < 3; ++q) {
+          for (int q = 0; q < 2; ++q) {
             const uint32_t k = o[q];
             if (k < kOpen) continue;
             const int e = g * a.gsize + i * V + (int)(kPlace - (k & kPlace));
             if (k > k1) {
-              k3 = k2, e3 = e2;
               k2 = k1, e2 = e1;
               k1 = k, e1 = e;
             } else if (k > k2) {
-              k3 = k2, e3 = e2;
               k2 = k, e2 = e;
-            } else if (k > k3) {
-              k3 = k, e3 = e;
             }
           }
         }
@@ -406,13 +403,27 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
         const double y = exact(e2);
         if (a.group_top == 2) {
           if (e2 >= 0) x += y;
-          all |= open && near(k2, k3) && !same(e2, e3);
+          ref = k2;
         } else {
           x = y > x ? y : x;
-          all |= open && near(k1, k3) && !same(e1, e3);
+          ref = k1;
         }
         all |= open && x != x;
         sh.score[tok][g] = x;
+      }
+      // Whether another of the group's may be above that one: every key is looked at, for before one a
+      // little larger there can be any number of equal ones, whose indexes are lower
+      const int from = (lane & ~(G - 1)) + group;
+      ref = (uint32_t)__shfl((int)ref, from, 64);
+      e1 = __shfl(e1, from, 64);
+      e2 = __shfl(e2, from, 64);
+      const int own = a.group_top == 2 ? e2 : e1;
+      if (open && near(ref, s[0])) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = at0.first + (int)(kPlace - (s[v] & kPlace));
+          if (near(ref, s[v]) && e != e1 && e != e2) all |= !same(own, e);
+        }
       }
       lds_order();
       if (open) {

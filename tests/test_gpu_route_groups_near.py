@@ -1,0 +1,74 @@
+"""Grouped routing where scores lie close together, a token a call.
+
+In a batch one token whose scores only fp64 tells apart has its neighbours'
+choices made in fp64 too; alone, each way of settling a near choice is seen.
+The choice is determined by the float64 oracle: its scores and the kernel's
+differ by 2^-50 at most, and no two here are so near but equal ones."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block
+from mean_residual_quantized_amd import averis as av
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    av.lib()
+
+
+def check_alone(l, k, bias=None, **kw):
+    """Each token's experts in a call of its own, and all tokens' in one, against the oracle."""
+    want, _ = block.route_groups(l.double().numpy(), k, bias, **kw)
+    lg = l.cuda()
+    bg = None if bias is None else torch.from_numpy(bias).cuda()
+    got = torch.cat([av.averis_moe_route_groups(lg[i:i + 1], k, bias=bg, **kw)[0] for i in range(len(l))])
+    np.testing.assert_array_equal(got.cpu().numpy(), want)
+    np.testing.assert_array_equal(av.averis_moe_route_groups(lg, k, bias=bg, **kw)[0].cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_larger_score_behind_equal_ones(dtype):
+    """Three equal experts lead their group; the fourth is larger by less than fp32 tells."""
+    l = torch.full((1, 16), -5.0)
+    l[0, :4] = torch.tensor([18.0, 18.0, 18.0, 18.25])
+    l[0, 8:11] = torch.tensor([18.125, 18.0, 18.0])
+    check_alone(l.to(dtype), 3, groups=2, topk_groups=1)
+    check_alone(l.to(dtype), 3, np.full(16, 0.25, np.float32), groups=2, topk_groups=1, group_top=1)
+    if dtype == F32:
+        u = 2.0 ** -23
+        l[0, :4], l[0, 8:11] = torch.tensor([1.0, 1.0, 1.0, 1.0 + 2 * u]), torch.tensor([1.0 + u, 1.0, 1.0])
+        for score in ("sigmoid", "softmax"):
+            check_alone(l, 3, score=score, groups=2, topk_groups=1, group_top=1)
+
+
+NEAR = [(8, 3, 2, 1), (64, 8, 8, 4), (160, 6, 8, 3), (600, 8, 4, 2), (1000, 12, 8, 2)]
+
+
+@pytest.mark.parametrize("e,k,groups,keep", NEAR)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_mostly_equal_scores(e, k, groups, keep, dtype):
+    """Most experts of a token alike, a few larger by less than an fp32 step of the score."""
+    rng = np.random.default_rng([e, k])
+    few = lambda p: torch.from_numpy(rng.choice(3, size=(60, e), p=[1 - p, p / 2, p / 2]).astype(np.float32))
+    equal = np.full(e, 0.25, np.float32)
+    for p in (0.02, 0.2):
+        n = few(p)
+        high = (18.0 + 0.125 * n).to(dtype)                 # sigmoids of nearly 1
+        low = (-30.0 + 0.125 * n).to(dtype)                 # of nearly 0, beside a bias
+        for top in (1, 2):
+            check_alone(high, k, groups=groups, topk_groups=keep, group_top=top)
+            check_alone(high, k, equal, groups=groups, topk_groups=keep, group_top=top)
+            check_alone(low, k, equal, groups=groups, topk_groups=keep, group_top=top)
+            check_alone(low, k, equal, score="softmax", groups=groups, topk_groups=keep, group_top=top)
+        if dtype == F32:                                    # by the logits themselves, a few steps apart
+            check_alone(1.0 + 2.0 ** -23 * n, k, groups=groups, topk_groups=keep, group_top=1)
+            check_alone(-1.0 + 2.0 ** -24 * n, k, score="softmax", groups=groups, topk_groups=keep, group_top=1)
+            check_alone(1.0 + 2.0 ** -23 * n, k)
