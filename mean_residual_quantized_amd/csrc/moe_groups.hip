@@ -296,9 +296,10 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
   }
   // A key's value, and whether one lies so near below another that their order is open.
   // Errors: a score's is at most 2^-20 (exp2 and the reciprocal 1 ulp each, the exponent |l| 2^-24, the
-  // sum of a softmax 2^-20), without a bias 2^-16 of it; a key's cut bits 2^-18 of the value.
+  // sum of a softmax 2^-20), without a bias 2^-16 of it and 2^-126 (exp2 and the reciprocal give 0 below
+  // the normal numbers); a key's cut bits 2^-18 of the value.
   auto value = [](uint32_t k, uint32_t cut) __attribute__((always_inline)) { return f32_from_ordered(k & ~cut); };
-  const float rel = a.bias ? 0x1p-17f : 0x1p-15f, abs_ = a.bias ? 0x1p-18f : 0.0f;
+  const float rel = a.bias ? 0x1p-17f : 0x1p-15f, abs_ = a.bias ? 0x1p-18f : 0x1p-125f;
   auto near = [&](uint32_t hi, uint32_t lo) __attribute__((always_inline)) {
     if (hi < kOpen || lo < kOpen) return false;
     if (by_logit) return sizeof(T) == 4 && (hi & ~kPlace) == (lo & ~kPlace);

@@ -72,3 +72,28 @@ def test_mostly_equal_scores(e, k, groups, keep, dtype):
             check_alone(1.0 + 2.0 ** -23 * n, k, groups=groups, topk_groups=keep, group_top=1)
             check_alone(-1.0 + 2.0 ** -24 * n, k, score="softmax", groups=groups, topk_groups=keep, group_top=1)
             check_alone(1.0 + 2.0 ** -23 * n, k)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_group_scores_around_the_smallest_normal_number(dtype):
+    """Sums of two scores of which fp32 has none, one or both: e^-87.34 is 2^-126."""
+    l = torch.full((1, 8), -200.0)
+    l[0, :2] = torch.tensor([-87.5, -87.5]) if dtype == BF16 else torch.tensor([-87.4, -87.4])
+    l[0, 4] = -87.0 if dtype == BF16 else -87.3
+    check_alone(l.to(dtype), 2, groups=2, topk_groups=1)
+    three = torch.cat([torch.tensor([[0.0, -1.0, -300.0, -300.0]]), l], 1)   # the same below the largest logit
+    check_alone(three.to(dtype), 4, score="softmax", groups=3, topk_groups=2, renorm=False)
+
+
+@pytest.mark.parametrize("e,k,groups,keep", NEAR)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scores_around_the_smallest_normal_number(e, k, groups, keep, dtype):
+    rng = np.random.default_rng([e, k, 1])
+    step = 0.5 if dtype == BF16 else 2.0 ** -13
+    n = rng.integers(-3 if dtype == BF16 else -6000, 2 if dtype == BF16 else 4000, (80, e))
+    l = torch.from_numpy((-87.0 + step * n).astype(np.float32))
+    l[::2][torch.from_numpy(rng.random((40, e)) < 0.8)] = -200.0
+    check_alone(l.to(dtype), k, groups=groups, topk_groups=keep)
+    top = l.clone()
+    top[:, 0] = 0.0
+    check_alone(top.to(dtype), k, score="softmax", groups=groups, topk_groups=keep)
