@@ -92,8 +92,7 @@ struct alignas(16) RouteShare {
   static constexpr int kSlots = G * V < kMaxTopk ? G * V : kMaxTopk;
   double pair[kTokens][G][2];          // (the fp32 keys in their place)
   double score[kTokens][kGroups];
-  float size[kTokens][kGroups];        // |first| + |second|
-  uint32_t edge[kTokens][4];           // score and size of the last group that stays, of the first that does not
+  uint32_t edge[kTokens][2];           // scores of the last group that stays, of the first that does not
   uint32_t key[kTokens][kSlots + 1];   // (the next one behind them)
   int32_t id[kTokens][kSlots + 1];
 };
@@ -324,12 +323,10 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
     uint32_t* pairs = reinterpret_cast<uint32_t*>(sh.pair[tok]);
     uint32_t* scores = reinterpret_cast<uint32_t*>(sh.score[tok]);
     *reinterpret_cast<u32x2_t*>(pairs + 4 * g) = u32x2_t{s[0], s[1]};
-    if (g < 4) sh.edge[tok][g] = 0u;
-    if constexpr (G < 4) {
-#pragma unroll
-      for (int i = G; i < 4; ++i) sh.edge[tok][i] = 0u;
-    }
+    if (g < 2) sh.edge[tok][g] = 0u;
+    if constexpr (G == 1) sh.edge[tok][1] = 0u;
     lds_order();
+    float size = 0.0f;   // |first| + |second|
     const int padded = (a.groups + 3) & ~3;
     for (int j = g; j < padded; j += G) {
       uint32_t k1 = 0u, k2 = 0u, score = 0u;
@@ -340,17 +337,20 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
         }
       }
       if (k1 >= kOpen) {
-        float x = value(k1, kPlace), size = __builtin_fabsf(x);
+        float x = value(k1, kPlace);
+        size = __builtin_fabsf(x);
         if (a.group_top == 2 && k2 >= kOpen) {
           const float y = value(k2, kPlace);
           x += y;
           size += __builtin_fabsf(y);
         }
-        sh.size[tok][j] = size;
         score = ((x != x ? 0xFFFFFFFFu : f32_ordered(x + 0.0f)) & ~kCut) | (kCut - j);
       }
       scores[j] = score;
     }
+    // With a bias the errors go by the largest parts of any group: one further from the edge, whose parts
+    // cancel, may be known less well than the two beside it
+    if (a.bias) size = group_fmax<G>(size);
     lds_order();
     const int group = at0.group < a.groups ? at0.group : 0;
     const uint32_t mine = scores[group];
@@ -362,20 +362,16 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
     }
     bool stays = rank < a.topk_groups && mine != 0u;
     if (at0.many > 0 && at0.first == at0.group * a.gsize && mine != 0u &&
-        (rank == a.topk_groups - 1 || rank == a.topk_groups)) {
-      const int i = rank == a.topk_groups ? 2 : 0;
-      sh.edge[tok][i] = mine;
-      sh.edge[tok][i + 1] = __float_as_uint(sh.size[tok][group]);
-    }
+        (rank == a.topk_groups - 1 || rank == a.topk_groups))
+      sh.edge[tok][rank == a.topk_groups ? 1 : 0] = mine;
     lds_order();
-    const uint32_t hi = sh.edge[tok][0], lo = sh.edge[tok][2];
+    const uint32_t hi = sh.edge[tok][0], lo = sh.edge[tok][1];
     if (hi != 0u && lo != 0u) {
       if (by_logit) {
         open = sizeof(T) == 4 && (hi & ~kCut) == (lo & ~kCut);
       } else {
         const float x = value(hi, kCut), y = value(lo, kCut);
-        const float size = __builtin_fmaxf(__uint_as_float(sh.edge[tok][1]), __uint_as_float(sh.edge[tok][3]));
-        open = x - y <= 2.0f * (rel * size + abs_) + 0x1p-16f * __builtin_fabsf(x);
+        open = x - y <= 2.0f * (rel * (a.bias ? size : x) + abs_) + 0x1p-16f * __builtin_fabsf(x);
       }
     }
     if (__builtin_expect(__ballot(open) != 0, 0)) {

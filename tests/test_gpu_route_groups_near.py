@@ -97,3 +97,22 @@ def test_scores_around_the_smallest_normal_number(e, k, groups, keep, dtype):
     top = l.clone()
     top[:, 0] = 0.0
     check_alone(top.to(dtype), k, score="softmax", groups=groups, topk_groups=keep)
+
+
+def test_group_scores_of_large_parts():
+    """Two large parts that cancel: their sum is known less well than those of the groups beside it."""
+    l = torch.full((1, 12), -8.0)
+    l[0, [0, 1, 4, 5, 8, 9]] = 0.0
+    bias = np.full(12, -2000.0, np.float32)
+    bias[[0, 1]], bias[[4, 5]], bias[[8, 9]] = (1000.30005, -1000.29999), (2.5e-5, 0.0), (-1.42e-4, 0.0)
+    check_alone(l, 1, bias, groups=3, topk_groups=1)
+    rng = np.random.default_rng(5)
+    for _ in range(200):
+        b = np.zeros(12, np.float32)
+        b[0], b[1] = 1000.3 + 1e-3 * rng.random(), -1000.3
+        b[4] = 2e-4 * rng.random()
+        b[8] = b[4] - 1e-4 * (1 + rng.random())
+        b[[2, 3, 6, 7, 10, 11]] = -2000.0
+        order = rng.permutation(3)
+        b, li = b.reshape(3, 4)[order].ravel(), l.reshape(3, 4)[torch.from_numpy(order)].reshape(1, 12)
+        check_alone(li, 2, b, groups=3, topk_groups=1)
