@@ -371,7 +371,8 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
         open = sizeof(T) == 4 && (hi & ~kCut) == (lo & ~kCut);
       } else {
         const float x = value(hi, kCut), y = value(lo, kCut);
-        open = x - y <= 2.0f * (rel * (a.bias ? size : x) + abs_) + 0x1p-16f * __builtin_fabsf(x);
+        // (not >, for two sums past fp32's range differ by NaN)
+        open = !(x - y > 2.0f * (rel * (a.bias ? size : x) + abs_) + 0x1p-16f * __builtin_fabsf(x));
       }
     }
     if (__builtin_expect(__ballot(open) != 0, 0)) {

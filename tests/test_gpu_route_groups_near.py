@@ -116,3 +116,14 @@ def test_group_scores_of_large_parts():
         order = rng.permutation(3)
         b, li = b.reshape(3, 4)[order].ravel(), l.reshape(3, 4)[torch.from_numpy(order)].reshape(1, 12)
         check_alone(li, 2, b, groups=3, topk_groups=1)
+
+
+def test_group_scores_past_the_largest_number():
+    """Sums of two that fp32 does not hold, on either side."""
+    l = torch.zeros(1, 8)
+    bias = np.array([3e38, 1e38, 0, 0, 3e38, 2e38, 0, 0], np.float32)
+    check_alone(l, 1, bias, groups=2, topk_groups=1)
+    bias = np.array([-1e38, -3e38, -3.3e38, -3.3e38, -1e38, -2.9e38, -3.3e38, -3.3e38], np.float32)
+    check_alone(l, 1, bias, groups=2, topk_groups=1)
+    bias = np.array([3e38, 1e38, 3e38, 2e38, 3e38, 1.5e38, 1.0, 2.0], np.float32)
+    check_alone(l, 4, bias, groups=4, topk_groups=2)
