@@ -432,7 +432,8 @@ hipError_t launch_norm_grad(const NormGradArgs& a, bool bf16, int64_t rows, int6
     grad_shape(cols, [&](auto wc, auto ic) {
       constexpr int W = decltype(wc)::value, I = decltype(ic)::value, PER = W > 4 ? 1 : 4 / W;
       const dim3 grid((unsigned)blocks), block(W > 4 ? 64 * W : 256);
-      const size_t lds = part && PER > 1 ? (size_t)PER * cols * 4 : 0;   // at most 32 KB
+      static_assert(PER == 1 || PER * 512 * W * I * 4 <= 8192, "LDS for four workgroups a CU and more");
+      const size_t lds = part && PER > 1 ? (size_t)PER * cols * 4 : 0;
       const float inv = (float)(1.0 / (double)cols);
       of_kind(bf16, cols, [&](auto t, auto ec) {
         k_norm_grad<decltype(t), W, I, decltype(ec)::value><<<grid, block, lds, st>>>(a, rows, cols, inv, part);
