@@ -156,15 +156,6 @@ __device__ __forceinline__ float activated(float z, int act) {
   if (act == kActRelu) return z < 0.0f ? 0.0f : z;
   return act == kActSilu ? act_silu(z) : act_gelu(z);
 }
-__device__ __forceinline__ void activate(float (&v)[8], int act) {
-  auto each = [&](auto f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f(v[i]);
-  };
-  if (act == kActGelu) each([](float z) { return act_gelu(z); });
-  else if (act == kActSilu) each([](float z) { return act_silu(z); });
-  else if (act == kActRelu) each([](float z) { return z < 0.0f ? 0.0f : z; });
-}
 template <int N>
 __device__ __forceinline__ void activate(f32x4_t (&v)[N][4], int act) {
   auto each = [&](auto f) __attribute__((always_inline)) {
