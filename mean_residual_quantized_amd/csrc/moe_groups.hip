@@ -378,8 +378,8 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
     if (__builtin_expect(__ballot(open) != 0, 0)) {
       // the groups' exact scores, of the two largest keys each
       all = open && !by_logit && a.score == kScoreSoftmax;
-      uint32_t ref = 0u;   // the key of the last that counts
-      int e1 = -1, e2 = -1;
+      uint32_t ref = 0u;               // the key of the last that counts
+      int e1 = -1, e2 = -1, own = -1;   // own: the one whose value counts last
       if (g < a.groups) {
         uint32_t k1 = 0u, k2 = 0u;
         for (int i = 0; i < a.group_lanes; ++i) {
@@ -400,9 +400,11 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
         double x = exact(e1);
         const double y = exact(e2);
         if (a.group_top == 2) {
+          own = x < y ? e1 : e2;
           if (e2 >= 0) x += y;
           ref = k2;
         } else {
+          own = x < y ? e2 : e1;
           x = y > x ? y : x;
           ref = k1;
         }
@@ -410,12 +412,13 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
         sh.score[tok][g] = x;
       }
       // Whether another of the group's may be above that one: every key is looked at, for before one a
-      // little larger there can be any number of equal ones, whose indexes are lower
+      // little larger there can be any number of equal ones, whose indexes are lower.  One that is the same
+      // as `own` is not
       const int from = (lane & ~(G - 1)) + group;
       ref = (uint32_t)__shfl((int)ref, from, 64);
       e1 = __shfl(e1, from, 64);
       e2 = __shfl(e2, from, 64);
-      const int own = a.group_top == 2 ? e2 : e1;
+      own = __shfl(own, from, 64);
       if (open && near(ref, s[0])) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {

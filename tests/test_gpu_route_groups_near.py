@@ -49,6 +49,21 @@ def test_a_larger_score_behind_equal_ones(dtype):
             check_alone(l, 3, score=score, groups=2, topk_groups=1, group_top=1)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_smaller_score_before_equal_ones(dtype):
+    """The first of a group is smaller than those behind it by less than fp32 tells: it is none of the two that count."""
+    l = torch.full((1, 10), 18.0)
+    l[0, 0] = 17.875
+    check_alone(l.to(dtype), 3, groups=2, topk_groups=1)
+    check_alone(l.to(dtype), 3, np.full(10, 0.25, np.float32), groups=2, topk_groups=1)
+    check_alone(l.to(dtype), 3, np.full(10, 0.25, np.float32), groups=2, topk_groups=1, group_top=1)
+    wide = torch.full((1, 32), -float("inf"))               # a group on several lanes
+    wide[0, [0, 9, 10, 15, 17, 31]] = 18.0
+    wide[0, 0] = 17.875
+    for many in (1, 3):
+        check_alone(wide.to(dtype).repeat(1, many), 2, groups=2 * many, topk_groups=many)
+
+
 NEAR = [(8, 3, 2, 1), (64, 8, 8, 4), (160, 6, 8, 3), (600, 8, 4, 2), (1000, 12, 8, 2)]
 
 
