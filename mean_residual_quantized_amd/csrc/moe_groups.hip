@@ -420,10 +420,19 @@ __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logi
       e2 = __shfl(e2, from, 64);
       own = __shfl(own, from, 64);
       if (open && near(ref, s[0])) {
+        uint32_t places = 0u;
+#pragma unroll
+        for (int v = 0; v < V; ++v) places |= (near(ref, s[v]) ? 1u : 0u) << (kPlace - (s[v] & kPlace));
+        // (in the experts' order, whole pieces a load: 65521 x 256 equal logits in 8 groups 70 us in fp32, 61
+        // in bf16; key by key 155 and 149)
+        float l[V], bias[V];
+        load_run<T, V>(row, at0.first, at0.many, l);
+        if (a.bias) load_run<float, V>(a.bias, at0.first, at0.many, bias);
+        const float its = Elem<T>::f32(row[own]), its_bias = bias_of(own);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const int e = at0.first + (int)(kPlace - (s[v] & kPlace));
-          if (near(ref, s[v]) && e != e1 && e != e2) all |= !same(own, e);
+          const int e = at0.first + v;
+          if ((places >> v & 1u) && e != e1 && e != e2) all |= !(l[v] == its && (!a.bias || bias[v] == its_bias));
         }
       }
       lds_order();
