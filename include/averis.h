@@ -511,10 +511,12 @@ typedef enum { AVERIS_SCORE_SOFTMAX = 0, AVERIS_SCORE_SIGMOID = 1 } averis_score
  *   weights[t][j] = scale s_e, divided by the sum of the chosen s_e with renorm = 1.
  * The choice is by the values of c_e in fp64 (without a bias, and with
  * group_top = 1 or all groups, of l_e, which order alike), equal ones by the
- * lowest index first.  A logit of -inf, or c_e = -inf, is closed: never chosen, and a
+ * lowest index first (sums of two different pairs that only fp64's own rounding
+ * tells apart may go either way).  A logit of -inf, or c_e = -inf, is closed: never chosen, and a
  * slot for which none is left gets id -1 and weight 0; a group without an open
- * expert does not stay.  A NaN logit counts as the largest and makes its weight NaN
- * (with renorm or softmax scores all of the token's; so does +inf with softmax).
+ * expert does not stay.  A NaN value counts as the largest.  A NaN logit makes its
+ * weight NaN (with renorm or softmax scores all of the token's; so does +inf with
+ * softmax: where the choice is by c_e, the lowest open indexes are then taken).
  * Other arguments as for averis_moe_route; topk <= topk_groups experts / groups. */
 averis_status_t averis_moe_route_groups(const void* logits, averis_dtype_t dtype, int64_t tokens,
                                         int experts, int64_t ld, int topk, const float* bias,

@@ -230,11 +230,12 @@ __device__ __forceinline__ float sigmoid_over(float x, float most) {
 // G lanes share a token, V experts each of one group's (lanes and places order as
 // the experts do).  Each lane sorts its keys once; a round then compares the
 // lanes' first keys alone, and the lane that has the largest moves on to its
-// next.  Bound by vector instructions, most of them the scores' and keys' (about
-// ten and two slow ones an expert), the sort's (eight an expert) and the rounds'
-// (about 40): 65521 tokens of 256 experts in 8 groups, top 8, fp32 33 us (67 MB,
-// 2.0 TB/s; 69 with eight experts a lane and every near choice made again whole),
-// 10007 of 160 in 8 groups bf16 8.3 us, 16 of 64 4.8 us (latency).
+// next.  Bound by vector instructions (their pipes are busy for 30 of the first
+// case's 36 us; 68 lane-instructions an expert), most of them the scores' and keys'
+// (about ten and two slow ones an expert), the sort's (eight an expert) and the
+// rounds' (about 40): 65521 tokens of 256 experts in 8 groups, top 8, fp32 36 us
+// (67 MB, 1.9 TB/s; 69 with eight experts a lane and every near choice made again
+// whole), 10007 of 160 in 8 groups bf16 8.4 us, 16 of 64 5.0 us (latency).
 template <typename T, int G, int V>
 __global__ __launch_bounds__(256) void k_route_groups(const T* __restrict__ logits, RouteGroups a) {
   __shared__ RouteShare<G, V> sh;
