@@ -722,8 +722,8 @@ averis_status_t averis_rmsnorm_grad(const void* dy, averis_dtype_t dtype, int64_
                                     float* dweight, void* ws, size_t ws_bytes,
                                     hipStream_t stream);
 
-/* dz = dy act'(z) (rows x cols; fp32, relu's slope at 0 is 0, the smooth ones'
- * at +-inf 1 and 0): rounded to the type of dy and z and quantized into out and
+/* dz = dy act'(z) (rows x cols; fp32, relu's slope at 0 is 0, and where it is 0 dz
+ * is +0 whatever dy is; the smooth ones' at +-inf 1 and 0): rounded to the type of dy and z and quantized into out and
  * out_t as averis_fp8_quant does, segments included, from one read; dbias[s][j]
  * = sum of dz (before it is rounded) over segment s's rows, nseg x cols floats
  * in a fixed order, zeros for a segment without any.  Each of the three may be
