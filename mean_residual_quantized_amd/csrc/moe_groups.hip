@@ -7,8 +7,9 @@
 //
 // The choice is by c_e in fp64 (equal ones: the lowest index first).  It is
 // made from fp32 scores, their lowest bits given to the expert's place, and
-// where two of those lie closer than their errors allow to tell, and are not of
-// the same logit and bias, the wavefront's tokens are chosen again in fp64.
+// where some of those lie closer than their errors allow to tell, and are not of
+// the same logit and bias, the few are ranked by their fp64 values, or, where that
+// does not settle it, the wavefront's tokens chosen again in fp64.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
